@@ -33,6 +33,26 @@ class Config(ctypes.Structure):
                 ("theta_global", ctypes.c_double), ("theta_local", ctypes.c_double)]
 
 
+class Scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class RotarySpec(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int), ("layout", ctypes.c_int), ("amplitude", ctypes.c_double),
+                ("freq", ctypes.c_double * 128)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("src", _vp), ("dst", _vp), ("weight", _vp), ("heads", ctypes.c_int),
+                ("src_row", _c_i64), ("src_head", _c_i64), ("dst_row", _c_i64), ("dst_head", _c_i64)]
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "yarn": 4}
+_NORMS = {"rms": 1, "layer": 2}
+
 SIGNATURES = {
     "mbert_attn_default_config": (_c_int, [ctypes.POINTER(Config)]),
     "mbert_attn_create": (_c_int, [ctypes.POINTER(_vp), ctypes.POINTER(Config), _c_int]),
@@ -43,6 +63,13 @@ SIGNATURES = {
     "mbert_attn_out_proj": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _vp, _vp]),
     "mbert_attn_ln_qkv": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, ctypes.c_float, _vp, _vp]),
     "mbert_attn_mlp": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_i64, ctypes.c_float, _vp, _vp]),
+    "mbert_attn_rotary_init": (_c_int, [ctypes.POINTER(RotarySpec), _c_int, _c_int, ctypes.c_double,
+                                        ctypes.POINTER(Scaling)]),
+    "mbert_attn_rotary": (_c_int, [_vp, ctypes.POINTER(Heads), _c_i64, _c_int, _c_int,
+                                   ctypes.POINTER(RotarySpec), _vp, _c_int, _vp, _c_int, _c_int, _vp]),
+    "mbert_attn_qk_norm_rotary": (_c_int, [_vp, ctypes.POINTER(Heads), ctypes.POINTER(Heads), _c_i64,
+                                           _c_int, _c_int, _c_int, ctypes.c_float,
+                                           ctypes.POINTER(RotarySpec), _vp, _c_int, _vp, _c_int, _vp]),
     "mbert_attn_get_error": (_c_int, [_vp]),
     "mbert_attn_selftest_timeout": (_c_int, [_vp, _c_i64, _vp]),
     "mbert_attn_forward_noalloc": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_int, _c_int, _vp, _vp,
@@ -106,6 +133,64 @@ def _kind(layer_kind) -> int:
 
 def _stream_ptr(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+class Rotary:
+    """How a head is rotated: its first `dim` numbers (even, up to 256) in
+    pairs, `layout` "half" (x[m], x[m + dim/2]) or "interleaved" (x[2m],
+    x[2m+1]), pair m by position * base^(-2m/dim).  `scaling` stretches the
+    frequencies for contexts longer than the trained one, a dict with "kind":
+
+      "linear"    factor: f / factor
+      "ntk"       factor: base * factor^(dim/(dim-2))
+      "by_parts"  factor, original, low=1, high=32: with r = original f / 2 pi
+                  turns over the original context, f where r >= high, f/factor
+                  where r <= low, linear in r between
+      "yarn"      factor, original, low=1, high=32, amplitude=None: the same
+                  borders as rounded pair numbers and a ramp over the pair
+                  numbers between; rows times 0.1 ln(factor) + 1 unless given
+
+    Host data only: made once, usable on every device."""
+
+    def __init__(self, dim: int, base: float = 10000.0, layout: str = "half", scaling: dict = None):
+        if layout not in _LAYOUTS:
+            raise ValueError(f"layout must be 'half' or 'interleaved', not {layout!r}")
+        sc = None
+        if scaling is not None:
+            given = dict(scaling)
+            kind = given.pop("kind", None)
+            if kind not in _SCALINGS:
+                raise ValueError(f"scaling kind must be one of {sorted(_SCALINGS)}, not {kind!r}")
+            takes = {"none": (), "linear": ("factor",), "ntk": ("factor",),
+                     "by_parts": ("factor", "original", "low", "high"),
+                     "yarn": ("factor", "original", "low", "high", "amplitude")}[kind]
+            extra = sorted(set(given) - set(takes))
+            missing = sorted(({"factor", "original"} & set(takes)) - set(given))
+            if extra or missing:
+                raise ValueError(f"scaling {kind!r}: unknown {extra}, missing {missing}")
+            amplitude = given.get("amplitude")
+            if amplitude is not None and not amplitude > 0:
+                raise ValueError("scaling amplitude must be positive")
+            sc = Scaling(_SCALINGS[kind], float(given.get("factor", 1.0)),
+                         float(given.get("original", 1.0)), float(given.get("low", 1.0)),
+                         float(given.get("high", 32.0)), float(amplitude or 0.0))
+        self.spec = RotarySpec()
+        _check(load_library().mbert_attn_rotary_init(
+            ctypes.byref(self.spec), int(dim), _LAYOUTS[layout], float(base),
+            None if sc is None else ctypes.byref(sc)), "rotary_init")
+
+    @property
+    def dim(self) -> int:
+        return self.spec.dim
+
+    @property
+    def frequencies(self):
+        """Radians per position of each pair."""
+        return list(self.spec.freq[:self.spec.dim // 2])
+
+    @property
+    def amplitude(self) -> float:
+        return self.spec.amplitude
 
 
 class Attention:
@@ -273,6 +358,99 @@ class Attention:
         _check(st, "mlp")
         return out
 
+    def _check_heads(self, t, name, like=None):
+        """A [T, H, D] tensor on this device whose last dimension is contiguous."""
+        if t.dim() != 3 or t.dtype not in _DTYPES or t.device != self.device:
+            raise TypeError(f"{name} must be a bf16, fp16 or fp32 [T, heads, head_dim] tensor on {self.device}")
+        if t.shape[2] > 1 and t.stride(2) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+        if like is not None and (t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]
+                                 or t.dtype != like.dtype):
+            raise TypeError(f"{name} must have the rows, head size and type of the other tensor")
+
+    def _heads(self, src, dst, name, weight=None):
+        if dst is None:
+            dst = torch.empty(src.shape, dtype=src.dtype, device=self.device)
+        else:
+            self._check_heads(dst, name, src)
+            if dst.shape != src.shape:
+                raise TypeError(f"{name} must have the shape {list(src.shape)}")
+        T, H, D = src.shape
+        # a dimension of one element has no stride that matters
+        strides = [(x.stride(0) if T > 1 else H * D, x.stride(1) if H > 1 else D) for x in (src, dst)]
+        return dst, Heads(src.data_ptr(), dst.data_ptr(), None if weight is None else weight.data_ptr(),
+                          H, *strides[0], *strides[1])
+
+    def _positions(self, positions, cu_seqlens, tokens):
+        """-> (positions pointer, bits, cu_seqlens pointer, sequences)"""
+        if (positions is None) == (cu_seqlens is None):
+            raise ValueError("give either positions or cu_seqlens")
+        if positions is None:
+            self._check_cu(cu_seqlens)
+            return None, 0, cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
+        if (positions.dtype not in (torch.int32, torch.int64) or tuple(positions.shape) != (tokens,)
+                or positions.device != self.device or not positions.is_contiguous()):
+            raise TypeError(f"positions must be a contiguous int32 or int64 [{tokens}] tensor on {self.device}")
+        return positions.data_ptr(), 8 * positions.element_size(), None, 0
+
+    def rotary(self, x: torch.Tensor, rope: Rotary, positions: torch.Tensor = None,
+               cu_seqlens: torch.Tensor = None, inverse: bool = False,
+               out: torch.Tensor = None) -> torch.Tensor:
+        """out[T, H, D] = x with every head turned by its row's position (bf16,
+        fp16 or fp32, fp32 arithmetic).  Positions: int32 or int64 [T], or from
+        cu_seqlens (int32 [n+1]; a row's place in its sequence; rows behind the
+        last sequence are left as they were).  x may be strided (a view of fused
+        rows); out may be x.  inverse=True turns the other way (the transpose:
+        the gradient of a turned tensor goes back through it)."""
+        self._check_heads(x, "x")
+        pos = self._positions(positions, cu_seqlens, x.shape[0])
+        out, heads = self._heads(x, out, "out")
+        st = load_library().mbert_attn_rotary(
+            self._h, ctypes.byref(heads), x.shape[0], x.shape[2], _DTYPES[x.dtype],
+            ctypes.byref(rope.spec), *pos, 1 if inverse else 0, _stream_ptr(self.device))
+        _check(st, "rotary")
+        return out
+
+    def qk_norm_rotary(self, q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
+                       k_weight: torch.Tensor, rope: Rotary = None, positions: torch.Tensor = None,
+                       cu_seqlens: torch.Tensor = None, norm: str = "rms", eps: float = 1e-6,
+                       q_out: torch.Tensor = None, k_out: torch.Tensor = None):
+        """(q_out, k_out) = every query and key head normed over its D numbers
+        ("rms" or bias-free "layer", weight [D]) and then turned, in one kernel.
+        q [T, Hq, D] and k [T, Hk, D] share rows and type; either may be None.
+        rope None: the norm alone.  Positions, strides and in-place use as in
+        rotary."""
+        if norm not in _NORMS:
+            raise ValueError(f"norm must be 'rms' or 'layer', not {norm!r}")
+        first = q if q is not None else k
+        if first is None:
+            raise ValueError("give q, k or both")
+        structs, outs = [], []
+        for t, w, o, name in ((q, q_weight, q_out, "q"), (k, k_weight, k_out, "k")):
+            if t is None:
+                structs.append(None)
+                outs.append(None)
+                continue
+            self._check_heads(t, name, first)
+            if (w is None or w.dtype != t.dtype or tuple(w.shape) != (t.shape[2],)
+                    or w.device != self.device or not w.is_contiguous()):
+                raise TypeError(f"{name}_weight must be a contiguous [{t.shape[2]}] tensor of {name}'s type")
+            o, h = self._heads(t, o, f"{name}_out", w)
+            structs.append(ctypes.byref(h))
+            outs.append(o)
+        if rope is None or rope.dim == 0:
+            if positions is not None or cu_seqlens is not None:
+                raise ValueError("positions or cu_seqlens without a rotation")
+            pos = (None, 0, None, 0)
+        else:
+            pos = self._positions(positions, cu_seqlens, first.shape[0])
+        st = load_library().mbert_attn_qk_norm_rotary(
+            self._h, structs[0], structs[1], first.shape[0], first.shape[2], _DTYPES[first.dtype],
+            _NORMS[norm], float(eps), None if rope is None else ctypes.byref(rope.spec), *pos,
+            _stream_ptr(self.device))
+        _check(st, "qk_norm_rotary")
+        return tuple(outs)
+
     def key_counts(self, cu_seqlens: torch.Tensor, total_tokens: int, layer_kind,
                    max_seqlen: int = 0) -> torch.Tensor:
         """int32 [T]: keys the kernels' schedule and mask admit per query row."""
@@ -371,3 +549,27 @@ def key_counts(cu_seqlens: torch.Tensor, total_tokens: int, layer_kind) -> torch
     if not cu_seqlens.is_cuda:
         raise ValueError("cu_seqlens must be a CUDA tensor")
     return _default(cu_seqlens.device).key_counts(cu_seqlens, total_tokens, layer_kind)
+
+
+def rotary(x: torch.Tensor, rope: Rotary, positions: torch.Tensor = None, cu_seqlens: torch.Tensor = None,
+           inverse: bool = False, out: torch.Tensor = None) -> torch.Tensor:
+    """Rotary positions on x [T, H, D] (CUDA; bf16, fp16 or fp32), positions
+    given or from cu_seqlens: Attention.rotary on the device's handle."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    return _default(x.device).rotary(x, rope, positions, cu_seqlens, inverse, out)
+
+
+def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                   rope: Rotary = None, positions: torch.Tensor = None, cu_seqlens: torch.Tensor = None,
+                   norm: str = "rms", eps: float = 1e-6, q_out: torch.Tensor = None,
+                   k_out: torch.Tensor = None):
+    """Norm of every query and key head and its rotation in one kernel:
+    Attention.qk_norm_rotary on the device's handle."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("give q, k or both")
+    if not first.is_cuda:
+        raise ValueError("q and k must be CUDA tensors")
+    return _default(first.device).qk_norm_rotary(q, k, q_weight, k_weight, rope, positions, cu_seqlens,
+                                                 norm, eps, q_out, k_out)

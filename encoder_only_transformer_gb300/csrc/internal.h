@@ -238,6 +238,40 @@ cudaError_t launch_scatter_rows(const __nv_bfloat16 *src, const int32_t *rank, c
                                 int B, int S, int width, __nv_bfloat16 *dst, int num_sms,
                                 cudaStream_t stream);
 
+// Rotary positions on rows of heads, alone or after a norm of every head
+// (rotary.cu): up to two tensors (queries and keys) of the same rows.
+struct RotaryRows {
+    const void *src = nullptr;
+    void *dst = nullptr;             // may be src
+    const void *weight = nullptr;    // [dim], with a norm
+    int heads = 0;                   // 0: no such tensor
+    long long src_row = 0, src_head = 0, dst_row = 0, dst_head = 0;   // strides in elements
+};
+
+constexpr int kMaxRotaryPairs = 128;
+
+struct RotaryArgs {
+    RotaryRows x[2];
+    int dtype = 0;                   // MBERT_BF16, MBERT_F16 or MBERT_F32
+    int dim = 0, rot = 0;            // head size, turned part (both even)
+    int interleaved = 0;
+    int norm = 0;                    // MBERT_NORM_*
+    float eps = 0.f;
+    float amplitude = 1.f, sin_amplitude = 1.f;   // sin_amplitude < 0: the inverse rotation
+    long long tokens = 0;
+    // positions: 32 or 64 bits per row, or from cu_seqlens; none for rot = 0
+    const int32_t *pos32 = nullptr;
+    const int64_t *pos64 = nullptr;
+    const int32_t *cu = nullptr;
+    int n_seqs = 0;
+    int32_t *err = nullptr;
+    // set by the launcher: lanes of a head, rows of a warp, warps of a row group
+    int lanes_log2 = 0, rows_per_warp = 1, parts = 1;
+    uint64_t turns[kMaxRotaryPairs] = {};   // turns per position, 64-bit binary fractions
+};
+
+cudaError_t launch_rotary(RotaryArgs &a, int num_sms, cudaStream_t stream);
+
 // Number of sequences up to which the local kernel finds its blocks itself
 // (above it the plan kernel writes a work list first).
 constexpr int kLocalSelfScheduleMaxSeqs = 256;

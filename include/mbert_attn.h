@@ -216,6 +216,112 @@ int mbert_attn_mlp(mbert_attn *h, const void *x, const void *norm_w, const void 
 int mbert_attn_out_proj(mbert_attn *h, const void *a, const void *wo, const void *x,
                         int64_t total_tokens, void *y, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Beside the block: rotary positions and per-head norms on any rows of heads,
+ * and attention over keys and values of another length.  For callers whose
+ * heads are turned or normed in another way than ModernBERT-base's, and for
+ * decoders and pooling heads that read the encoder's states.  These calls
+ * keep nothing in the handle but the error word, so calls on different
+ * streams may overlap on the GPU.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the calls below. */
+enum {
+    MBERT_BF16 = 0,
+    MBERT_F16 = 1,
+    MBERT_F32 = 2     /* rotary and qk_norm_rotary only */
+};
+
+/* Which numbers of a head form pair m (of the first dim numbers). */
+enum {
+    MBERT_ROTARY_HALF = 0,          /* x[m], x[m + dim/2] */
+    MBERT_ROTARY_INTERLEAVED = 1    /* x[2m], x[2m + 1] */
+};
+
+/* How the frequencies are scaled for contexts longer than the trained one. */
+enum {
+    MBERT_SCALING_NONE = 0,
+    MBERT_SCALING_LINEAR = 1,    /* f / factor */
+    MBERT_SCALING_NTK = 2,       /* base * factor^(dim / (dim - 2)); dim > 2 */
+    MBERT_SCALING_BY_PARTS = 3,  /* by the turns r = original f / (2 pi) over the original
+                                  * context: f where r >= high, f / factor where r <= low,
+                                  * linear in r between */
+    MBERT_SCALING_YARN = 4       /* the same two borders as pair numbers,
+                                  * dim ln(original / (2 pi turns)) / (2 ln base), rounded
+                                  * down (high) and up (low), kept within 0 .. dim - 1, and a
+                                  * ramp linear in the pair number between them; amplitude
+                                  * 0.1 ln(factor) + 1 unless given */
+};
+
+typedef struct {
+    int kind;           /* MBERT_SCALING_* */
+    double factor;      /* > 0; >= 1 for NTK, BY_PARTS and YARN */
+    double original;    /* trained context length (BY_PARTS, YARN), > 0 */
+    double low, high;   /* borders in turns (BY_PARTS, YARN), 0 < low < high */
+    double amplitude;   /* YARN: > 0, or 0 for 0.1 ln(factor) + 1 */
+} mbert_attn_scaling;
+
+/* The rotation of a head: its first `dim` numbers, pair m by
+ * position * freq[m] radians, both results times `amplitude`. */
+typedef struct {
+    int dim;            /* even, 0 .. 256 (0: no rotation) */
+    int layout;         /* MBERT_ROTARY_* */
+    double amplitude;
+    double freq[128];   /* dim / 2 of them, radians per position, finite, >= 0 */
+} mbert_attn_rotary_spec;
+
+/* Fill *spec: freq[m] = base^(-2m/dim), scaled (scaling == NULL: not at all).
+ * Host only.  base > 1, or MBERT_ERR_BAD_ARG. */
+int mbert_attn_rotary_init(mbert_attn_rotary_spec *spec, int dim, int layout, double base,
+                           const mbert_attn_scaling *scaling);
+
+/* One tensor of heads: element (t, h, d) at t * row + h * head + d, strides in
+ * elements.  src strides may be 0 (broadcast); the elements of dst must be
+ * distinct.  dst may be src itself with the same strides (in place); else the
+ * two must not overlap (interleaved column blocks of the same rows may). */
+typedef struct {
+    const void *src;
+    void *dst;
+    const void *weight;             /* [head_dim], same type: the norm's weight */
+    int heads;
+    int64_t src_row, src_head, dst_row, dst_head;
+} mbert_attn_heads;
+
+/* Rotary positions: dst(t, h) = src(t, h) turned by the position of row t.
+ *   tokens         rows, 0 <= tokens < 2^31 (0 enqueues nothing).
+ *   head_dim       even, 2 .. 256, >= rope->dim; numbers past rope->dim are copied.
+ *   dtype          MBERT_BF16, MBERT_F16 or MBERT_F32; fp32 arithmetic, one rounding.
+ *   positions      device, int32 or int64 [tokens] (position_bits 32 or 64), any value; or
+ *                  NULL, and then
+ *   cu_seqlens     device int32 [n_seqs + 1], cu[0] = 0, non-decreasing, cu[n] <= tokens: a
+ *                  row's position is its place in its sequence; rows from cu[n] on are left
+ *                  as they were.  A bad cu_seqlens sets MBERT_ERR_BAD_CU_SEQLENS for
+ *                  mbert_attn_get_error(), and the results are then unspecified.
+ *   inverse        non-zero: by the negative angle (with the same amplitude: the transpose,
+ *                  which also is the gradient with respect to src).
+ * Any alignment of the element size; 16-byte aligned addresses, strides and parts (head_dim and
+ * rope->dim multiples of 16, of 8 for fp32) are read in 16-byte vectors.  One kernel. */
+int mbert_attn_rotary(mbert_attn *h, const mbert_attn_heads *x, int64_t tokens, int head_dim,
+                      int dtype, const mbert_attn_rotary_spec *rope, const void *positions,
+                      int position_bits, const int32_t *cu_seqlens, int n_seqs, int inverse,
+                      void *stream);
+
+/* Norms of one head's numbers. */
+enum {
+    MBERT_NORM_RMS = 1,     /* x / sqrt(mean(x^2) + eps) * weight */
+    MBERT_NORM_LAYER = 2    /* (x - mean) / sqrt(population variance + eps) * weight */
+};
+
+/* Norm of every query and key head, then the rotation, in one pass and one
+ * kernel.  q and k share the rows; either may be NULL (the other is then done
+ * alone).  rope == NULL (or rope->dim == 0): the norm alone, without
+ * positions.  0 <= eps <= 1; statistics in fp32.  Else as mbert_attn_rotary. */
+int mbert_attn_qk_norm_rotary(mbert_attn *h, const mbert_attn_heads *q, const mbert_attn_heads *k,
+                              int64_t tokens, int head_dim, int dtype, int norm, float eps,
+                              const mbert_attn_rotary_spec *rope, const void *positions,
+                              int position_bits, const int32_t *cu_seqlens, int n_seqs,
+                              void *stream);
+
 /* Wait for the handle's most recent stream, then return (and clear) the
  * device error word as a status: MBERT_OK, MBERT_ERR_BAD_CU_SEQLENS,
  * MBERT_ERR_SEQ_TOO_LONG or MBERT_ERR_TIMEOUT; MBERT_ERR_CUDA if the wait
