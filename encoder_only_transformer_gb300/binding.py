@@ -48,6 +48,15 @@ class Heads(ctypes.Structure):
                 ("src_row", _c_i64), ("src_head", _c_i64), ("dst_row", _c_i64), ("dst_head", _c_i64)]
 
 
+class CrossArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("out", _vp),
+                ("q_row", _c_i64), ("k_row", _c_i64), ("v_row", _c_i64), ("out_row", _c_i64),
+                ("rows_q", _c_i64), ("rows_k", _c_i64),
+                ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("n_seqs", ctypes.c_int),
+                ("cu_q", _vp), ("cu_k", _vp), ("max_seqlen_q", ctypes.c_int), ("key_mask", _vp)]
+
+
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "yarn": 4}
@@ -70,6 +79,8 @@ SIGNATURES = {
     "mbert_attn_qk_norm_rotary": (_c_int, [_vp, ctypes.POINTER(Heads), ctypes.POINTER(Heads), _c_i64,
                                            _c_int, _c_int, _c_int, ctypes.c_float,
                                            ctypes.POINTER(RotarySpec), _vp, _c_int, _vp, _c_int, _vp]),
+    "mbert_attn_cross_workspace": (_c_int, [_vp, ctypes.POINTER(CrossArgs), ctypes.POINTER(_c_i64)]),
+    "mbert_attn_cross": (_c_int, [_vp, ctypes.POINTER(CrossArgs), _vp, _c_i64, _vp]),
     "mbert_attn_get_error": (_c_int, [_vp]),
     "mbert_attn_selftest_timeout": (_c_int, [_vp, _c_i64, _vp]),
     "mbert_attn_forward_noalloc": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_int, _c_int, _vp, _vp,
@@ -451,6 +462,101 @@ class Attention:
         _check(st, "qk_norm_rotary")
         return tuple(outs)
 
+    def _check_cross(self, t, name, dims):
+        """A [..., heads, head_dim] tensor whose heads lie side by side."""
+        if (t.dim() != dims or t.dtype not in (torch.bfloat16, torch.float16) or t.device != self.device
+                or t.shape[-1] not in (64, 128) or t.shape[-2] < 1):
+            raise TypeError(f"{name} must be a bf16 or fp16 tensor of {dims} dimensions "
+                            f"[..., heads, 64 or 128] on {self.device}")
+        if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]):
+            raise ValueError(f"the heads of {name} must lie side by side in each row")
+
+    def _cross(self, q, k, v, out, rows_q, rows_k, pitches, n_seqs, cu_q, cu_k, max_seqlen_q, key_mask, scale):
+        if scale is None:
+            scale = 0.0
+        elif not 0.0 < scale < float("inf"):
+            raise ValueError("scale must be positive and finite")
+        args = CrossArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *pitches, rows_q, rows_k,
+                         q.shape[-2], k.shape[-2], q.shape[-1], _DTYPES[q.dtype], scale, n_seqs, cu_q, cu_k,
+                         int(max_seqlen_q), None if key_mask is None else key_mask.data_ptr())
+        lib = load_library()
+        need = _c_i64()
+        _check(lib.mbert_attn_cross_workspace(self._h, ctypes.byref(args), ctypes.byref(need)), "cross_attention")
+        # of the call's own, from torch's allocator: calls on other streams and
+        # captured ones never share it
+        ws = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+        st = lib.mbert_attn_cross(self._h, ctypes.byref(args), ws.data_ptr(), need.value,
+                                  _stream_ptr(self.device))
+        _check(st, "cross_attention")
+        return out
+
+    def cross_attention(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, max_seqlen_q: int = 0,
+                        key_mask: torch.Tensor = None, scale: float = None,
+                        out: torch.Tensor = None) -> torch.Tensor:
+        """out[Tq, Hq, D] = attention of packed queries over keys and values of
+        another length: q [Tq, Hq, D], k and v [Tk, Hk, D] (bf16 or fp16, D 64 or
+        128, Hq a multiple of Hk), sequence s the rows cu_seqlens_q[s] ..
+        cu_seqlens_q[s+1] over cu_seqlens_k[s] .. cu_seqlens_k[s+1] (int32 [n+1]).
+        No rotation and no causal mask; key_mask (int32 [Tk], non-zero = visible)
+        hides keys; a row without a visible key is 0; rows of out behind the
+        last sequence are left as they were.  max_seqlen_q is the caller's bound
+        on the longest query sequence: give it for single tokens (at most
+        16 / (Hq / Hk) rows a sequence), which then read k and v once.  scale
+        None: 1 / sqrt(D).  Rows may be strided (views of fused rows)."""
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            self._check_cross(t, name, 3)
+        if k.shape != v.shape or k.shape[2] != q.shape[2] or not q.dtype == k.dtype == v.dtype:
+            raise TypeError("q, k and v must agree in type and head size, k and v in shape")
+        self._check_cu(cu_seqlens_q)
+        self._check_cu(cu_seqlens_k)
+        if cu_seqlens_q.numel() != cu_seqlens_k.numel() or cu_seqlens_q.numel() < 1:
+            raise ValueError("cu_seqlens_q and cu_seqlens_k must name the same number of sequences")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        else:
+            self._check_cross(out, "out", 3)
+            if out.shape != q.shape or out.dtype != q.dtype:
+                raise TypeError(f"out must be a {q.dtype} tensor of shape {list(q.shape)}")
+        if key_mask is not None and (key_mask.dtype != torch.int32 or tuple(key_mask.shape) != (k.shape[0],)
+                                     or key_mask.device != self.device or not key_mask.is_contiguous()):
+            raise TypeError(f"key_mask must be a contiguous int32 [{k.shape[0]}] tensor on {self.device}")
+        # one row has no pitch that matters
+        pitches = [t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2] for t in (q, k, v, out)]
+        return self._cross(q, k, v, out, q.shape[0], k.shape[0], pitches, cu_seqlens_q.numel() - 1,
+                           cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), max_seqlen_q, key_mask, scale)
+
+    def cross_attention_padded(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                               key_mask: torch.Tensor = None, scale: float = None,
+                               out: torch.Tensor = None) -> torch.Tensor:
+        """The padded form: q [B, Sq, Hq, D] over k and v [B, Sk, Hk, D] with
+        key_mask int32 [B, Sk] (1 = real token, 0 = pad; None: all real) ->
+        out [B, Sq, Hq, D].  Every query row is computed; one whose keys are all
+        pads is 0.  Rows may be strided, with the batch rows one pitch apart
+        (views of fused rows).  Else as cross_attention."""
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            self._check_cross(t, name, 4)
+        if (k.shape != v.shape or k.shape[3] != q.shape[3] or k.shape[0] != q.shape[0]
+                or not q.dtype == k.dtype == v.dtype):
+            raise TypeError("q, k and v must agree in type, batch and head size, k and v in shape")
+        B, Sq, Sk = q.shape[0], q.shape[1], k.shape[1]
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        else:
+            self._check_cross(out, "out", 4)
+            if out.shape != q.shape or out.dtype != q.dtype:
+                raise TypeError(f"out must be a {q.dtype} tensor of shape {list(q.shape)}")
+        if key_mask is not None and (key_mask.dtype != torch.int32 or tuple(key_mask.shape) != (B, Sk)
+                                     or key_mask.device != self.device or not key_mask.is_contiguous()):
+            raise TypeError(f"key_mask must be a contiguous int32 [{B}, {Sk}] tensor on {self.device}")
+        pitches = []
+        for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+            pitch = t.stride(1) if t.shape[1] > 1 else t.stride(0) if B > 1 else t.shape[2] * t.shape[3]
+            if B > 1 and t.shape[1] > 0 and t.stride(0) != t.shape[1] * pitch:
+                raise ValueError(f"the rows of {name} must be one pitch apart throughout the batch")
+            pitches.append(pitch)
+        return self._cross(q, k, v, out, B * Sq, B * Sk, pitches, B, None, None, 0, key_mask, scale)
+
     def key_counts(self, cu_seqlens: torch.Tensor, total_tokens: int, layer_kind,
                    max_seqlen: int = 0) -> torch.Tensor:
         """int32 [T]: keys the kernels' schedule and mask admit per query row."""
@@ -573,3 +679,23 @@ def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_w
         raise ValueError("q and k must be CUDA tensors")
     return _default(first.device).qk_norm_rotary(q, k, q_weight, k_weight, rope, positions, cu_seqlens,
                                                  norm, eps, q_out, k_out)
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                    cu_seqlens_k: torch.Tensor, max_seqlen_q: int = 0, key_mask: torch.Tensor = None,
+                    scale: float = None, out: torch.Tensor = None) -> torch.Tensor:
+    """Attention of packed queries over keys and values of another length
+    (CUDA, bf16 or fp16): Attention.cross_attention on the device's handle."""
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    return _default(q.device).cross_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, key_mask,
+                                              scale, out)
+
+
+def cross_attention_padded(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_mask: torch.Tensor = None,
+                           scale: float = None, out: torch.Tensor = None) -> torch.Tensor:
+    """The padded form, q [B, Sq, Hq, D] over k and v [B, Sk, Hk, D] with a mask
+    [B, Sk]: Attention.cross_attention_padded on the device's handle."""
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    return _default(q.device).cross_attention_padded(q, k, v, key_mask, scale, out)

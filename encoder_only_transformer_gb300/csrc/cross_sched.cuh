@@ -1,0 +1,249 @@
+// The split of cross attention among CTAs, shared by its kernels.
+//
+// A unit is one (sequence, head, block of query rows); it takes tiles(s) key
+// tiles.  All units stand one after the other on a line of costs, in order of
+// sequence, head, block: a unit takes tiles + kAlpha of it (kAlpha for its
+// fixed work: the query load, the end of its softmax, its output).  CTA c of n
+// owns the tiles whose place lies in [c X / n, (c + 1) X / n), X the line's
+// length; so every CTA gets the same cost whatever the lengths of the
+// sequences, and a long unit among few is cut between many CTAs.  A border
+// that falls into a unit of kSnap tiles or fewer moves to that unit's start:
+// joining its parts would cost more than it evens out.
+//
+// No list of the work is made: each CTA sums the sequences' costs and finds
+// its own range, one thread per sequence.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace mbert {
+
+// kBlockQ: query rows of a unit (0: all of a sequence's); kTile: keys of a tile.
+template <int kThreads, int kBlockQ_, int kTile_, int kAlpha_, int kSnap_>
+struct CrossSplit {
+    static constexpr int kBlockQ = kBlockQ_, kTile = kTile_, kAlpha = kAlpha_, kSnap = kSnap_;
+    static constexpr int kWarps = kThreads / 32;
+
+    struct Scratch {
+        long long warp[kWarps];
+        long long base[2];
+        int seq[2];
+    };
+
+    // What a sequence needs: rows, tiles and units.
+    struct Seq {
+        int q_row, q_len, k_row, k_all, k_len, tiles, blocks;   // k_len: up to the last visible key
+        long long units;
+        __device__ __forceinline__ long long cost() const { return units * (tiles + kAlpha); }
+    };
+
+    const CrossArgs &a;
+    int unit_heads;         // heads that units are made for
+    int ctas;
+    long long total;        // X
+    long long lo, hi;       // this CTA's range
+    int seq0;               // the sequence that holds lo, and where it starts
+    long long base0;
+
+    __device__ explicit CrossSplit(const CrossArgs &args, int heads) : a(args), unit_heads(heads) {}
+
+    __device__ __forceinline__ Seq load(int s) const
+    {
+        Seq q;
+        if (a.cu_q) {
+            q.q_row = __ldg(a.cu_q + s);
+            q.q_len = __ldg(a.cu_q + s + 1) - q.q_row;
+        } else {
+            q.q_row = s * a.len_q;
+            q.q_len = a.len_q;
+        }
+        if (a.cu_k) {
+            q.k_row = __ldg(a.cu_k + s);
+            q.k_all = __ldg(a.cu_k + s + 1) - q.k_row;
+        } else {
+            q.k_row = s * a.len_k;
+            q.k_all = a.len_k;
+        }
+        q.k_len = a.key_len ? min(q.k_all, __ldg(a.key_len + s)) : q.k_all;
+        q.tiles = max(1, (q.k_len + kTile - 1) / kTile);
+        q.blocks = kBlockQ ? (q.q_len + (kBlockQ ? kBlockQ : 1) - 1) / (kBlockQ ? kBlockQ : 1) : (q.q_len > 0);
+        q.units = static_cast<long long>(unit_heads) * q.blocks;
+        return q;
+    }
+
+    __device__ __forceinline__ long long border(int c) const
+    {
+        return static_cast<long long>(c) * total / ctas;
+    }
+
+    // The CTA whose range holds x (borders inside long units do not move).
+    __device__ __forceinline__ int cta_of(long long x) const
+    {
+        return static_cast<int>(((x + 1) * ctas - 1) / total);
+    }
+
+    // Every thread of the block.  False: nothing to do for this CTA (or the
+    // offsets are bad, then *a.err says so and no CTA does anything).
+    __device__ bool find(Scratch &sm, int max_ctas, int min_cost)
+    {
+        const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+        long long sum = 0;
+        int bad = 0;
+        for (int s = tid; s < a.n_seqs; s += kThreads) {
+            const Seq q = load(s);
+            if (q.q_len < 0 || q.k_all < 0 || q.q_row < 0 || q.k_row < 0 ||
+                static_cast<long long>(q.q_row) + q.q_len > a.rows_q ||
+                static_cast<long long>(q.k_row) + q.k_all > a.rows_k)
+                bad |= kErrBadCu;
+            else if (q.q_len > a.max_q)
+                bad |= kErrTooLong;
+            else
+                sum += q.cost();
+        }
+        if (tid == 0 && ((a.cu_q && a.cu_q[0] != 0) || (a.cu_k && a.cu_k[0] != 0)))
+            bad |= kErrBadCu;
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0)
+            sm.warp[warp] = sum;
+        if (tid < 2)
+            sm.seq[tid] = -1;
+        const int any = __syncthreads_or(bad);
+        if (any) {
+            if (bad && blockIdx.x == 0)
+                atomicOr(a.err, bad);
+            return false;
+        }
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            total += sm.warp[w];
+        if (total == 0)
+            return false;
+        const long long want = (total + min_cost - 1) / min_cost;
+        ctas = want < max_ctas ? static_cast<int>(want) : max_ctas;
+        if (static_cast<int>(blockIdx.x) >= ctas)
+            return false;
+        lo = border(blockIdx.x);
+        hi = border(blockIdx.x + 1);
+        // the sequences that hold lo and hi
+        long long carry = 0;
+        for (int s0 = 0; s0 < a.n_seqs; s0 += kThreads) {
+            const int s = s0 + tid;
+            const long long v = s < a.n_seqs ? load(s).cost() : 0;
+            long long incl = v;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d)
+                    incl += o;
+            }
+            __syncthreads();            // the sums of the last round are read
+            if (lane == 31)
+                sm.warp[warp] = incl;
+            __syncthreads();
+            long long before = carry, all = carry;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                before += w < warp ? sm.warp[w] : 0;
+                all += sm.warp[w];
+            }
+            const long long start = before + incl - v;
+            if (start <= lo && lo < start + v) {
+                sm.seq[0] = s;
+                sm.base[0] = start;
+            }
+            if (start <= hi && hi < start + v) {
+                sm.seq[1] = s;
+                sm.base[1] = start;
+            }
+            carry = all;
+            if (carry > hi)
+                break;
+        }
+        __syncthreads();
+        seq0 = sm.seq[0];
+        base0 = sm.base[0];
+        lo = snap(lo, seq0, base0);
+        hi = snap(hi, sm.seq[1], sm.base[1]);   // none for hi = total: stays
+        return lo < hi;
+    }
+
+    __device__ __forceinline__ long long snap(long long x, int s, long long base) const
+    {
+        if (s < 0)
+            return x;
+        const Seq q = load(s);
+        if (q.tiles > kSnap)
+            return x;
+        return x - (x - base) % (q.tiles + kAlpha);
+    }
+
+    // A run of key tiles [kb, ke) of one unit.
+    struct Seg {
+        Seq s;
+        int seq, head, q0;
+        int kb, ke;
+        long long xa;       // place of the unit's first tile
+    };
+
+    // Walks this CTA's segments in order.
+    struct Iter {
+        int seq = -1;
+        long long base = 0, x = 0;
+        Seq s;
+    };
+
+    __device__ __forceinline__ Iter begin() const
+    {
+        Iter it;
+        it.seq = seq0;
+        it.base = base0;
+        it.x = lo;
+        it.s = load(seq0);
+        return it;
+    }
+
+    __device__ bool next(Iter &it, Seg &g) const
+    {
+        while (it.x < hi) {
+            const long long d = it.x - it.base, c = it.s.cost();
+            if (d >= c) {
+                it.base += c;
+                if (++it.seq >= a.n_seqs)
+                    return false;
+                it.s = load(it.seq);
+                continue;
+            }
+            const int per = it.s.tiles + kAlpha;
+            const long long u = d / per;
+            const int r = static_cast<int>(d - u * per);
+            const long long after = it.base + (u + 1) * per;
+            if (r >= it.s.tiles) {
+                it.x = after;
+                continue;
+            }
+            const long long left = hi - it.x;
+            g.s = it.s;
+            g.seq = it.seq;
+            g.head = static_cast<int>(u / it.s.blocks);
+            g.q0 = static_cast<int>(u % it.s.blocks) * kBlockQ;
+            g.kb = r;
+            g.ke = left < it.s.tiles - r ? static_cast<int>(r + left) : it.s.tiles;
+            g.xa = it.base + u * per;
+            it.x = g.ke < it.s.tiles ? hi : after;
+            return true;
+        }
+        return false;
+    }
+
+    // Parts that a cut unit has.
+    __device__ __forceinline__ int parts(const Seg &g) const
+    {
+        return cta_of(g.xa + g.s.tiles - 1) - cta_of(g.xa) + 1;
+    }
+};
+
+}  // namespace mbert

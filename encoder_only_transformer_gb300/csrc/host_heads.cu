@@ -1,5 +1,6 @@
 // Host side of the calls beside the attention block: argument checks of the
-// rotary and norm calls, the rotation's frequencies.
+// rotary, norm and cross-attention calls, the rotation's frequencies, the
+// choice of the cross-attention kernel.
 #include <cmath>
 
 #include "mbert_attn.h"
@@ -245,4 +246,167 @@ MBERT_API int mbert_attn_qk_norm_rotary(mbert_attn *h, const mbert_attn_heads *q
     const mbert_attn_heads *const xs[2] = {q, k};
     return rotary_impl(h, xs, tokens, head_dim, dtype, norm, eps, rope, positions, position_bits, cu_seqlens,
                        n_seqs, 0, stream);
+}
+
+namespace {
+
+// How a cross-attention call runs: the kernel, its CTAs and the workspace.
+struct CrossPlan {
+    bool token;             // few rows per sequence and key head
+    int group, max_q, ctas, unit_rows;
+    int64_t records, parts, lens, bits, bytes;      // offsets and the total
+};
+
+int64_t align256(int64_t x) { return (x + 255) & ~static_cast<int64_t>(255); }
+
+// Checks everything but the device pointers' contents.
+int cross_plan(const mbert_attn *h, const mbert_attn_cross_args *c, CrossPlan *p)
+{
+    if (!h || !c)
+        return MBERT_ERR_BAD_ARG;
+    if ((c->head_dim != 64 && c->head_dim != 128) || (c->dtype != MBERT_BF16 && c->dtype != MBERT_F16))
+        return MBERT_ERR_UNSUPPORTED;
+    if (c->heads < 1 || c->heads > 65536 || c->kv_heads < 1 || c->heads % c->kv_heads ||
+        c->rows_q < 0 || c->rows_q > INT32_MAX || c->rows_k < 0 || c->rows_k > INT32_MAX || c->n_seqs < 0 ||
+        c->max_seqlen_q < 0 || !(c->scale >= 0.f) || !std::isfinite(c->scale))
+        return MBERT_ERR_BAD_ARG;
+    if (c->n_seqs == 0 && (c->rows_q > 0 || c->rows_k > 0))
+        return MBERT_ERR_BAD_ARG;
+    if (c->n_seqs > 0 && ((!c->cu_q && c->rows_q % c->n_seqs) || (!c->cu_k && c->rows_k % c->n_seqs)))
+        return MBERT_ERR_BAD_ARG;
+    p->group = c->heads / c->kv_heads;
+    int64_t most = c->cu_q || c->n_seqs == 0 ? c->rows_q : c->rows_q / c->n_seqs;
+    if (c->max_seqlen_q > 0 && c->max_seqlen_q < most) {
+        if (!c->cu_q)
+            return MBERT_ERR_SEQ_TOO_LONG;
+        most = c->max_seqlen_q;
+    }
+    p->max_q = static_cast<int>(most);
+    // up to 16 rows per (sequence, key head): the kernel that reads K and V
+    // once for all of them
+    p->token = most * p->group <= kCrossTokenRows;
+    p->ctas = p->token ? h->num_sms * cross_token_ctas(c->head_dim) : h->num_sms;
+    p->unit_rows = p->token ? kCrossTokenRows : kCrossBlockRows;
+    p->records = 0;
+    p->parts = align256(static_cast<int64_t>(sizeof(CrossRecord)) * p->ctas);
+    p->lens = align256(p->parts + 2 * p->ctas * cross_slot_floats(p->unit_rows, c->head_dim) * 4);
+    p->bits = c->key_mask ? align256(p->lens + 4ll * c->n_seqs) : p->lens;
+    p->bytes = c->key_mask ? align256(p->bits + 4 * (key_bit_word(c->rows_k, c->n_seqs) + 1)) : p->lens;
+    return MBERT_OK;
+}
+
+}  // namespace
+
+MBERT_API int mbert_attn_cross_workspace(mbert_attn *h, const mbert_attn_cross_args *args, int64_t *bytes)
+{
+    CrossPlan p;
+    if (!bytes)
+        return MBERT_ERR_BAD_ARG;
+    const int rc = cross_plan(h, args, &p);
+    if (rc == MBERT_OK)
+        *bytes = p.bytes;
+    return rc;
+}
+
+MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args, void *workspace,
+                               int64_t workspace_bytes, void *stream)
+{
+    CrossPlan p;
+    int rc = cross_plan(h, args, &p);
+    if (rc != MBERT_OK)
+        return rc;
+    const mbert_attn_cross_args &c = *args;
+    if (c.rows_q == 0)
+        return MBERT_OK;
+    const bool keys = c.rows_k > 0;
+    if (!c.q || !c.out || !workspace || workspace_bytes < p.bytes || (keys && (!c.k || !c.v)))
+        return MBERT_ERR_BAD_ARG;
+    for (const void *ptr : {c.q, c.k, c.v, static_cast<const void *>(c.out), static_cast<const void *>(workspace)})
+        if (reinterpret_cast<uintptr_t>(ptr) & 15)
+            return MBERT_ERR_BAD_ARG;
+    for (const void *ptr : {static_cast<const void *>(c.cu_q), static_cast<const void *>(c.cu_k),
+                            static_cast<const void *>(c.key_mask)})
+        if (reinterpret_cast<uintptr_t>(ptr) & 3)
+            return MBERT_ERR_BAD_ARG;
+    const int D = c.head_dim;
+    const int64_t qw = static_cast<int64_t>(c.heads) * D, kw = static_cast<int64_t>(c.kv_heads) * D;
+    // rows of whole 16-byte vectors that do not run into each other
+    auto row_ok = [](int64_t pitch, int64_t width) {
+        return pitch >= width && pitch % 8 == 0 && pitch < (1ll << 38);
+    };
+    if (!row_ok(c.q_row, qw) || !row_ok(c.out_row, qw) ||
+        (keys && (!row_ok(c.k_row, kw) || !row_ok(c.v_row, kw))))
+        return MBERT_ERR_BAD_ARG;
+    auto rows = [&](const void *ptr, int64_t n, int64_t pitch, int64_t width) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(ptr);
+        return Extent{lo, lo + static_cast<uintptr_t>(((n - 1) * pitch + width) * 2)};
+    };
+    auto flat = [&](const void *ptr, int64_t bytes) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(ptr);
+        return Extent{lo, lo + static_cast<uintptr_t>(bytes)};
+    };
+    const Extent oe = rows(c.out, c.rows_q, c.out_row, qw), we = flat(workspace, p.bytes);
+    auto meet = [](Extent x, Extent y) { return x.lo < y.hi && y.lo < x.hi; };
+    if (may_overlap(oe, c.out_row, qw, rows(c.q, c.rows_q, c.q_row, qw), c.q_row, qw, 2) || meet(oe, we) ||
+        meet(we, rows(c.q, c.rows_q, c.q_row, qw)))
+        return MBERT_ERR_BAD_ARG;
+    if (keys) {
+        const Extent ke = rows(c.k, c.rows_k, c.k_row, kw), ve = rows(c.v, c.rows_k, c.v_row, kw);
+        if (may_overlap(oe, c.out_row, qw, ke, c.k_row, kw, 2) || may_overlap(oe, c.out_row, qw, ve, c.v_row, kw, 2) ||
+            meet(we, ke) || meet(we, ve))
+            return MBERT_ERR_BAD_ARG;
+    }
+    for (const Extent x : {flat(c.cu_q, c.cu_q ? 4ll * (c.n_seqs + 1) : 0), flat(c.cu_k, c.cu_k ? 4ll * (c.n_seqs + 1) : 0),
+                           flat(c.key_mask, c.key_mask ? 4 * c.rows_k : 0)})
+        if (x.hi > x.lo && (meet(oe, x) || meet(we, x)))
+            return MBERT_ERR_BAD_ARG;
+
+    DeviceGuard g(h->device);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    CrossArgs a;
+    const int kbox = p.token ? 64 : kBlockN;
+    // without any key row the maps stand over q: all of it is masked
+    if (encode_rows(h, &a.tm_q, c.q, qw, c.rows_q, c.q_row, kBlockM) != MBERT_OK ||
+        encode_rows(h, &a.tm_k, keys ? c.k : c.q, keys ? kw : qw, keys ? c.rows_k : c.rows_q,
+                    keys ? c.k_row : c.q_row, kbox) != MBERT_OK ||
+        encode_rows(h, &a.tm_v, keys ? c.v : c.q, keys ? kw : qw, keys ? c.rows_k : c.rows_q,
+                    keys ? c.v_row : c.q_row, kbox) != MBERT_OK)
+        return MBERT_ERR_CUDA;
+    a.q = c.q;
+    a.out = c.out;
+    a.q_row = c.q_row;
+    a.out_row = c.out_row;
+    a.cu_q = c.cu_q;
+    a.cu_k = c.cu_k;
+    a.n_seqs = c.n_seqs;
+    a.len_q = c.cu_q ? 0 : static_cast<int>(c.rows_q / c.n_seqs);
+    a.len_k = c.cu_k ? 0 : static_cast<int>(c.rows_k / c.n_seqs);
+    a.rows_q = c.rows_q;
+    a.rows_k = c.rows_k;
+    a.max_q = p.max_q;
+    a.heads = c.heads;
+    a.group = p.group;
+    a.scale_log2 = static_cast<float>((c.scale > 0.f ? c.scale : 1.0 / std::sqrt(static_cast<double>(D))) *
+                                      1.4426950408889634);
+    a.err = h->err;
+    char *ws = static_cast<char *>(workspace);
+    a.records = reinterpret_cast<CrossRecord *>(ws + p.records);
+    a.parts = reinterpret_cast<float *>(ws + p.parts);
+    const bool half = c.dtype == MBERT_F16;
+    cudaError_t e = cudaSuccess;
+    if (c.key_mask && keys) {
+        int32_t *lens = reinterpret_cast<int32_t *>(ws + p.lens);
+        uint32_t *bits = reinterpret_cast<uint32_t *>(ws + p.bits);
+        e = launch_key_bits(a, c.key_mask, bits, lens, st);
+        a.key_len = lens;
+        a.key_bits = bits;
+        h->launches += 1;
+    }
+    if (e == cudaSuccess)
+        e = p.token ? launch_cross_token(a, D, half, p.ctas, st) : launch_cross_blocks(a, D, half, p.ctas, st);
+    if (e == cudaSuccess)
+        e = launch_cross_join(a, D, half, p.token ? p.max_q * p.group : kCrossBlockRows, p.ctas, st);
+    h->launches += 2;
+    h->last_stream = st;
+    return e == cudaSuccess ? MBERT_OK : MBERT_ERR_CUDA;
 }

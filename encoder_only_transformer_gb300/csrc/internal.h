@@ -272,6 +272,58 @@ struct RotaryArgs {
 
 cudaError_t launch_rotary(RotaryArgs &a, int num_sms, cudaStream_t stream);
 
+// Cross attention: packed queries over keys and values of another length
+// (attn_cross.cu: blocks of queries; attn_cross_token.cu: few rows a
+// sequence; cross_join.cu: what goes before and after).
+struct CrossArgs {
+    CUtensorMap tm_q, tm_k, tm_v;       // [rows][heads * D], box 64 columns
+    const void *q = nullptr;
+    void *out = nullptr;
+    long long q_row = 0, out_row = 0;   // row strides in elements
+    const int32_t *cu_q = nullptr, *cu_k = nullptr;   // null: sequences of len_q / len_k rows
+    int n_seqs = 0, len_q = 0, len_k = 0;
+    long long rows_q = 0, rows_k = 0;
+    int max_q = 0;                      // longest query sequence accepted
+    int heads = 0, group = 1;           // query heads, query heads per key head
+    float scale_log2 = 0.f;             // softmax scale in base 2
+    // with a key mask: per sequence the visible keys as bits (sequence s from
+    // word key_bit_word(s) on) and the place after the last visible one
+    const uint32_t *key_bits = nullptr;
+    const int32_t *key_len = nullptr;
+    int32_t *err = nullptr;
+    // units cut between CTAs: a record and two part slots per CTA
+    struct CrossRecord *records = nullptr;
+    float *parts = nullptr;
+};
+
+// What the joining kernel needs of a unit whose first part CTA c holds.
+struct CrossRecord {
+    long long row0;     // first query row
+    int rows;           // rows of the unit (row r: query row0 + r / group, head head0 + r % group)
+    int head0, group;
+    int parts;          // 0: CTA c holds no first part
+};
+
+constexpr int kCrossBlockRows = 256;    // rows of a unit of attn_cross.cu
+constexpr int kCrossTokenRows = 16;     // rows of a unit of attn_cross_token.cu
+
+// First word of sequence s's key bits: every sequence starts a new word.
+__host__ __device__ inline long long key_bit_word(long long k_row, int s) { return k_row / 32 + s; }
+
+constexpr long long cross_slot_floats(int rows, int dim) { return static_cast<long long>(rows) * (dim + 2); }
+
+// CTAs of the token kernel on one SM (by shared memory and registers).
+constexpr int cross_token_ctas(int dim) { return dim == 64 ? 3 : 2; }
+
+// key_mask [rows_k] (non-zero: visible) to bits and lengths per sequence.
+cudaError_t launch_key_bits(const CrossArgs &a, const int32_t *key_mask, uint32_t *bits, int32_t *len,
+                            cudaStream_t stream);
+cudaError_t launch_cross_blocks(const CrossArgs &a, int dim, bool half, int ctas, cudaStream_t stream);
+cudaError_t launch_cross_token(const CrossArgs &a, int dim, bool half, int ctas, cudaStream_t stream);
+// Joins the parts of cut units; rows: those of a unit (kCrossBlockRows after
+// the first kernel, at most kCrossTokenRows after the second).
+cudaError_t launch_cross_join(const CrossArgs &a, int dim, bool half, int rows, int ctas, cudaStream_t stream);
+
 // Number of sequences up to which the local kernel finds its blocks itself
 // (above it the plan kernel writes a work list first).
 constexpr int kLocalSelfScheduleMaxSeqs = 256;

@@ -322,6 +322,56 @@ int mbert_attn_qk_norm_rotary(mbert_attn *h, const mbert_attn_heads *q, const mb
                               int position_bits, const int32_t *cu_seqlens, int n_seqs,
                               void *stream);
 
+/* Attention of packed queries over keys and values of another length (a
+ * decoder's queries over the encoder's states, a pooling head's, or rows that
+ * were turned by mbert_attn_rotary, with cu_q = cu_k):
+ *   out[i, h] = sum_j softmax_j(scale q[i, h] . k[j, h / g]) v[j, h / g],
+ * j over the visible keys of i's sequence, g = heads / kv_heads query heads
+ * sharing a key head.  No rotation, no causal mask.  A row without a visible
+ * key is 0.  What invisible and other sequences' rows hold, infinities and NaN
+ * included, does not matter.
+ *   q, out       device [rows_q][heads][head_dim], rows q_row / out_row elements apart
+ *   k, v         device [rows_k][kv_heads][head_dim], rows k_row / v_row apart
+ *                (16-byte aligned, pitches multiples of 8 and at least the
+ *                row's width, so views of fused rows are fine; out overlaps
+ *                nothing else; k and v unused for rows_k = 0).
+ *   head_dim     64 or 128; dtype MBERT_BF16 or MBERT_F16, else MBERT_ERR_UNSUPPORTED.
+ *   scale        > 0 and finite, or 0 for 1 / sqrt(head_dim).
+ *   cu_q, cu_k   device int32 [n_seqs + 1]: cu[0] = 0, non-decreasing, cu[n] <= rows; empty
+ *                sequences are allowed on either side; rows of out from cu_q[n] on are left
+ *                as they were.  NULL: n_seqs sequences of rows / n_seqs each (a padded batch).
+ *   max_seqlen_q the caller's bound on the longest query sequence, 0 for none.  Up to
+ *                16 / g a kernel for single tokens runs, which reads k and v once; a longer
+ *                sequence found on the device sets MBERT_ERR_SEQ_TOO_LONG.
+ *   key_mask     device int32 [rows_k], non-zero = visible, or NULL for all.
+ * Scores, weights' sums and products in fp32; weights are rounded to dtype for the second
+ * product (off by 2^-8 of themselves at most in bf16, 2^-11 in fp16), out once. */
+typedef struct {
+    const void *q, *k, *v;
+    void *out;
+    int64_t q_row, k_row, v_row, out_row;
+    int64_t rows_q, rows_k;
+    int heads, kv_heads, head_dim, dtype;
+    float scale;
+    int n_seqs;
+    const int32_t *cu_q, *cu_k;
+    int max_seqlen_q;
+    const int32_t *key_mask;
+} mbert_attn_cross_args;
+
+/* Bytes of device workspace that mbert_attn_cross needs for these arguments
+ * (pointers need only be NULL or not).  Host only. */
+int mbert_attn_cross_workspace(mbert_attn *h, const mbert_attn_cross_args *args, int64_t *bytes);
+
+/* Enqueue the call.  workspace: device memory of that size, 16-byte aligned,
+ * contents irrelevant; it may be used again once the call's work is done, so
+ * calls that may overlap on the GPU need one each.  When the device-side
+ * checks of cu_q and cu_k fail nothing is written and the error is reported by
+ * mbert_attn_get_error().  Results do not depend on timing: the parts of a
+ * sequence that several CTAs share are joined in a fixed order. */
+int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+
 /* Wait for the handle's most recent stream, then return (and clear) the
  * device error word as a status: MBERT_OK, MBERT_ERR_BAD_CU_SEQLENS,
  * MBERT_ERR_SEQ_TOO_LONG or MBERT_ERR_TIMEOUT; MBERT_ERR_CUDA if the wait
