@@ -146,6 +146,20 @@ def _stream_ptr(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+# the current stream's handle without a Stream object around it (a tenth of
+# the time, which single-token calls feel), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device) -> int:
+    return _raw_stream(device.index) if _raw_stream is not None else _stream_ptr(device)
+
+
+def _layout(*tensors):
+    """What the checks of a call look at besides the pointers."""
+    return tuple([(t.shape, t.stride(), t.dtype, t.device) for t in tensors])
+
+
 class Rotary:
     """How a head is rotated: its first `dim` numbers (even, up to 256) in
     pairs, `layout` "half" (x[m], x[m + dim/2]) or "interleaved" (x[2m],
@@ -229,6 +243,15 @@ class Attention:
         h = _vp()
         _check(lib.mbert_attn_create(ctypes.byref(h), ctypes.byref(cfg), self.device.index), "create")
         self._h = h
+        # layouts that have passed a call's checks, and what follows from them
+        # (no data, no addresses): a call like an earlier one skips the checks
+        self._known = {}
+
+    def _remember(self, key, value):
+        if len(self._known) >= 1024:
+            self._known.clear()
+        self._known[key] = value
+        return value
 
     @property
     def handle(self):
@@ -380,17 +403,21 @@ class Attention:
             raise TypeError(f"{name} must have the rows, head size and type of the other tensor")
 
     def _heads(self, src, dst, name, weight=None):
+        """-> (dst, Heads) of a [T, H, D] tensor and its result"""
         if dst is None:
             dst = torch.empty(src.shape, dtype=src.dtype, device=self.device)
-        else:
+        elif dst is not src:
             self._check_heads(dst, name, src)
             if dst.shape != src.shape:
                 raise TypeError(f"{name} must have the shape {list(src.shape)}")
         T, H, D = src.shape
-        # a dimension of one element has no stride that matters
-        strides = [(x.stride(0) if T > 1 else H * D, x.stride(1) if H > 1 else D) for x in (src, dst)]
+        (a, b, _), (c, d, _) = src.stride(), dst.stride()
+        if T <= 1 or H <= 1:
+            # a dimension of one element has no stride that matters
+            a, c = (a, c) if T > 1 else (H * D, H * D)
+            b, d = (b, d) if H > 1 else (D, D)
         return dst, Heads(src.data_ptr(), dst.data_ptr(), None if weight is None else weight.data_ptr(),
-                          H, *strides[0], *strides[1])
+                          H, a, b, c, d)
 
     def _positions(self, positions, cu_seqlens, tokens):
         """-> (positions pointer, bits, cu_seqlens pointer, sequences)"""
@@ -398,8 +425,8 @@ class Attention:
             raise ValueError("give either positions or cu_seqlens")
         if positions is None:
             self._check_cu(cu_seqlens)
-            return None, 0, cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
-        if (positions.dtype not in (torch.int32, torch.int64) or tuple(positions.shape) != (tokens,)
+            return None, 0, cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1
+        if (positions.dtype not in (torch.int32, torch.int64) or positions.shape != (tokens,)
                 or positions.device != self.device or not positions.is_contiguous()):
             raise TypeError(f"positions must be a contiguous int32 or int64 [{tokens}] tensor on {self.device}")
         return positions.data_ptr(), 8 * positions.element_size(), None, 0
@@ -413,12 +440,16 @@ class Attention:
         last sequence are left as they were).  x may be strided (a view of fused
         rows); out may be x.  inverse=True turns the other way (the transpose:
         the gradient of a turned tensor goes back through it)."""
-        self._check_heads(x, "x")
-        pos = self._positions(positions, cu_seqlens, x.shape[0])
+        key = ("rotary", _layout(x))
+        known = self._known.get(key)
+        if known is None:
+            self._check_heads(x, "x")
+            known = self._remember(key, (x.shape[0], x.shape[2], _DTYPES[x.dtype]))
+        T, D, dtype = known
+        pos = self._positions(positions, cu_seqlens, T)
         out, heads = self._heads(x, out, "out")
-        st = load_library().mbert_attn_rotary(
-            self._h, ctypes.byref(heads), x.shape[0], x.shape[2], _DTYPES[x.dtype],
-            ctypes.byref(rope.spec), *pos, 1 if inverse else 0, _stream_ptr(self.device))
+        st = _lib.mbert_attn_rotary(self._h, ctypes.byref(heads), T, D, dtype, ctypes.byref(rope.spec), *pos,
+                                    1 if inverse else 0, _stream_of(self.device))
         _check(st, "rotary")
         return out
 
@@ -436,31 +467,40 @@ class Attention:
         first = q if q is not None else k
         if first is None:
             raise ValueError("give q, k or both")
-        structs, outs = [], []
-        for t, w, o, name in ((q, q_weight, q_out, "q"), (k, k_weight, k_out, "k")):
-            if t is None:
-                structs.append(None)
-                outs.append(None)
-                continue
-            self._check_heads(t, name, first)
-            if (w is None or w.dtype != t.dtype or tuple(w.shape) != (t.shape[2],)
-                    or w.device != self.device or not w.is_contiguous()):
-                raise TypeError(f"{name}_weight must be a contiguous [{t.shape[2]}] tensor of {name}'s type")
-            o, h = self._heads(t, o, f"{name}_out", w)
-            structs.append(ctypes.byref(h))
-            outs.append(o)
+        for t, w, name in ((q, q_weight, "q"), (k, k_weight, "k")):
+            if t is not None and w is None:
+                raise TypeError(f"{name}_weight is missing")
+        key = ("qk_norm_rotary", None if q is None else _layout(q, q_weight),
+               None if k is None else _layout(k, k_weight))
+        known = self._known.get(key)
+        if known is None:
+            for t, w, name in ((q, q_weight, "q"), (k, k_weight, "k")):
+                if t is None:
+                    continue
+                self._check_heads(t, name, first)
+                if (w.dtype != t.dtype or tuple(w.shape) != (t.shape[2],)
+                        or w.device != self.device or not w.is_contiguous()):
+                    raise TypeError(f"{name}_weight must be a contiguous [{t.shape[2]}] tensor of {name}'s type")
+            known = self._remember(key, (first.shape[0], first.shape[2], _DTYPES[first.dtype]))
+        T, D, dtype = known
         if rope is None or rope.dim == 0:
             if positions is not None or cu_seqlens is not None:
                 raise ValueError("positions or cu_seqlens without a rotation")
             pos = (None, 0, None, 0)
         else:
-            pos = self._positions(positions, cu_seqlens, first.shape[0])
-        st = load_library().mbert_attn_qk_norm_rotary(
-            self._h, structs[0], structs[1], first.shape[0], first.shape[2], _DTYPES[first.dtype],
-            _NORMS[norm], float(eps), None if rope is None else ctypes.byref(rope.spec), *pos,
-            _stream_ptr(self.device))
+            pos = self._positions(positions, cu_seqlens, T)
+        qh = kh = None
+        if q is not None:
+            q_out, qh = self._heads(q, q_out, "q_out", q_weight)
+            qh = ctypes.byref(qh)
+        if k is not None:
+            k_out, kh = self._heads(k, k_out, "k_out", k_weight)
+            kh = ctypes.byref(kh)
+        st = _lib.mbert_attn_qk_norm_rotary(
+            self._h, qh, kh, T, D, dtype, _NORMS[norm], float(eps),
+            None if rope is None else ctypes.byref(rope.spec), *pos, _stream_of(self.device))
         _check(st, "qk_norm_rotary")
-        return tuple(outs)
+        return (q_out if q is not None else None), (k_out if k is not None else None)
 
     def _check_cross(self, t, name, dims):
         """A [..., heads, head_dim] tensor whose heads lie side by side."""
@@ -471,24 +511,39 @@ class Attention:
         if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]):
             raise ValueError(f"the heads of {name} must lie side by side in each row")
 
-    def _cross(self, q, k, v, out, rows_q, rows_k, pitches, n_seqs, cu_q, cu_k, max_seqlen_q, key_mask, scale):
+    def _cross(self, known, q, k, v, out, cu_q, cu_k, key_mask):
+        """Enqueue a call whose layouts have been checked; known: the arguments
+        without their pointers, and the workspace's size."""
+        template, need = known
+        args = CrossArgs.from_buffer_copy(template)
+        args.q, args.k, args.v, args.out = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr()
+        if cu_q is not None:
+            args.cu_q, args.cu_k = cu_q.data_ptr(), cu_k.data_ptr()
+        if key_mask is not None:
+            args.key_mask = key_mask.data_ptr()
+        # of the call's own, from torch's allocator: calls on other streams and
+        # captured ones never share it
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        st = _lib.mbert_attn_cross(self._h, ctypes.byref(args), ws.data_ptr(), need, _stream_of(self.device))
+        _check(st, "cross_attention")
+        return out
+
+    def _cross_known(self, key, q, k, v, out, rows_q, rows_k, pitches, n_seqs, packed, max_seqlen_q, key_mask, scale):
+        """Remember the arguments (without pointers) and the workspace's size."""
         if scale is None:
             scale = 0.0
         elif not 0.0 < scale < float("inf"):
             raise ValueError("scale must be positive and finite")
-        args = CrossArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *pitches, rows_q, rows_k,
-                         q.shape[-2], k.shape[-2], q.shape[-1], _DTYPES[q.dtype], scale, n_seqs, cu_q, cu_k,
-                         int(max_seqlen_q), None if key_mask is None else key_mask.data_ptr())
-        lib = load_library()
+        # the size depends on which pointers there are, not on where they point
+        there = ctypes.addressof(ctypes.c_int(0))
+        args = CrossArgs(None, None, None, None, *pitches, rows_q, rows_k, q.shape[-2], k.shape[-2], q.shape[-1],
+                         _DTYPES[q.dtype], scale, n_seqs, there if packed else None, there if packed else None,
+                         int(max_seqlen_q), None if key_mask is None else there)
         need = _c_i64()
-        _check(lib.mbert_attn_cross_workspace(self._h, ctypes.byref(args), ctypes.byref(need)), "cross_attention")
-        # of the call's own, from torch's allocator: calls on other streams and
-        # captured ones never share it
-        ws = torch.empty(need.value, dtype=torch.uint8, device=self.device)
-        st = lib.mbert_attn_cross(self._h, ctypes.byref(args), ws.data_ptr(), need.value,
-                                  _stream_ptr(self.device))
-        _check(st, "cross_attention")
-        return out
+        _check(load_library().mbert_attn_cross_workspace(self._h, ctypes.byref(args), ctypes.byref(need)),
+               "cross_attention")
+        args.cu_q = args.cu_k = args.key_mask = None
+        return self._remember(key, (bytes(args), need.value))
 
     def cross_attention(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                         cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, max_seqlen_q: int = 0,
@@ -504,27 +559,34 @@ class Attention:
         on the longest query sequence: give it for single tokens (at most
         16 / (Hq / Hk) rows a sequence), which then read k and v once.  scale
         None: 1 / sqrt(D).  Rows may be strided (views of fused rows)."""
-        for t, name in ((q, "q"), (k, "k"), (v, "v")):
-            self._check_cross(t, name, 3)
-        if k.shape != v.shape or k.shape[2] != q.shape[2] or not q.dtype == k.dtype == v.dtype:
-            raise TypeError("q, k and v must agree in type and head size, k and v in shape")
-        self._check_cu(cu_seqlens_q)
-        self._check_cu(cu_seqlens_k)
-        if cu_seqlens_q.numel() != cu_seqlens_k.numel() or cu_seqlens_q.numel() < 1:
-            raise ValueError("cu_seqlens_q and cu_seqlens_k must name the same number of sequences")
+        key = ("cross", _layout(q, k, v, cu_seqlens_q, cu_seqlens_k), None if out is None else _layout(out),
+               None if key_mask is None else _layout(key_mask), max_seqlen_q, scale)
+        known = self._known.get(key)
+        if known is None:
+            for t, name in ((q, "q"), (k, "k"), (v, "v")):
+                self._check_cross(t, name, 3)
+            if k.shape != v.shape or k.shape[2] != q.shape[2] or not q.dtype == k.dtype == v.dtype:
+                raise TypeError("q, k and v must agree in type and head size, k and v in shape")
+            self._check_cu(cu_seqlens_q)
+            self._check_cu(cu_seqlens_k)
+            if cu_seqlens_q.numel() != cu_seqlens_k.numel() or cu_seqlens_q.numel() < 1:
+                raise ValueError("cu_seqlens_q and cu_seqlens_k must name the same number of sequences")
+            if out is not None:
+                self._check_cross(out, "out", 3)
+                if out.shape != q.shape or out.dtype != q.dtype:
+                    raise TypeError(f"out must be a {q.dtype} tensor of shape {list(q.shape)}")
+            if key_mask is not None and (key_mask.dtype != torch.int32 or tuple(key_mask.shape) != (k.shape[0],)
+                                         or key_mask.device != self.device or not key_mask.is_contiguous()):
+                raise TypeError(f"key_mask must be a contiguous int32 [{k.shape[0]}] tensor on {self.device}")
+            # one row has no pitch that matters, and a new result is contiguous
+            width = q.shape[1] * q.shape[2]
+            pitches = [t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2] for t in (q, k, v)]
+            pitches.append(out.stride(0) if out is not None and out.shape[0] > 1 else width)
+            known = self._cross_known(key, q, k, v, out, q.shape[0], k.shape[0], pitches,
+                                      cu_seqlens_q.numel() - 1, True, max_seqlen_q, key_mask, scale)
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        else:
-            self._check_cross(out, "out", 3)
-            if out.shape != q.shape or out.dtype != q.dtype:
-                raise TypeError(f"out must be a {q.dtype} tensor of shape {list(q.shape)}")
-        if key_mask is not None and (key_mask.dtype != torch.int32 or tuple(key_mask.shape) != (k.shape[0],)
-                                     or key_mask.device != self.device or not key_mask.is_contiguous()):
-            raise TypeError(f"key_mask must be a contiguous int32 [{k.shape[0]}] tensor on {self.device}")
-        # one row has no pitch that matters
-        pitches = [t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2] for t in (q, k, v, out)]
-        return self._cross(q, k, v, out, q.shape[0], k.shape[0], pitches, cu_seqlens_q.numel() - 1,
-                           cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), max_seqlen_q, key_mask, scale)
+        return self._cross(known, q, k, v, out, cu_seqlens_q, cu_seqlens_k, key_mask)
 
     def cross_attention_padded(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                                key_mask: torch.Tensor = None, scale: float = None,
@@ -534,28 +596,36 @@ class Attention:
         out [B, Sq, Hq, D].  Every query row is computed; one whose keys are all
         pads is 0.  Rows may be strided, with the batch rows one pitch apart
         (views of fused rows).  Else as cross_attention."""
-        for t, name in ((q, "q"), (k, "k"), (v, "v")):
-            self._check_cross(t, name, 4)
-        if (k.shape != v.shape or k.shape[3] != q.shape[3] or k.shape[0] != q.shape[0]
-                or not q.dtype == k.dtype == v.dtype):
-            raise TypeError("q, k and v must agree in type, batch and head size, k and v in shape")
-        B, Sq, Sk = q.shape[0], q.shape[1], k.shape[1]
+        key = ("cross_padded", _layout(q, k, v), None if out is None else _layout(out),
+               None if key_mask is None else _layout(key_mask), scale)
+        known = self._known.get(key)
+        if known is None:
+            for t, name in ((q, "q"), (k, "k"), (v, "v")):
+                self._check_cross(t, name, 4)
+            if (k.shape != v.shape or k.shape[3] != q.shape[3] or k.shape[0] != q.shape[0]
+                    or not q.dtype == k.dtype == v.dtype):
+                raise TypeError("q, k and v must agree in type, batch and head size, k and v in shape")
+            B, Sq, Sk = q.shape[0], q.shape[1], k.shape[1]
+            if out is not None:
+                self._check_cross(out, "out", 4)
+                if out.shape != q.shape or out.dtype != q.dtype:
+                    raise TypeError(f"out must be a {q.dtype} tensor of shape {list(q.shape)}")
+            if key_mask is not None and (key_mask.dtype != torch.int32 or tuple(key_mask.shape) != (B, Sk)
+                                         or key_mask.device != self.device or not key_mask.is_contiguous()):
+                raise TypeError(f"key_mask must be a contiguous int32 [{B}, {Sk}] tensor on {self.device}")
+            pitches = []
+            for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+                if t is None:
+                    pitches.append(q.shape[2] * q.shape[3])
+                    continue
+                pitch = t.stride(1) if t.shape[1] > 1 else t.stride(0) if B > 1 else t.shape[2] * t.shape[3]
+                if B > 1 and t.shape[1] > 0 and t.stride(0) != t.shape[1] * pitch:
+                    raise ValueError(f"the rows of {name} must be one pitch apart throughout the batch")
+                pitches.append(pitch)
+            known = self._cross_known(key, q, k, v, out, B * Sq, B * Sk, pitches, B, False, 0, key_mask, scale)
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        else:
-            self._check_cross(out, "out", 4)
-            if out.shape != q.shape or out.dtype != q.dtype:
-                raise TypeError(f"out must be a {q.dtype} tensor of shape {list(q.shape)}")
-        if key_mask is not None and (key_mask.dtype != torch.int32 or tuple(key_mask.shape) != (B, Sk)
-                                     or key_mask.device != self.device or not key_mask.is_contiguous()):
-            raise TypeError(f"key_mask must be a contiguous int32 [{B}, {Sk}] tensor on {self.device}")
-        pitches = []
-        for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-            pitch = t.stride(1) if t.shape[1] > 1 else t.stride(0) if B > 1 else t.shape[2] * t.shape[3]
-            if B > 1 and t.shape[1] > 0 and t.stride(0) != t.shape[1] * pitch:
-                raise ValueError(f"the rows of {name} must be one pitch apart throughout the batch")
-            pitches.append(pitch)
-        return self._cross(q, k, v, out, B * Sq, B * Sk, pitches, B, None, None, 0, key_mask, scale)
+        return self._cross(known, q, k, v, out, None, None, key_mask)
 
     def key_counts(self, cu_seqlens: torch.Tensor, total_tokens: int, layer_kind,
                    max_seqlen: int = 0) -> torch.Tensor:

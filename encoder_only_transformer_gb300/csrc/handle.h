@@ -56,13 +56,12 @@ struct mbert_attn {
     std::vector<cudaEvent_t> ev[MBERT_PROFILE_SLOTS];
     size_t ev_used[MBERT_PROFILE_SLOTS] = {};
     int64_t launches = 0;                   // every kernel this handle enqueued
-    // recently encoded tensor maps, by (address, shape, pitch, box): encoding one
+    // recently encoded tensor maps, by (address, width, rows): encoding one
     // costs microseconds of host time, as much as a short kernel
     struct MapEntry {
         const void *ptr = nullptr;
-        int64_t width = 0;
-        int64_t rows = -1, pitch = 0;
-        int box = 0;
+        int width = 0;
+        int64_t rows = -1;
         uint64_t used = 0;
         CUtensorMap map;
     };
@@ -74,8 +73,8 @@ namespace mbert {
 
 // 2-D tensor map of 16-bit elements over [rows][width], rows `pitch` elements
 // apart, box 64 columns x `box` rows, 128-byte swizzle, out-of-range reads
-// give 0.  Kept in the handle's cache.
-int encode_rows(mbert_attn *h, CUtensorMap *tm, const void *ptr, int64_t width, int64_t rows,
+// give 0.
+int encode_rows(const mbert_attn *h, CUtensorMap *tm, const void *ptr, int64_t width, int64_t rows,
                 int64_t pitch, int box);
 
 struct DeviceGuard {

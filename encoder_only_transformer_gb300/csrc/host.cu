@@ -138,10 +138,27 @@ int profile_events(mbert_attn *h, int slot, cudaEvent_t *ev0, cudaEvent_t *ev1)
 }
 
 // 2-D bf16 tensor map over [rows][width] (row pitch = width * 2 bytes),
-// box 64 columns x 128 rows.
+// box 64 columns x 128 rows, from the handle's cache.
 int encode_map(mbert_attn *h, CUtensorMap *tm, const void *ptr, int width, int64_t rows)
 {
-    return encode_rows(h, tm, ptr, width, rows, width, kBlockM);
+    mbert_attn::MapEntry *victim = &h->maps[0];
+    for (auto &m : h->maps) {
+        if (m.ptr == ptr && m.width == width && m.rows == rows) {
+            m.used = ++h->map_clock;
+            *tm = m.map;
+            return MBERT_OK;
+        }
+        if (m.used < victim->used)
+            victim = &m;
+    }
+    if (encode_rows(h, tm, ptr, width, rows, width, kBlockM) != MBERT_OK)
+        return MBERT_ERR_CUDA;
+    victim->ptr = ptr;
+    victim->width = width;
+    victim->rows = rows;
+    victim->used = ++h->map_clock;
+    victim->map = *tm;
+    return MBERT_OK;
 }
 
 bool ranges_overlap(const void *a, size_t na, const void *b, size_t nb)
@@ -183,19 +200,9 @@ Plan make_plan(mbert_attn *h, const int32_t *cu, int n_seqs, int64_t T, int max_
 
 }  // namespace
 
-int mbert::encode_rows(mbert_attn *h, CUtensorMap *tm, const void *ptr, int64_t width, int64_t rows,
+int mbert::encode_rows(const mbert_attn *h, CUtensorMap *tm, const void *ptr, int64_t width, int64_t rows,
                        int64_t pitch, int box_rows)
 {
-    mbert_attn::MapEntry *victim = &h->maps[0];
-    for (auto &m : h->maps) {
-        if (m.ptr == ptr && m.width == width && m.rows == rows && m.pitch == pitch && m.box == box_rows) {
-            m.used = ++h->map_clock;
-            *tm = m.map;
-            return MBERT_OK;
-        }
-        if (m.used < victim->used)
-            victim = &m;
-    }
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(kHeadDim), static_cast<cuuint32_t>(box_rows)};
@@ -204,16 +211,7 @@ int mbert::encode_rows(mbert_attn *h, CUtensorMap *tm, const void *ptr, int64_t 
                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        return MBERT_ERR_CUDA;
-    victim->ptr = ptr;
-    victim->width = width;
-    victim->rows = rows;
-    victim->pitch = pitch;
-    victim->box = box_rows;
-    victim->used = ++h->map_clock;
-    victim->map = *tm;
-    return MBERT_OK;
+    return r == CUDA_SUCCESS ? MBERT_OK : MBERT_ERR_CUDA;
 }
 
 MBERT_API int mbert_attn_default_config(mbert_attn_config *cfg)

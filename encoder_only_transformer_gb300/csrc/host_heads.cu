@@ -96,9 +96,8 @@ int rotary_impl(mbert_attn *h, const mbert_attn_heads *const (&xs)[2], int64_t t
             // turns per position modulo 1 as a 64-bit binary fraction
             double t = rope->freq[m] / kTwoPi;
             t -= std::floor(t);
-            const double t32 = std::ldexp(t, 32), hi = std::floor(t32);
-            a.turns[m] = (static_cast<uint64_t>(hi) << 32) +
-                         static_cast<uint64_t>(std::floor(std::ldexp(t32 - hi, 32)));
+            const double t32 = t * 0x1p32, hi = std::floor(t32);
+            a.turns[m] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>((t32 - hi) * 0x1p32);
         }
         // exactly one source of positions
         if (positions) {
@@ -366,7 +365,7 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     CrossArgs a;
     const int kbox = p.token ? 64 : kBlockN;
     // without any key row the maps stand over q: all of it is masked
-    if (encode_rows(h, &a.tm_q, c.q, qw, c.rows_q, c.q_row, kBlockM) != MBERT_OK ||
+    if ((!p.token && encode_rows(h, &a.tm_q, c.q, qw, c.rows_q, c.q_row, kBlockM) != MBERT_OK) ||
         encode_rows(h, &a.tm_k, keys ? c.k : c.q, keys ? kw : qw, keys ? c.rows_k : c.rows_q,
                     keys ? c.k_row : c.q_row, kbox) != MBERT_OK ||
         encode_rows(h, &a.tm_v, keys ? c.v : c.q, keys ? kw : qw, keys ? c.rows_k : c.rows_q,

@@ -265,8 +265,9 @@ struct RotaryArgs {
     const int32_t *cu = nullptr;
     int n_seqs = 0;
     int32_t *err = nullptr;
-    // set by the launcher: lanes of a head, rows of a warp, warps of a row group
-    int lanes_log2 = 0, rows_per_warp = 1, parts = 1;
+    // set by the launcher: lanes of a head; a block's heads, rows, and the
+    // rows it takes side by side
+    int lanes_log2 = 0, block_heads = 1, block_rows = 1, teams = 1;
     uint64_t turns[kMaxRotaryPairs] = {};   // turns per position, 64-bit binary fractions
 };
 

@@ -14,13 +14,14 @@
 // and of one fp32 rounding, at any position.
 //
 // What bounds it: every element is read once and written once, a few flops
-// each; the sines are the only dear part, and all heads of a row share them.
-// So a warp takes a few whole rows: it computes their cosines and sines once,
-// one pair per lane, into shared memory (2 KB per warp), then walks the rows'
-// heads.  A head is cut into slots of two vectors of VW numbers (the two
-// halves of VW pairs), one slot per lane, the 2^k >= slots lanes of a head
-// side by side, so a norm needs k shuffles and no shared memory.  Loads of kU
-// heads are in flight per lane before the first is needed.
+// each, so memory, as long as the instructions per element stay few.  So a
+// thread keeps one place of a row (its tensor, its head, its slot of two
+// vectors of VW numbers, the halves of VW pairs) and walks down the rows: no
+// index arithmetic but an add, weights in registers.  kU rows are in flight
+// per thread before the first is needed.  The 2^k >= slots lanes of a head lie
+// side by side, so a norm needs k shuffles and no shared memory.  All heads of
+// a row share its cosines and sines: the block computes its rows' once into
+// shared memory, laid out so that the lanes' 16-byte reads have no conflicts.
 #include <cuda_fp16.h>
 
 #include "mbert_attn.h"
@@ -30,24 +31,81 @@
 namespace mbert {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kTableBytes = 2048;      // cos/sin per warp
-constexpr int kTablePairs = kTableBytes / 8;
-
-template <typename T> __device__ __forceinline__ float to_f32(T v);
-template <> __device__ __forceinline__ float to_f32(float v) { return v; }
-template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ float from_f32(float v) { return v; }
-template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+constexpr int kMaxThreads = 384;
+constexpr int kTableBytes = 16384;      // cosines and sines of a block's rows
+constexpr int kMaxRows = 64;            // rows of a block
 
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Vec {
     T v[N];
 };
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const Vec<T, N> &x, float (&f)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f[i] = to_f32<T>(x.v[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void pack(const float (&f)[N], Vec<float, N> &x)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        x.v[i] = f[i];
+}
+template <int N>
+__device__ __forceinline__ void pack(const float (&f)[N], Vec<__half, N> &x)
+{
+    if constexpr (N == 1) {
+        x.v[0] = __float2half_rn(f[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            *reinterpret_cast<__half2 *>(&x.v[i]) = __floats2half2_rn(f[i], f[i + 1]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void pack(const float (&f)[N], Vec<__nv_bfloat16, N> &x)
+{
+    if constexpr (N == 1) {
+        x.v[0] = __float2bfloat16_rn(f[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            *reinterpret_cast<__nv_bfloat162 *>(&x.v[i]) = __floats2bfloat162_rn(f[i], f[i + 1]);
+    }
+}
+
+// Two fp32 products or sums per instruction where N is even.
+template <int N>
+__device__ __forceinline__ void mul_to(float (&y)[N], const float (&a)[N], const float (&b)[N])
+{
+    if constexpr (N == 1) {
+        y[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            f2_split(fmul2(f2(a[i], a[i + 1]), f2(b[i], b[i + 1])), y[i], y[i + 1]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void fma_to(float (&y)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N])
+{
+    if constexpr (N == 1) {
+        y[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            f2_split(ffma2(f2(a[i], a[i + 1]), f2(b[i], b[i + 1]), f2(c[i], c[i + 1])), y[i], y[i + 1]);
+    }
+}
 
 // Position of a row: given (32 or 64 bits), or its place in its sequence.
 // False for a row behind the last sequence.
@@ -67,209 +125,244 @@ __device__ __forceinline__ bool row_position(const RotaryArgs &a, long long row,
         pos = row - __ldg(a.cu + lo);
         return true;
     }
-    if (a.pos32)
-        pos = __ldg(a.pos32 + row);
-    else if (a.pos64)
-        pos = __ldg(a.pos64 + row);
-    else
-        pos = 0;
+    pos = a.pos32 ? __ldg(a.pos32 + row) : a.pos64 ? __ldg(a.pos64 + row) : 0;
     return true;
 }
 
+// Place of pair m in a row's table of cosines (sines follow): with 8 pairs per
+// slot, the first 4 of every slot, then the second 4, so that neighbouring
+// lanes read neighbouring 16 bytes.
+template <int VW>
+__device__ __forceinline__ int table_place(int m, int rot_slots)
+{
+    return VW == 8 ? (((m >> 2 & 1) * rot_slots + (m >> 3)) << 2) + (m & 3) : m;
+}
+
+template <int VW>
+__device__ __forceinline__ void table_read(const float *t, int slot, int rot_slots, float (&c)[VW])
+{
+    if constexpr (VW == 8) {
+        *reinterpret_cast<float4 *>(&c[0]) = *reinterpret_cast<const float4 *>(t + 4 * slot);
+        *reinterpret_cast<float4 *>(&c[4]) = *reinterpret_cast<const float4 *>(t + 4 * (rot_slots + slot));
+    } else {
+#pragma unroll
+        for (int i = 0; i < VW; ++i)
+            c[i] = t[VW * slot + i];
+    }
+}
+
 // VW numbers per vector; SPL slots per lane (more than one only where a head
-// has more than 32 slots); kU heads in flight per lane.
-template <typename T, int VW, int SPL, int kU, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads)
+// has more than 32 slots); kU rows in flight per thread.
+template <typename T, int VW, int SPL, int kU, bool kInterleaved, bool kNorm>
+__global__ void __launch_bounds__(kMaxThreads)
 rotary_kernel(const __grid_constant__ RotaryArgs a)
 {
     pdl_wait();
-    __shared__ __align__(16) float2 s_table[kWarps][kTablePairs];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = a.rot >> 1;
+    __shared__ __align__(16) float s_table[kTableBytes / 4];
+    __shared__ long long s_pos[kMaxRows];
+    __shared__ bool s_live[kMaxRows];
     using V = Vec<T, VW>;
+    const int tid = threadIdx.x;
+    const int half = a.rot >> 1;
+    const int slots = a.dim / (2 * VW), rot_slots = a.rot / (2 * VW);
+    const long long row0 = static_cast<long long>(blockIdx.x) * a.block_rows;
+    const int rows = static_cast<int>(min(static_cast<long long>(a.block_rows), a.tokens - row0));
+
+    // this thread's place: its rows team, team + teams, ..., its head and slot
+    const int item = tid >> a.lanes_log2, slot0 = tid & ((1 << a.lanes_log2) - 1);
+    const int heads = a.x[0].heads + a.x[1].heads;
+    const int head_all = blockIdx.y * a.block_heads + item % a.block_heads;
+    const int team = item / a.block_heads;
+    const bool placed = team < a.teams && head_all < heads;
+    const int which = head_all >= a.x[0].heads;
+    const RotaryRows &x = a.x[which];
+    const int head = head_all - (which ? a.x[0].heads : 0);
+    const T *src = static_cast<const T *>(x.src) + head * x.src_head + (row0 + team) * x.src_row;
+    T *dst = static_cast<T *>(x.dst) + head * x.dst_head + (row0 + team) * x.dst_row;
+    const long long src_step = a.teams * x.src_row, dst_step = a.teams * x.dst_row;
+    int off0[SPL], off1[SPL];
+#pragma unroll
+    for (int j = 0; j < SPL; ++j) {
+        const int s = slot0 + 32 * j;
+        const bool turned = s < rot_slots;
+        off0[j] = turned && !kInterleaved ? s * VW : 2 * s * VW;
+        off1[j] = off0[j] + (turned && !kInterleaved ? half : VW);
+    }
+    auto load = [&](int r, V (&v0)[SPL], V (&v1)[SPL]) {
+#pragma unroll
+        for (int j = 0; j < SPL; ++j) {
+            v0[j] = v1[j] = V{};
+            if (placed && r < rows && slot0 + 32 * j < slots) {
+                v0[j] = *reinterpret_cast<const V *>(src + off0[j]);
+                v1[j] = *reinterpret_cast<const V *>(src + off1[j]);
+            }
+        }
+        src += src_step;
+    };
+    // the first rows are on their way while the table is made
+    V v0[kU][SPL], v1[kU][SPL];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+        load(team + u * a.teams, v0[u], v1[u]);
 
     // cu_seqlens is only data here (a bad one cannot lead outside the rows);
     // one block reports it
-    if (a.cu && blockIdx.x == 0) {
-        bool bad = threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.n_seqs] > a.tokens);
-        for (int s = threadIdx.x; s < a.n_seqs; s += kThreads)
+    if (a.cu && blockIdx.x == 0 && blockIdx.y == 0) {
+        bool bad = tid == 0 && (a.cu[0] != 0 || a.cu[a.n_seqs] > a.tokens);
+        for (int s = tid; s < a.n_seqs; s += blockDim.x)
             bad |= a.cu[s + 1] < a.cu[s];
         if (bad)
             atomicOr(a.err, kErrBadCu);
     }
+    for (int r = tid; r < rows; r += blockDim.x) {
+        long long p = 0;
+        s_live[r] = row_position(a, row0 + r, p);
+        s_pos[r] = p;
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * half; i += blockDim.x) {
+        const int r = i / half, m = i - r * half;
+        // t / 2^63 half turns, in [-1, 1)
+        const unsigned long long t = static_cast<unsigned long long>(s_pos[r]) * a.turns[m];
+        float s, c;
+        sincospif(static_cast<float>(static_cast<long long>(t)) * 0x1p-63f, &s, &c);
+        float *row = s_table + 2 * half * r + table_place<VW>(m, rot_slots);
+        row[0] = c * a.amplitude;
+        row[half] = s * a.sin_amplitude;
+    }
+    __syncthreads();
 
-    // this warp's rows [row0, row0 + rows) and its share of their heads
-    const long long task = static_cast<long long>(blockIdx.x) * kWarps + warp;
-    const int part = static_cast<int>(task % a.parts);
-    const long long row0 = task / a.parts * a.rows_per_warp;
-    if (row0 < a.tokens) {
-        const int rows = static_cast<int>(min(static_cast<long long>(a.rows_per_warp), a.tokens - row0));
-        uint32_t live = 0;             // bit i: row row0 + i has a position
-        {
-            long long pos = 0;
-            const bool ok = lane < rows && row_position(a, row0 + lane, pos);
-            live = __ballot_sync(0xffffffffu, ok);
-            for (int m0 = 0; m0 < half; m0 += 32) {
-                const int m = m0 + lane;
-                const unsigned long long w = m < half ? a.turns[m] : 0ull;
-                for (int i = 0; i < rows; ++i) {
-                    const long long p = __shfl_sync(0xffffffffu, pos, i);
-                    const unsigned long long t = static_cast<unsigned long long>(p) * w;
-                    float s, c;
-                    // t / 2^63 half turns, in [-1, 1)
-                    sincospif(static_cast<float>(static_cast<long long>(t)) * 0x1p-63f, &s, &c);
-                    if (m < half)
-                        s_table[warp][i * half + m] = make_float2(c * a.amplitude, s * a.sin_amplitude);
-                }
+    float w0[SPL][VW], w1[SPL][VW];
+    if constexpr (kNorm) {
+#pragma unroll
+        for (int j = 0; j < SPL; ++j) {
+            V w{}, z{};
+            if (placed && slot0 + 32 * j < slots) {
+                w = *reinterpret_cast<const V *>(static_cast<const T *>(x.weight) + off0[j]);
+                z = *reinterpret_cast<const V *>(static_cast<const T *>(x.weight) + off1[j]);
             }
+            unpack(w, w0[j]);
+            unpack(z, w1[j]);
         }
-        __syncwarp();
-
-        const int gl = 1 << a.lanes_log2;               // lanes of one head
-        const int sub = lane >> a.lanes_log2, slot0 = lane & (gl - 1);
-        const int ipw = 32 >> a.lanes_log2;             // heads side by side
-        const int slots = a.dim / (2 * VW), rot_slots = a.rot / (2 * VW);
-        const int mid_off = kInterleaved ? VW : half;   // second vector of a turned slot
-        for (int t = 0; t < 2; ++t) {
-            const RotaryRows &x = a.x[t];
-            if (x.heads == 0)
-                continue;
-            // the lane's slots: offsets of its two vectors, the weights
-            int off0[SPL], off1[SPL];
-            V w0[SPL], w1[SPL];
+    }
+    const float inv_dim = 1.f / a.dim;
+    for (int r0 = 0; r0 < rows; r0 += kU * a.teams) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int r = r0 + team + u * a.teams;
+            float f0[SPL][VW], f1[SPL][VW];
 #pragma unroll
             for (int j = 0; j < SPL; ++j) {
-                const int s = slot0 + 32 * j;
-                const bool turned = s < rot_slots;
-                off0[j] = turned && !kInterleaved ? s * VW : 2 * s * VW;
-                off1[j] = off0[j] + (turned ? mid_off : VW);
-                if (a.norm && s < slots) {
-                    w0[j] = *reinterpret_cast<const V *>(static_cast<const T *>(x.weight) + off0[j]);
-                    w1[j] = *reinterpret_cast<const V *>(static_cast<const T *>(x.weight) + off1[j]);
-                }
+                unpack(v0[u][j], f0[j]);
+                unpack(v1[u][j], f1[j]);
             }
-            const int items = rows * x.heads;
-            for (int it0 = part * ipw; it0 < items; it0 += a.parts * ipw * kU) {
-                V v0[kU][SPL], v1[kU][SPL];
-                int row_of[kU];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int it = it0 + u * a.parts * ipw + sub;
-                    const int r = it / x.heads;
-                    row_of[u] = it < items && (live >> r & 1) ? r : -1;
-                    if (row_of[u] >= 0) {
-                        const T *src = static_cast<const T *>(x.src) + (row0 + r) * x.src_row +
-                                       static_cast<long long>(it - r * x.heads) * x.src_head;
-#pragma unroll
-                        for (int j = 0; j < SPL; ++j)
-                            if (slot0 + 32 * j < slots) {
-                                v0[u][j] = *reinterpret_cast<const V *>(src + off0[j]);
-                                v1[u][j] = *reinterpret_cast<const V *>(src + off1[j]);
-                            }
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const bool mine = row_of[u] >= 0;
-                    float f0[SPL][VW], f1[SPL][VW];
+            // this slot's next row
+            load(r + kU * a.teams, v0[u], v1[u]);
+            if constexpr (kNorm) {
+                // statistics in fp32 over the head's lanes; LayerNorm in two
+                // passes (mean, then squared deviations)
+                if (a.norm == MBERT_NORM_LAYER) {
+                    float s = 0.f;
 #pragma unroll
                     for (int j = 0; j < SPL; ++j)
 #pragma unroll
-                        for (int i = 0; i < VW; ++i) {
-                            const bool in = mine && slot0 + 32 * j < slots;
-                            f0[j][i] = in ? to_f32<T>(v0[u][j].v[i]) : 0.f;
-                            f1[j][i] = in ? to_f32<T>(v1[u][j].v[i]) : 0.f;
-                        }
-                    if (a.norm) {
-                        // statistics in fp32 over the head's lanes; LayerNorm in
-                        // two passes (mean, then squared deviations)
-                        float mean = 0.f;
-                        if (a.norm == MBERT_NORM_LAYER) {
-                            float s = 0.f;
+                        for (int i = 0; i < VW; ++i)
+                            s += f0[j][i] + f1[j][i];
+                    for (int d = 1 << a.lanes_log2 >> 1; d; d >>= 1)
+                        s += __shfl_xor_sync(0xffffffffu, s, d);
+                    const float mean = s * inv_dim;
 #pragma unroll
-                            for (int j = 0; j < SPL; ++j)
-#pragma unroll
-                                for (int i = 0; i < VW; ++i)
-                                    s += f0[j][i] + f1[j][i];
-                            for (int d = gl >> 1; d; d >>= 1)
-                                s += __shfl_xor_sync(0xffffffffu, s, d);
-                            mean = s / a.dim;
-                        }
-                        float q = 0.f;
-#pragma unroll
-                        for (int j = 0; j < SPL; ++j)
-                            if (slot0 + 32 * j < slots) {
-#pragma unroll
-                                for (int i = 0; i < VW; ++i) {
-                                    f0[j][i] -= mean;
-                                    f1[j][i] -= mean;
-                                    q = fmaf(f0[j][i], f0[j][i], q);
-                                    q = fmaf(f1[j][i], f1[j][i], q);
-                                }
-                            }
-                        for (int d = gl >> 1; d; d >>= 1)
-                            q += __shfl_xor_sync(0xffffffffu, q, d);
-                        const float inv = 1.f / sqrtf(q / a.dim + a.eps);
-#pragma unroll
-                        for (int j = 0; j < SPL; ++j)
+                    for (int j = 0; j < SPL; ++j)
+                        if (slot0 + 32 * j < slots) {
 #pragma unroll
                             for (int i = 0; i < VW; ++i) {
-                                f0[j][i] *= inv * to_f32<T>(w0[j].v[i]);
-                                f1[j][i] *= inv * to_f32<T>(w1[j].v[i]);
-                            }
-                    }
-                    if (!mine)
-                        continue;
-                    const int it = it0 + u * a.parts * ipw + sub;
-                    T *dst = static_cast<T *>(x.dst) + (row0 + row_of[u]) * x.dst_row +
-                             static_cast<long long>(it - row_of[u] * x.heads) * x.dst_head;
-#pragma unroll
-                    for (int j = 0; j < SPL; ++j) {
-                        const int s = slot0 + 32 * j;
-                        if (s >= slots)
-                            continue;
-                        V o0, o1;
-                        if (s < rot_slots) {
-                            const float2 *cs = &s_table[warp][row_of[u] * half + s * VW];
-                            if (kInterleaved) {
-                                // pairs are neighbours: (0, 1), (2, 3), ... over both vectors
-                                float y[2 * VW], z[2 * VW];
-#pragma unroll
-                                for (int i = 0; i < VW; ++i) {
-                                    y[i] = f0[j][i];
-                                    y[VW + i] = f1[j][i];
-                                }
-#pragma unroll
-                                for (int m = 0; m < VW; ++m) {
-                                    const float2 r = cs[m];
-                                    z[2 * m] = y[2 * m] * r.x - y[2 * m + 1] * r.y;
-                                    z[2 * m + 1] = y[2 * m + 1] * r.x + y[2 * m] * r.y;
-                                }
-#pragma unroll
-                                for (int i = 0; i < VW; ++i) {
-                                    o0.v[i] = from_f32<T>(z[i]);
-                                    o1.v[i] = from_f32<T>(z[VW + i]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < VW; ++i) {
-                                    const float2 r = cs[i];
-                                    o0.v[i] = from_f32<T>(f0[j][i] * r.x - f1[j][i] * r.y);
-                                    o1.v[i] = from_f32<T>(f1[j][i] * r.x + f0[j][i] * r.y);
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < VW; ++i) {
-                                o0.v[i] = from_f32<T>(f0[j][i]);
-                                o1.v[i] = from_f32<T>(f1[j][i]);
+                                f0[j][i] -= mean;
+                                f1[j][i] -= mean;
                             }
                         }
-                        *reinterpret_cast<V *>(dst + off0[j]) = o0;
-                        *reinterpret_cast<V *>(dst + off1[j]) = o1;
-                    }
+                }
+                float q[VW];
+#pragma unroll
+                for (int i = 0; i < VW; ++i)
+                    q[i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < SPL; ++j) {
+                    fma_to(q, f0[j], f0[j], q);
+                    fma_to(q, f1[j], f1[j], q);
+                }
+                float sum = q[0];
+#pragma unroll
+                for (int i = 1; i < VW; ++i)
+                    sum += q[i];
+                for (int d = 1 << a.lanes_log2 >> 1; d; d >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const float inv = rsqrtf(fmaf(sum, inv_dim, a.eps));
+                float scale[VW];
+#pragma unroll
+                for (int i = 0; i < VW; ++i)
+                    scale[i] = inv;
+#pragma unroll
+                for (int j = 0; j < SPL; ++j) {
+                    mul_to(f0[j], f0[j], scale);
+                    mul_to(f1[j], f1[j], scale);
+                    mul_to(f0[j], f0[j], w0[j]);
+                    mul_to(f1[j], f1[j], w1[j]);
                 }
             }
+            if (placed && r < rows && s_live[r]) {
+                const float *row = s_table + 2 * half * r;
+#pragma unroll
+                for (int j = 0; j < SPL; ++j) {
+                    const int s = slot0 + 32 * j;
+                    if (s >= slots)
+                        continue;
+                    if (s < rot_slots) {
+                        float c[VW], sn[VW];
+                        table_read<VW>(row, s, rot_slots, c);
+                        table_read<VW>(row + half, s, rot_slots, sn);
+                        if constexpr (kInterleaved) {
+                            // pairs are neighbours: (0, 1), (2, 3), ... over both vectors
+                            float y[2 * VW];
+#pragma unroll
+                            for (int i = 0; i < VW; ++i) {
+                                y[i] = f0[j][i];
+                                y[VW + i] = f1[j][i];
+                            }
+#pragma unroll
+                            for (int m = 0; m < VW; ++m) {
+                                const float p = y[2 * m], q2 = y[2 * m + 1];
+                                y[2 * m] = p * c[m] - q2 * sn[m];
+                                y[2 * m + 1] = q2 * c[m] + p * sn[m];
+                            }
+#pragma unroll
+                            for (int i = 0; i < VW; ++i) {
+                                f0[j][i] = y[i];
+                                f1[j][i] = y[VW + i];
+                            }
+                        } else {
+                            float p[VW], q2[VW], ns[VW];
+#pragma unroll
+                            for (int i = 0; i < VW; ++i)
+                                ns[i] = -sn[i];
+                            mul_to(p, f0[j], c);
+                            mul_to(q2, f1[j], c);
+                            fma_to(p, f1[j], ns, p);
+                            fma_to(q2, f0[j], sn, q2);
+#pragma unroll
+                            for (int i = 0; i < VW; ++i) {
+                                f0[j][i] = p[i];
+                                f1[j][i] = q2[i];
+                            }
+                        }
+                    }
+                    V o0, o1;
+                    pack(f0[j], o0);
+                    pack(f1[j], o1);
+                    *reinterpret_cast<V *>(dst + off0[j]) = o0;
+                    *reinterpret_cast<V *>(dst + off1[j]) = o1;
+                }
+            }
+            dst += dst_step;
         }
     }
     pdl_trigger();
@@ -282,27 +375,44 @@ cudaError_t launch(RotaryArgs &a, int num_sms, cudaStream_t stream)
     a.lanes_log2 = 0;
     while ((1 << a.lanes_log2) < slots && a.lanes_log2 < 5)
         ++a.lanes_log2;
-    const int ipw = 32 >> a.lanes_log2;
-    const int heads = a.x[0].heads > a.x[1].heads ? a.x[0].heads : a.x[1].heads;
-    // rows per warp: enough that a warp's sines serve kU heads per lane, as
-    // far as its table goes, and fewer while that leaves SMs without work
-    int rows = (kU * ipw + heads - 1) / heads;
-    const int fit = a.rot ? kTablePairs / (a.rot / 2) : 32;
-    rows = rows > fit ? fit : rows;
-    rows = rows > 32 ? 32 : rows;
-    while (rows > 1 && (a.tokens + rows - 1) / rows < static_cast<long long>(num_sms) * 16)
-        rows = (rows + 1) / 2;
-    a.rows_per_warp = rows;
-    const long long groups = (a.tokens + rows - 1) / rows;
-    // few rows (single tokens): the heads of a row go to several warps
-    a.parts = 1;
-    if (groups < static_cast<long long>(num_sms) * 4) {
-        const int want = (rows * heads + ipw - 1) / ipw;
-        a.parts = want > kWarps ? kWarps : want;
+    const int lanes = 1 << a.lanes_log2;
+    const int heads = a.x[0].heads + a.x[1].heads;
+    // Heads of a block: all, where they fit; else equal shares.  Then as many
+    // teams (rows side by side) as leave the fewest lanes of whole warps idle.
+    const int fit = kMaxThreads / lanes;
+    const int shares = (heads + fit - 1) / fit;
+    a.block_heads = (heads + shares - 1) / shares;
+    int threads = 0;
+    double best = -1.0;
+    for (int t = 1; t * a.block_heads * lanes <= kMaxThreads && t <= a.tokens; ++t) {
+        const int th = (t * a.block_heads * lanes + 31) / 32 * 32;
+        const double use = static_cast<double>(t * a.block_heads * lanes) / th + (th >= 192 ? 0.5 : th / 384.0);
+        if (use > best + 1e-9) {
+            best = use;
+            threads = th;
+            a.teams = t;
+        }
     }
-    const long long blocks = (groups * a.parts + kWarps - 1) / kWarps;
-    auto kernel = a.interleaved ? rotary_kernel<T, VW, SPL, kU, true> : rotary_kernel<T, VW, SPL, kU, false>;
-    return launch_chained(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a);
+    // Rows of a block: what the table holds, fewer while that leaves less than
+    // six blocks per SM (and at least kU per team while that leaves two)
+    const int step = a.teams * kU;
+    int rows = a.rot ? kTableBytes / (4 * a.rot) : kMaxRows;
+    rows = rows > kMaxRows ? kMaxRows : rows;
+    const long long even = (a.tokens * shares + num_sms * 6 - 1) / (num_sms * 6);
+    if (even < rows)
+        rows = static_cast<int>(even);
+    if (rows > step)
+        rows = rows / step * step;
+    if (rows < a.teams)
+        rows = a.teams;
+    const int most = a.rot ? kTableBytes / (4 * a.rot) : kMaxRows;
+    a.block_rows = rows > most ? most : rows;
+    const dim3 grid(static_cast<unsigned>((a.tokens + a.block_rows - 1) / a.block_rows), shares);
+    void (*kernel)(RotaryArgs) =
+        a.norm ? (a.interleaved ? rotary_kernel<T, VW, SPL, kU, true, true> : rotary_kernel<T, VW, SPL, kU, false, true>)
+               : (a.interleaved ? rotary_kernel<T, VW, SPL, kU, true, false>
+                                : rotary_kernel<T, VW, SPL, kU, false, false>);
+    return launch_chained(kernel, grid, dim3(threads), 0, stream, a);
 }
 
 }  // namespace
