@@ -203,6 +203,7 @@ class Rotary:
         _check(load_library().mbert_attn_rotary_init(
             ctypes.byref(self.spec), int(dim), _LAYOUTS[layout], float(base),
             None if sc is None else ctypes.byref(sc)), "rotary_init")
+        self._ref = ctypes.byref(self.spec)
 
     @property
     def dim(self) -> int:
@@ -448,8 +449,8 @@ class Attention:
         T, D, dtype = known
         pos = self._positions(positions, cu_seqlens, T)
         out, heads = self._heads(x, out, "out")
-        st = _lib.mbert_attn_rotary(self._h, ctypes.byref(heads), T, D, dtype, ctypes.byref(rope.spec), *pos,
-                                    1 if inverse else 0, _stream_of(self.device))
+        st = _lib.mbert_attn_rotary(self._h, ctypes.byref(heads), T, D, dtype, rope._ref, *pos, 1 if inverse else 0,
+                                    _stream_of(self.device))
         _check(st, "rotary")
         return out
 
@@ -498,7 +499,7 @@ class Attention:
             kh = ctypes.byref(kh)
         st = _lib.mbert_attn_qk_norm_rotary(
             self._h, qh, kh, T, D, dtype, _NORMS[norm], float(eps),
-            None if rope is None else ctypes.byref(rope.spec), *pos, _stream_of(self.device))
+            None if rope is None else rope._ref, *pos, _stream_of(self.device))
         _check(st, "qk_norm_rotary")
         return (q_out if q is not None else None), (k_out if k is not None else None)
 

@@ -267,7 +267,7 @@ struct RotaryArgs {
     int32_t *err = nullptr;
     // set by the launcher: lanes of a head; a block's heads, rows, and the
     // rows it takes side by side
-    int lanes_log2 = 0, block_heads = 1, block_rows = 1, teams = 1;
+    int lanes_log2 = 0, block_heads = 1, block_rows = 1, teams = 1, table_offset = 0;
     uint64_t turns[kMaxRotaryPairs] = {};   // turns per position, 64-bit binary fractions
 };
 

@@ -9,16 +9,19 @@
 // Angles.  f_m / (2 pi), the turns per position, is a 64-bit binary fraction,
 // so the turns of any 64-bit position are exact modulo 1 in one integer
 // multiply (positions wrap in two's complement, so negative ones work too);
-// the signed fraction then goes through sincospif, which needs no range
-// reduction.  The error of an angle is that of f_m's double (2^-53 relative)
-// and of one fp32 rounding, at any position.
+// the signed fraction needs no range reduction.  The error of an angle is that
+// of f_m's double (2^-53 relative), of the cut to 32 bits and of one fp32
+// rounding, at any position.
 //
 // What bounds it: every element is read once and written once, a few flops
 // each, so memory, as long as the instructions per element stay few.  So a
 // thread keeps one place of a row (its tensor, its head, its slot of two
 // vectors of VW numbers, the halves of VW pairs) and walks down the rows: no
-// index arithmetic but an add, weights in registers.  kU rows are in flight
-// per thread before the first is needed.  The 2^k >= slots lanes of a head lie
+// index arithmetic but an add, weights in registers.  kAhead rows are in flight
+// per thread, through its own places in shared memory (cp.async: no registers
+// held by loads, which is what lets enough warps be resident; with the rows in
+// registers the kernel spilled or ran with half the warps, and took 1.7 to 2.2
+// times as long).  The 2^k >= slots lanes of a head lie
 // side by side, so a norm needs k shuffles and no shared memory.  All heads of
 // a row share its cosines and sines: the block computes its rows' once into
 // shared memory, laid out so that the lanes' 16-byte reads have no conflicts.
@@ -31,8 +34,11 @@
 namespace mbert {
 namespace {
 
-constexpr int kMaxThreads = 384;
-constexpr int kTableBytes = 16384;      // cosines and sines of a block's rows
+constexpr int kMaxThreads = 192;
+constexpr int kMinBlocks = 5;
+constexpr int kAhead = 2;               // rows in flight per thread
+constexpr int kBlocksPerSm = 16;        // blocks that the rows are cut into, at least
+constexpr int kTableBytes = 16384;      // cosines and sines of a block's rows, at most
 constexpr int kMaxRows = 64;            // rows of a block
 
 template <typename T, int N>
@@ -83,6 +89,23 @@ __device__ __forceinline__ void pack(const float (&f)[N], Vec<__nv_bfloat16, N> 
     }
 }
 
+// One vector of a thread from global to shared memory, without a register:
+// asynchronously where the hardware can (4, 8 or 16 bytes).
+template <int kBytes>
+__device__ __forceinline__ void fetch(void *smem, const void *gmem)
+{
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(smem)), "l"(gmem) : "memory");
+    else if constexpr (kBytes >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                     :: "r"(smem_u32(smem)), "l"(gmem), "n"(kBytes) : "memory");
+    else
+        *static_cast<uint16_t *>(smem) = *static_cast<const uint16_t *>(gmem);
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kPending) : "memory"); }
+
 // Two fp32 products or sums per instruction where N is even.
 template <int N>
 __device__ __forceinline__ void mul_to(float (&y)[N], const float (&a)[N], const float (&b)[N])
@@ -107,6 +130,32 @@ __device__ __forceinline__ void fma_to(float (&y)[N], const float (&a)[N], const
     }
 }
 
+template <int N>
+__device__ __forceinline__ void add_to(float (&y)[N], const float (&a)[N], const float (&b)[N])
+{
+    if constexpr (N == 1) {
+        y[0] = a[0] + b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            float p = a[i], q = a[i + 1];
+            fadd2(p, q, b[i], b[i + 1]);
+            y[i] = p;
+            y[i + 1] = q;
+        }
+    }
+}
+
+// Sum over the `lanes` (a power of two) neighbouring lanes of a head.
+__device__ __forceinline__ float head_sum(float s, int lanes)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        if (lanes > d)
+            s += __shfl_xor_sync(0xffffffffu, s, d);
+    return s;
+}
+
 // Position of a row: given (32 or 64 bits), or its place in its sequence.
 // False for a row behind the last sequence.
 __device__ __forceinline__ bool row_position(const RotaryArgs &a, long long row, long long &pos)
@@ -127,6 +176,27 @@ __device__ __forceinline__ bool row_position(const RotaryArgs &a, long long row,
     }
     pos = a.pos32 ? __ldg(a.pos32 + row) : a.pos64 ? __ldg(a.pos64 + row) : 0;
     return true;
+}
+
+// Sine and cosine of pos * w turns, w a 64-bit binary fraction.  The product's
+// upper 32 bits modulo 1 are exact but for a carry (2^-32 turns); as a signed
+// number of half turns in [-1, 1) they need no range reduction.  fp32 rows take
+// the accurate functions; for 16-bit rows the fast ones' error (2^-20.9
+// absolute on [-pi, pi]) is far below the rows' own rounding (2^-11, 2^-8).
+template <typename T>
+__device__ __forceinline__ void sin_cos(long long pos, uint64_t w, float &s, float &c)
+{
+    const uint32_t plo = static_cast<uint32_t>(pos), phi = static_cast<uint32_t>(pos >> 32);
+    const uint32_t wlo = static_cast<uint32_t>(w), whi = static_cast<uint32_t>(w >> 32);
+    const int t = static_cast<int>(__umulhi(plo, wlo) + plo * whi + phi * wlo);
+    const float half_turns = static_cast<float>(t) * 0x1p-31f;
+    if constexpr (sizeof(T) == 4) {
+        sincospif(half_turns, &s, &c);
+    } else {
+        const float x = half_turns * 3.14159265f;
+        s = __sinf(x);
+        c = __cosf(x);
+    }
 }
 
 // Place of pair m in a row's table of cosines (sines follow): with 8 pairs per
@@ -152,16 +222,19 @@ __device__ __forceinline__ void table_read(const float *t, int slot, int rot_slo
 }
 
 // VW numbers per vector; SPL slots per lane (more than one only where a head
-// has more than 32 slots); kU rows in flight per thread.
-template <typename T, int VW, int SPL, int kU, bool kInterleaved, bool kNorm>
-__global__ void __launch_bounds__(kMaxThreads)
+// has more than 32 slots).
+template <typename T, int VW, int SPL, bool kInterleaved, bool kNorm>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
 rotary_kernel(const __grid_constant__ RotaryArgs a)
 {
     pdl_wait();
-    __shared__ __align__(16) float s_table[kTableBytes / 4];
+    extern __shared__ __align__(16) uint8_t s_dynamic[];
     __shared__ long long s_pos[kMaxRows];
     __shared__ bool s_live[kMaxRows];
     using V = Vec<T, VW>;
+    // every thread's rows in flight, [ahead][slot][2][thread], then the table
+    V *s_rows = reinterpret_cast<V *>(s_dynamic);
+    float *s_table = reinterpret_cast<float *>(s_dynamic + a.table_offset);
     const int tid = threadIdx.x;
     const int half = a.rot >> 1;
     const int slots = a.dim / (2 * VW), rot_slots = a.rot / (2 * VW);
@@ -188,22 +261,21 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
         off0[j] = turned && !kInterleaved ? s * VW : 2 * s * VW;
         off1[j] = off0[j] + (turned && !kInterleaved ? half : VW);
     }
-    auto load = [&](int r, V (&v0)[SPL], V (&v1)[SPL]) {
+    const int threads = blockDim.x;
+    auto load = [&](int r, int u) {
 #pragma unroll
-        for (int j = 0; j < SPL; ++j) {
-            v0[j] = v1[j] = V{};
+        for (int j = 0; j < SPL; ++j)
             if (placed && r < rows && slot0 + 32 * j < slots) {
-                v0[j] = *reinterpret_cast<const V *>(src + off0[j]);
-                v1[j] = *reinterpret_cast<const V *>(src + off1[j]);
+                fetch<sizeof(V)>(&s_rows[((u * SPL + j) * 2) * threads + tid], src + off0[j]);
+                fetch<sizeof(V)>(&s_rows[((u * SPL + j) * 2 + 1) * threads + tid], src + off1[j]);
             }
-        }
+        fetch_commit();
         src += src_step;
     };
     // the first rows are on their way while the table is made
-    V v0[kU][SPL], v1[kU][SPL];
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
-        load(team + u * a.teams, v0[u], v1[u]);
+    for (int u = 0; u < kAhead; ++u)
+        load(team + u * a.teams, u);
 
     // cu_seqlens is only data here (a bad one cannot lead outside the rows);
     // one block reports it
@@ -220,15 +292,20 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
         s_pos[r] = p;
     }
     __syncthreads();
-    for (int i = tid; i < rows * half; i += blockDim.x) {
-        const int r = i / half, m = i - r * half;
-        // t / 2^63 half turns, in [-1, 1)
-        const unsigned long long t = static_cast<unsigned long long>(s_pos[r]) * a.turns[m];
-        float s, c;
-        sincospif(static_cast<float>(static_cast<long long>(t)) * 0x1p-63f, &s, &c);
-        float *row = s_table + 2 * half * r + table_place<VW>(m, rot_slots);
-        row[0] = c * a.amplitude;
-        row[half] = s * a.sin_amplitude;
+    if (half > 0) {
+        // a thread keeps its pair and walks down the rows
+        const int per = min(half, threads), down = threads / per;
+        if (tid < per * down)
+            for (int m = tid % per; m < half; m += per) {
+                const uint64_t w = a.turns[m];
+                float *place = s_table + table_place<VW>(m, rot_slots);
+                for (int r = tid / per; r < rows; r += down) {
+                    float s, c;
+                    sin_cos<T>(s_pos[r], w, s, c);
+                    place[2 * half * r] = c * a.amplitude;
+                    place[2 * half * r + half] = s * a.sin_amplitude;
+                }
+            }
     }
     __syncthreads();
 
@@ -246,47 +323,53 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
         }
     }
     const float inv_dim = 1.f / a.dim;
-    for (int r0 = 0; r0 < rows; r0 += kU * a.teams) {
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int r = r0 + team + u * a.teams;
+    const int lanes = 1 << a.lanes_log2;
+    auto step = [&](int r0, int u) {
+            const int r = r0 + team;
             float f0[SPL][VW], f1[SPL][VW];
+            fetch_wait<kAhead - 1>();
 #pragma unroll
             for (int j = 0; j < SPL; ++j) {
-                unpack(v0[u][j], f0[j]);
-                unpack(v1[u][j], f1[j]);
+                V x0{}, x1{};
+                if (placed && slot0 + 32 * j < slots) {
+                    x0 = s_rows[((u * SPL + j) * 2) * threads + tid];
+                    x1 = s_rows[((u * SPL + j) * 2 + 1) * threads + tid];
+                }
+                unpack(x0, f0[j]);
+                unpack(x1, f1[j]);
             }
-            // this slot's next row
-            load(r + kU * a.teams, v0[u], v1[u]);
+            // the place is free for a later row
+            load(r + kAhead * a.teams, u);
             if constexpr (kNorm) {
                 // statistics in fp32 over the head's lanes; LayerNorm in two
                 // passes (mean, then squared deviations)
+                float q[VW];
                 if (a.norm == MBERT_NORM_LAYER) {
-                    float s = 0.f;
+                    add_to(q, f0[0], f1[0]);
 #pragma unroll
-                    for (int j = 0; j < SPL; ++j)
+                    for (int j = 1; j < SPL; ++j) {
+                        add_to(q, q, f0[j]);
+                        add_to(q, q, f1[j]);
+                    }
+                    float s = q[0];
 #pragma unroll
-                        for (int i = 0; i < VW; ++i)
-                            s += f0[j][i] + f1[j][i];
-                    for (int d = 1 << a.lanes_log2 >> 1; d; d >>= 1)
-                        s += __shfl_xor_sync(0xffffffffu, s, d);
-                    const float mean = s * inv_dim;
+                    for (int i = 1; i < VW; ++i)
+                        s += q[i];
+                    const float mean = head_sum(s, lanes) * inv_dim;
+#pragma unroll
+                    for (int i = 0; i < VW; ++i)
+                        q[i] = -mean;
 #pragma unroll
                     for (int j = 0; j < SPL; ++j)
                         if (slot0 + 32 * j < slots) {
-#pragma unroll
-                            for (int i = 0; i < VW; ++i) {
-                                f0[j][i] -= mean;
-                                f1[j][i] -= mean;
-                            }
+                            add_to(f0[j], f0[j], q);
+                            add_to(f1[j], f1[j], q);
                         }
                 }
-                float q[VW];
+                mul_to(q, f0[0], f0[0]);
+                fma_to(q, f1[0], f1[0], q);
 #pragma unroll
-                for (int i = 0; i < VW; ++i)
-                    q[i] = 0.f;
-#pragma unroll
-                for (int j = 0; j < SPL; ++j) {
+                for (int j = 1; j < SPL; ++j) {
                     fma_to(q, f0[j], f0[j], q);
                     fma_to(q, f1[j], f1[j], q);
                 }
@@ -294,8 +377,7 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
 #pragma unroll
                 for (int i = 1; i < VW; ++i)
                     sum += q[i];
-                for (int d = 1 << a.lanes_log2 >> 1; d; d >>= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                sum = head_sum(sum, lanes);
                 const float inv = rsqrtf(fmaf(sum, inv_dim, a.eps));
                 float scale[VW];
 #pragma unroll
@@ -363,12 +445,28 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
                 }
             }
             dst += dst_step;
-        }
-    }
+    };
+#pragma unroll 1
+    for (int r0 = 0, u = 0; r0 < rows; r0 += a.teams, u = (u + 1) % kAhead)
+        step(r0, u);
     pdl_trigger();
 }
 
-template <typename T, int VW, int SPL, int kU>
+template <typename T, int VW, int SPL, bool kInterleaved, bool kNorm>
+cudaError_t launch_as(RotaryArgs &a, dim3 grid, int threads, cudaStream_t stream)
+{
+    constexpr int kRowBytes = kAhead * SPL * 2 * VW * static_cast<int>(sizeof(T));   // of a thread
+    static PerDeviceOnce smem_once;
+    const cudaError_t e = smem_opt_in(smem_once, rotary_kernel<T, VW, SPL, kInterleaved, kNorm>,
+                                      kRowBytes * kMaxThreads + kTableBytes);
+    if (e != cudaSuccess)
+        return e;
+    a.table_offset = kRowBytes * threads;
+    return launch_chained(rotary_kernel<T, VW, SPL, kInterleaved, kNorm>, grid, dim3(threads),
+                          a.table_offset + a.block_rows * a.rot * 4, stream, a);
+}
+
+template <typename T, int VW, int SPL>
 cudaError_t launch(RotaryArgs &a, int num_sms, cudaStream_t stream)
 {
     const int slots = a.dim / (2 * VW);
@@ -394,11 +492,11 @@ cudaError_t launch(RotaryArgs &a, int num_sms, cudaStream_t stream)
         }
     }
     // Rows of a block: what the table holds, fewer while that leaves less than
-    // six blocks per SM (and at least kU per team while that leaves two)
-    const int step = a.teams * kU;
+    // kBlocksPerSm blocks per SM (and at least kAhead per team while that leaves two)
+    const int step = a.teams * kAhead;
     int rows = a.rot ? kTableBytes / (4 * a.rot) : kMaxRows;
     rows = rows > kMaxRows ? kMaxRows : rows;
-    const long long even = (a.tokens * shares + num_sms * 6 - 1) / (num_sms * 6);
+    const long long even = (a.tokens * shares + num_sms * kBlocksPerSm - 1) / (num_sms * kBlocksPerSm);
     if (even < rows)
         rows = static_cast<int>(even);
     if (rows > step)
@@ -408,11 +506,10 @@ cudaError_t launch(RotaryArgs &a, int num_sms, cudaStream_t stream)
     const int most = a.rot ? kTableBytes / (4 * a.rot) : kMaxRows;
     a.block_rows = rows > most ? most : rows;
     const dim3 grid(static_cast<unsigned>((a.tokens + a.block_rows - 1) / a.block_rows), shares);
-    void (*kernel)(RotaryArgs) =
-        a.norm ? (a.interleaved ? rotary_kernel<T, VW, SPL, kU, true, true> : rotary_kernel<T, VW, SPL, kU, false, true>)
-               : (a.interleaved ? rotary_kernel<T, VW, SPL, kU, true, false>
-                                : rotary_kernel<T, VW, SPL, kU, false, false>);
-    return launch_chained(kernel, grid, dim3(threads), 0, stream, a);
+    return a.norm ? (a.interleaved ? launch_as<T, VW, SPL, true, true>(a, grid, threads, stream)
+                                   : launch_as<T, VW, SPL, false, true>(a, grid, threads, stream))
+                  : (a.interleaved ? launch_as<T, VW, SPL, true, false>(a, grid, threads, stream)
+                                   : launch_as<T, VW, SPL, false, false>(a, grid, threads, stream));
 }
 
 }  // namespace
@@ -437,19 +534,19 @@ cudaError_t launch_rotary(RotaryArgs &a, int num_sms, cudaStream_t stream)
         vw /= 2;
     switch (a.dtype) {
     case MBERT_F32:
-        return vw == 4 ? launch<float, 4, 1, 4>(a, num_sms, stream)
-               : vw == 2 ? launch<float, 2, 2, 2>(a, num_sms, stream)
-                         : launch<float, 1, 4, 1>(a, num_sms, stream);
+        return vw == 4 ? launch<float, 4, 1>(a, num_sms, stream)
+               : vw == 2 ? launch<float, 2, 2>(a, num_sms, stream)
+                         : launch<float, 1, 4>(a, num_sms, stream);
     case MBERT_F16:
-        return vw == 8 ? launch<__half, 8, 1, 4>(a, num_sms, stream)
-               : vw == 4 ? launch<__half, 4, 1, 4>(a, num_sms, stream)
-               : vw == 2 ? launch<__half, 2, 2, 2>(a, num_sms, stream)
-                         : launch<__half, 1, 4, 1>(a, num_sms, stream);
+        return vw == 8 ? launch<__half, 8, 1>(a, num_sms, stream)
+               : vw == 4 ? launch<__half, 4, 1>(a, num_sms, stream)
+               : vw == 2 ? launch<__half, 2, 2>(a, num_sms, stream)
+                         : launch<__half, 1, 4>(a, num_sms, stream);
     default:
-        return vw == 8 ? launch<__nv_bfloat16, 8, 1, 4>(a, num_sms, stream)
-               : vw == 4 ? launch<__nv_bfloat16, 4, 1, 4>(a, num_sms, stream)
-               : vw == 2 ? launch<__nv_bfloat16, 2, 2, 2>(a, num_sms, stream)
-                         : launch<__nv_bfloat16, 1, 4, 1>(a, num_sms, stream);
+        return vw == 8 ? launch<__nv_bfloat16, 8, 1>(a, num_sms, stream)
+               : vw == 4 ? launch<__nv_bfloat16, 4, 1>(a, num_sms, stream)
+               : vw == 2 ? launch<__nv_bfloat16, 2, 2>(a, num_sms, stream)
+                         : launch<__nv_bfloat16, 1, 4>(a, num_sms, stream);
     }
 }
 
