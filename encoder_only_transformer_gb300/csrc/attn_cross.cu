@@ -10,20 +10,27 @@
 // (cross_join.cu) in a fixed order.  Query heads that share a key head read
 // the same key columns; the copies after the first come from L2.
 //
-// CTA (12 warps):
-//   warps 0-3   softmax group 0 (query tile 0, TMEM lanes 0..127, a thread a row)
-//   warps 4-7   softmax group 1 (query tile 1)
-//   warp  8     TMA producer: Q, K and V rings
-//   warps 9,10  MMA issuers, one per query tile
-//   warp  11    masks: the key bits of a tile to shared memory, and zeros over
-//               the V rows that nothing may see (a weight of 0 times an
-//               infinity there would be NaN)
+// CTA (12 warps for D = 64, 16 for D = 128):
+//   warps 0-3    softmax group 0 (query tile 0, TMEM lanes 0..127, a thread a row)
+//   warps 4-7    softmax group 1 (query tile 1)
+//   warp  8      TMA producer: Q, K and V rings
+//   warp  9      masks: the key bits of a tile to shared memory, and zeros over
+//                the V rows that nothing may see (a weight of 0 times an
+//                infinity there would be NaN)
+//   warps 10,11  MMA issuers, one per query tile
+//   warps 12,13  (D = 128) issuers of O += P V, one per query tile, with S = Q K^T
+//                left to warps 10 and 11
+// An issuer's waits and commits take 100 to 150 clocks each, completed or not.
+// For D = 128, with its steps of 64 keys, they came to the whole period of the
+// loop; with an issuer for each product an iteration went from 3600 clocks to
+// ###.  For D = 64, where the softmax bounds the loop, the larger block would
+// only take registers from it (217 us against 194 at 8192 x 8192 keys).
 // TMEM (512 columns), fp32 except P (16-bit pairs):
 //   D = 64:   S0 S1 (128 each), P0 P1 (64 each), O0 O1 (64 each); S of the next
 //             tile is computed while the softmax works on this one
-//   D = 128:  S0 S1, O0 O1 (128 each); P takes the first half of its S, so S
-//             of the next tile follows P V of this one, and the two query
-//             tiles fill each other's gaps
+//   D = 128:  two S of 64 keys (64 each) per query tile, O0 O1 (128 each); P
+//             takes the first half of its own S, and S of the next 64 keys is
+//             computed into the other one meanwhile
 //
 // Softmax: online, in base 2, held in fp32.  The reference m moves (and O is
 // rescaled) only when a tile's maximum passes it by more than 8, so weights
@@ -39,31 +46,40 @@
 namespace mbert {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 216;   // 4 x 72 + 8 x 216 = 12 x 168 (the launch budget)
-constexpr int kRegsControl = 72;
 constexpr int kMaskSlots = 4;
 
-// A unit's fixed work costs about four key tiles (the query load, the refill
-// of the pipeline, the end of the softmax, the output).
-using Split = CrossSplit<kThreads, kCrossBlockRows, kBlockN, 4, 4>;
+// Costs, by a fit over the CTAs' times: a key tile for both query tiles 2100
+// (D = 64) or 2900 clocks (D = 128), for one 1900 (D = 128); a unit's fixed work
+// (the end of the softmax, the output, the refill) 2600 to 4600.
+template <int D>
+using Split = CrossSplit<D == 64 ? 384 : 512, kCrossBlockRows, kBlockN, 6, 4, 10, 4>;
 
 template <int D>
 struct Layout {
-    static constexpr bool kAlias = D == 128;            // P lies in its S
+    static constexpr bool kSplitIssuers = D == 128;     // S and P V issued by different warps
+    static constexpr int kThreads = D == 64 ? 384 : 512;
+    // registers a thread: 4 x 72 + 8 x 216 = 12 x 168, 8 x 56 + 8 x 200 = 16 x 128
+    static constexpr int kRegsSoftmax = D == 64 ? 216 : 200;
+    static constexpr int kRegsControl = D == 64 ? 72 : 56;
+    static constexpr int kRecReaders = kSplitIssuers ? 13 : 11;  // issuers, eight softmax warps, the mask warp
+    static constexpr int kKeys = D == 64 ? 128 : 64;    // keys of a step (an S)
+    static constexpr int kSteps = kBlockN / kKeys;      // steps of a tile
     static constexpr int kHalves = D / 64;              // 64-column boxes of a tile
     static constexpr uint32_t kTile = kHalves * kTileBytes;
     static constexpr int kQSets = D == 64 ? 2 : 1;      // of two query tiles
     static constexpr int kStages = D == 64 ? 3 : 2;     // of K and of V
     static constexpr uint32_t kOffK = kQSets * 2 * kTile;
     static constexpr uint32_t kOffV = kOffK + kStages * kTile;
-    static constexpr uint32_t kOffBar = kOffV + kStages * kTile;
+    static constexpr uint32_t kOffOut = kOffV + kStages * kTile;    // 4 KB per softmax warp: 32 rows x 64 columns
+    static constexpr uint32_t kOffBar = kOffOut + 8 * 4096;
     static constexpr uint32_t kOffWords = kOffBar + 512;            // key bits, kMaskSlots x 4 words
-    static constexpr uint32_t kOffScratch = kOffWords + 16 * kMaskSlots;
-    static constexpr uint32_t kSmemBytes = kOffScratch + sizeof(Split::Scratch) + 1024;
-    static constexpr uint32_t col_s(int w) { return 128u * w; }
-    static constexpr uint32_t col_p(int w) { return kAlias ? 128u * w : 256u + 64u * w; }
-    static constexpr uint32_t col_o(int w) { return kAlias ? 256u + 128u * w : 384u + 64u * w; }
+    static constexpr uint32_t kOffRecs = kOffWords + 16 * kMaskSlots;
+    static constexpr uint32_t kOffScratch = kOffRecs + 48 * 4;
+    static constexpr uint32_t kSmemBytes = kOffScratch + sizeof(typename Split<D>::Scratch) + 1024;
+    // S and P of query tile w's step (D = 128: two buffers in turn), O
+    static constexpr uint32_t col_s(int w, uint32_t step) { return 128u * w + (D == 64 ? 0u : 64u * (step & 1)); }
+    static constexpr uint32_t col_p(int w, uint32_t step) { return D == 64 ? 256u + 64u * w : col_s(w, step); }
+    static constexpr uint32_t col_o(int w) { return D == 64 ? 384u + 64u * w : 256u + 128u * w; }
 };
 static_assert(Layout<64>::kSmemBytes <= 232448 && Layout<128>::kSmemBytes <= 232448, "shared memory");
 
@@ -75,14 +91,19 @@ constexpr int kBarKEmpty = 7;
 constexpr int kBarVFull = 10;
 constexpr int kBarVEmpty = 13;
 constexpr int kBarSFull = 16;     // + group (2)
-constexpr int kBarSEmpty = 18;    // D = 64 only
+constexpr int kBarSEmpty = 18;    // + group: S has been read (D = 64)
+constexpr int kBarSOdd = 18;      // + group: kBarSFull of the odd steps (D = 128)
 constexpr int kBarPFull = 20;
 constexpr int kBarODone = 22;
 constexpr int kBarOFree = 24;
 constexpr int kBarBitsFull = 26;  // + mask slot (4): a tile's key bits are in shared memory
 constexpr int kBarBitsEmpty = 30; // + mask slot: read by all 256 softmax threads
 constexpr int kBarVClean = 34;    // + mask slot: a tile's unseen V rows are zeros
-constexpr int kNumBars = 38;
+constexpr int kBarRecFull = 38;   // + record slot (4)
+constexpr int kBarRecEmpty = 42;  // + record slot
+constexpr int kBarPOdd = 46;      // + group: kBarPFull of the odd steps (D = 128)
+constexpr int kBarOOdd = 48;      // + group: kBarODone of the odd steps (D = 128)
+constexpr int kNumBars = 50;
 constexpr uint32_t kSlotInBars = 8 * kNumBars;                 // TMEM address
 static_assert(kSlotInBars + 4 <= 512, "barriers");
 
@@ -96,42 +117,97 @@ __device__ __forceinline__ constexpr uint32_t idesc(int M, int N, bool b_mn_majo
     return half ? d & ~((7u << 7) | (7u << 10)) : d;
 }
 
+// A segment (a unit and a run of its key tiles) as the producer hands it to
+// the other warps, through a ring in shared memory: finding it takes global
+// loads and 64-bit divisions, 3500 clocks that stood between the segments when
+// every warp did it for itself.
+struct alignas(16) Rec {
+    int q_row, q_len, q0, k_row, k_len;
+    int kb, ke, tiles;      // key tiles [kb, ke) of tiles; ke = 0: no more segments
+    int head, seq;
+    int parts;              // of a cut unit whose first part this is
+    int pad;
+};
+constexpr int kRecs = 4;
+
 struct Ctx {
     uint32_t base;          // 1024-aligned shared address
     uint32_t tmem;
     uint8_t *sbase;         // generic pointer to the same address
     const CrossArgs &a;
-    const Split &split;
     uint32_t bars;
 };
 
 __device__ __forceinline__ uint32_t bar(const Ctx &c, int i) { return c.bars + 8u * i; }
 
-// A tile whose keys are not all visible (or not known to be).
-__device__ __forceinline__ bool needs_mask(const Ctx &c, const Split::Seg &s, int k)
+// The CTA's segment sg (all lanes of a reading warp).  False: there is none.
+template <int D>
+__device__ __forceinline__ bool read_rec(const Ctx &c, uint32_t sg, int lane, Rec &r)
 {
-    return c.a.key_bits != nullptr || s.s.k_len - k * kBlockN < kBlockN;
+    const int slot = sg % kRecs;
+    if (!mbar_wait(bar(c, kBarRecFull + slot), (sg / kRecs) & 1, c.a.err))
+        return false;
+    r = reinterpret_cast<const Rec *>(c.sbase + Layout<D>::kOffRecs)[slot];
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(bar(c, kBarRecEmpty + slot));
+    return r.ke > 0;
+}
+
+// A tile whose keys are not all visible (or not known to be).
+__device__ __forceinline__ bool needs_mask(const Ctx &c, const Rec &s, int k)
+{
+    return c.a.key_bits != nullptr || s.k_len - k * kBlockN < kBlockN;
 }
 
 // The unit's second query tile holds rows.
-__device__ __forceinline__ bool second_tile(const Split::Seg &s) { return s.s.q_len - s.q0 > kBlockM; }
+__device__ __forceinline__ bool second_tile(const Rec &s) { return s.q_len - s.q0 > kBlockM; }
+
+// Steps of a segment: a last tile of at most 64 keys takes one step of 64.
+template <int D>
+__device__ __forceinline__ int seg_steps(const Rec &s)
+{
+    const int n = (s.ke - s.kb) * Layout<D>::kSteps;
+    return n - (Layout<D>::kSteps == 2 && s.k_len - (s.ke - 1) * kBlockN <= 64);
+}
 
 // ---------------------------------------------------------------- producer
 template <int D>
-__device__ void producer(const Ctx &c)
+__device__ void producer(const Ctx &c, const Split<D> &split)
 {
     using L = Layout<D>;
     int *err = c.a.err;
-    auto it = c.split.begin();
-    Split::Seg s;
+    auto it = split.begin();
+    typename Split<D>::Seg seg;
     uint32_t g = 0;          // key tiles issued by this CTA so far
-    for (uint32_t sg = 0; c.split.next(it, s); ++sg) {
+    for (uint32_t sg = 0;; ++sg) {
+        Rec s{};
+        if (split.next(it, seg)) {
+            s.q_row = seg.s.q_row;
+            s.q_len = seg.s.q_len;
+            s.q0 = seg.q0;
+            s.k_row = seg.s.k_row;
+            s.k_len = seg.s.k_len;
+            s.kb = seg.kb;
+            s.ke = seg.ke;
+            s.tiles = seg.s.tiles;
+            s.head = seg.head;
+            s.seq = seg.seq;
+            s.parts = seg.kb == 0 && seg.ke < seg.s.tiles ? split.parts(seg) : 0;
+        }
+        const int slot = sg % kRecs;
+        if (sg >= kRecs && !mbar_wait(bar(c, kBarRecEmpty + slot), (sg / kRecs - 1) & 1, err))
+            return;
+        reinterpret_cast<Rec *>(c.sbase + L::kOffRecs)[slot] = s;
+        mbar_arrive(bar(c, kBarRecFull + slot));
+        if (s.ke == 0)
+            return;
         const int qs = sg % L::kQSets;
         const bool two = second_tile(s);
         if (sg >= L::kQSets && !mbar_wait(bar(c, kBarQEmpty + qs), (sg / L::kQSets - 1) & 1, err))
             return;
         const int col_q = s.head * D, col_k = s.head / c.a.group * D;
-        const int qrow = s.s.q_row + s.q0;
+        const int qrow = s.q_row + s.q0;
         const uint32_t qdst = c.base + qs * 2 * L::kTile;
         mbar_arrive_expect_tx(bar(c, kBarQFull + qs), (two ? 2 : 1) * L::kTile);
         for (int w = 0; w < (two ? 2 : 1); ++w)
@@ -141,7 +217,7 @@ __device__ void producer(const Ctx &c)
         for (int k = s.kb; k < s.ke; ++k, ++g) {
             const int st = g % L::kStages;
             const uint32_t u = g / L::kStages;
-            const int krow = s.s.k_row + k * kBlockN;
+            const int krow = s.k_row + k * kBlockN;
             if (u > 0 && !mbar_wait(bar(c, kBarKEmpty + st), (u - 1) & 1, err))
                 return;
             mbar_arrive_expect_tx(bar(c, kBarKFull + st), L::kTile);
@@ -159,150 +235,220 @@ __device__ void producer(const Ctx &c)
 }
 
 // ---------------------------------------------------------------- MMA issuers
+// S of 64 (D = 128) or 128 keys from key `key0` of the stage.
 template <int D, bool kHalf>
-__device__ __forceinline__ void issue_s(const Ctx &c, int w, int qs, int st)
+__device__ __forceinline__ void issue_s(const Ctx &c, int w, int qs, int st, int key0, uint32_t step)
 {
     using L = Layout<D>;
-    constexpr uint32_t kIdesc = idesc(128, 128, false, kHalf);
+    constexpr uint32_t kIdesc = idesc(128, L::kKeys, false, kHalf);
     const uint32_t q = c.base + (qs * 2 + w) * L::kTile;
-    const uint32_t k = c.base + L::kOffK + st * L::kTile;
+    const uint32_t k = c.base + L::kOffK + st * L::kTile + 128 * key0;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * kTileBytes + 32 * (kk % 4);
-        mma_bf16_ss_warp(c.tmem + L::col_s(w), make_sdesc_sw128(q + off, 16, 1024),
+        mma_bf16_ss_warp(c.tmem + L::col_s(w, step), make_sdesc_sw128(q + off, 16, 1024),
                          make_sdesc_sw128(k + off, 16, 1024), kIdesc, kk > 0);
     }
 }
 
+// O += P V over the step's keys, all D columns per instruction.  V is the
+// MN-major operand: 64 columns (128 bytes) x 8 keys are one swizzle atom; atoms
+// follow each other by 1024 bytes along the keys (stride offset) and by a
+// 64-column box along the columns (leading offset).
 template <int D, bool kHalf>
-__device__ __forceinline__ void issue_o(const Ctx &c, int w, int st, bool accumulate)
+__device__ __forceinline__ void issue_o(const Ctx &c, int w, int st, int key0, uint32_t step, bool accumulate)
 {
     using L = Layout<D>;
-    // 64 columns of O per instruction: with P read from TMEM they run at the
-    // full rate
-    constexpr uint32_t kIdesc = idesc(128, 64, true, kHalf);
-    const uint32_t v = c.base + L::kOffV + st * L::kTile;
+    constexpr uint32_t kIdesc = idesc(128, D, true, kHalf);
+    const uint32_t v = c.base + L::kOffV + st * L::kTile + 128 * key0;
 #pragma unroll
-    for (int kk = 0; kk < kBlockN / 16; ++kk)
-#pragma unroll
-        for (int h = 0; h < L::kHalves; ++h)
-            mma_bf16_ts_warp(c.tmem + L::col_o(w) + 64 * h, c.tmem + L::col_p(w) + 8 * kk,
-                             make_sdesc_sw128(v + h * kTileBytes + 2048 * kk, 1024, 1024), kIdesc,
-                             (accumulate || kk > 0) ? 1u : 0u);
+    for (int kk = 0; kk < L::kKeys / 16; ++kk)
+        mma_bf16_ts_warp(c.tmem + L::col_o(w), c.tmem + L::col_p(w, step) + 8 * kk,
+                         make_sdesc_sw128(v + 2048 * kk, kTileBytes, 1024), kIdesc,
+                         (accumulate || kk > 0) ? 1u : 0u);
 }
 
-// A segment whose second query tile is empty: issuer 1 hands the ring slots
-// back as they fill (each phase only once it has begun).
-template <int D>
-__device__ bool pass_segment(const Ctx &c, const Split::Seg &s, int qs, uint32_t sg, uint32_t g0, int lane)
+// D = 64: the issuer of query tile w, S of a key tile and then P V of the one
+// before, while the softmax works on the former's predecessor.  `gw` counts the
+// steps of this query tile (its S, P and O barriers), `g` all tiles of the CTA
+// (the rings).  In a segment whose second query tile is empty, issuer 1 only
+// hands the ring slots back as they fill (each phase only once it has begun).
+template <bool kHalf>
+__device__ void so_issuer(const Ctx &c, int w, int lane)
 {
+    constexpr int D = 64;
     using L = Layout<D>;
     int *err = c.a.err;
-    if (!mbar_wait(bar(c, kBarQFull + qs), (sg / L::kQSets) & 1, err))
-        return false;
-    for (int t = 0; t < s.ke - s.kb; ++t) {
-        const uint32_t g = g0 + t;
-        const int st = g % L::kStages;
-        if (!mbar_wait(bar(c, kBarKFull + st), (g / L::kStages) & 1, err) ||
-            !mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
-            return false;
-        if (lane == 0) {
-            mbar_arrive(bar(c, kBarKEmpty + st));
-            mbar_arrive(bar(c, kBarVEmpty + st));
-        }
-        __syncwarp();
-    }
-    if (lane == 0)
-        mbar_arrive(bar(c, kBarQEmpty + qs));
-    __syncwarp();
-    return true;
-}
-
-// Issuer for query tile w.  `gw` counts the tiles of this query tile (its S,
-// P and O barriers), `g` all tiles of the CTA (the rings).
-template <int D, bool kHalf>
-__device__ void mma_issuer(const Ctx &c, int w, int lane)
-{
-    using L = Layout<D>;
-    int *err = c.a.err;
-    auto it = c.split.begin();
-    Split::Seg s;
+    Rec s;
     uint32_t g0 = 0, gw0 = 0, sw = 0, masked = 0;
-    for (uint32_t sg = 0; c.split.next(it, s); ++sg) {
+    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
         const int qs = sg % L::kQSets;
         const int n = s.ke - s.kb;
-        if (w == 1 && !second_tile(s)) {
-            if (!pass_segment<D>(c, s, qs, sg, g0, lane))
-                return;
-            for (int t = 0; t < n; ++t)
-                masked += needs_mask(c, s, s.kb + t);
-            g0 += n;
-            continue;
-        }
+        const bool mine = w == 0 || second_tile(s);
         if (!mbar_wait(bar(c, kBarQFull + qs), (sg / L::kQSets) & 1, err))
             return;
-        // P V of tile t
-        auto step_o = [&](int t) -> bool {
-            const uint32_t g = g0 + t, gw = gw0 + t;
-            const int st = g % L::kStages;
-            if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
-                return false;
-            if (needs_mask(c, s, s.kb + t)) {
-                if (!mbar_wait(bar(c, kBarVClean + masked % kMaskSlots), (masked / kMaskSlots) & 1, err))
-                    return false;
-                ++masked;
-            }
-            if (!mbar_wait(bar(c, kBarPFull + w), gw & 1, err))
-                return false;
-            if (t == 0 && sw > 0 && !mbar_wait(bar(c, kBarOFree + w), (sw - 1) & 1, err))
-                return false;
-            __syncwarp();
-            tc_fence_after();
-            issue_o<D, kHalf>(c, w, st, t > 0);
-            mma_commit_warp(bar(c, kBarODone + w));
-            mma_commit_warp(bar(c, kBarVEmpty + st));
-            return true;
-        };
-        for (int t = 0; t < n; ++t) {
-            const uint32_t g = g0 + t, gw = gw0 + t;
-            const int st = g % L::kStages;
-            if (!mbar_wait(bar(c, kBarKFull + st), (g / L::kStages) & 1, err))
-                return;
-            if constexpr (L::kAlias) {
-                // S takes the place of the last tile's P
-                if (gw > 0 && !mbar_wait(bar(c, kBarODone + w), (gw - 1) & 1, err))
+        for (int t = 0; t <= n; ++t) {
+            if (t < n) {
+                const uint32_t g = g0 + t, gw = gw0 + t;
+                const int st = g % L::kStages;
+                if (!mbar_wait(bar(c, kBarKFull + st), (g / L::kStages) & 1, err))
                     return;
-            } else {
-                if (gw > 0 && !mbar_wait(bar(c, kBarSEmpty + w), (gw - 1) & 1, err))
-                    return;
+                if (mine) {
+                    if (gw > 0 && !mbar_wait(bar(c, kBarSEmpty + w), (gw - 1) & 1, err))
+                        return;
+                    __syncwarp();
+                    tc_fence_after();
+                    issue_s<D, kHalf>(c, w, qs, st, 0, gw);
+                    mma_commit_warp(bar(c, kBarSFull + w));
+                    mma_commit_warp(bar(c, kBarKEmpty + st));
+                    if (t == n - 1)
+                        mma_commit_warp(bar(c, kBarQEmpty + qs));
+                } else if (lane == 0) {
+                    mbar_arrive(bar(c, kBarKEmpty + st));
+                    if (t == n - 1)
+                        mbar_arrive(bar(c, kBarQEmpty + qs));
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            tc_fence_after();
-            issue_s<D, kHalf>(c, w, qs, st);
-            mma_commit_warp(bar(c, kBarSFull + w));
-            mma_commit_warp(bar(c, kBarKEmpty + st));
-            if (t == n - 1)
-                mma_commit_warp(bar(c, kBarQEmpty + qs));
-            // D = 64: P V one tile behind, while the softmax works on tile t
-            if (L::kAlias ? !step_o(t) : (t > 0 && !step_o(t - 1)))
-                return;
+            if (t > 0) {
+                const uint32_t g = g0 + t - 1, gw = gw0 + t - 1;
+                const int st = g % L::kStages;
+                if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
+                    return;
+                if (needs_mask(c, s, s.kb + t - 1)) {
+                    if (mine &&
+                        !mbar_wait(bar(c, kBarVClean + masked % kMaskSlots), (masked / kMaskSlots) & 1, err))
+                        return;
+                    ++masked;
+                }
+                if (mine) {
+                    if (!mbar_wait(bar(c, kBarPFull + w), gw & 1, err))
+                        return;
+                    if (t == 1 && sw > 0 && !mbar_wait(bar(c, kBarOFree + w), (sw - 1) & 1, err))
+                        return;
+                    __syncwarp();
+                    tc_fence_after();
+                    issue_o<D, kHalf>(c, w, st, 0, gw, t > 1);
+                    mma_commit_warp(bar(c, kBarODone + w));
+                    mma_commit_warp(bar(c, kBarVEmpty + st));
+                } else if (lane == 0) {
+                    mbar_arrive(bar(c, kBarVEmpty + st));
+                }
+                __syncwarp();
+            }
         }
-        if (!L::kAlias && !step_o(n - 1))
-            return;
         g0 += n;
-        gw0 += n;
-        ++sw;
+        if (mine) {
+            gw0 += n;
+            ++sw;
+        }
+    }
+}
+
+// D = 128: issuer of query tile w's S.
+template <int D, bool kHalf>
+__device__ void s_issuer(const Ctx &c, int w, int lane)
+{
+    using L = Layout<D>;
+    int *err = c.a.err;
+    Rec s;
+    uint32_t g = 0, gw = 0;
+    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
+        const int qs = sg % L::kQSets;
+        const int n = seg_steps<D>(s);
+        const bool mine = w == 0 || second_tile(s);
+        if (!mbar_wait(bar(c, kBarQFull + qs), (sg / L::kQSets) & 1, err))
+            return;
+        for (int j = 0; j < n; ++j) {
+            const int st = g % L::kStages, sub = j % L::kSteps;
+            const bool last_sub = sub == L::kSteps - 1 || j == n - 1;
+            if (sub == 0 && !mbar_wait(bar(c, kBarKFull + st), (g / L::kStages) & 1, err))
+                return;
+            g += last_sub;
+            if (!mine) {
+                if (lane == 0 && last_sub)
+                    mbar_arrive(bar(c, kBarKEmpty + st));
+                __syncwarp();
+                continue;
+            }
+            // this buffer's last P has been multiplied
+            if (gw > 1 && !mbar_wait(bar(c, (gw & 1 ? kBarOOdd : kBarODone) + w), ((gw >> 1) - 1) & 1, err))
+                return;
+            __syncwarp();
+            tc_fence_after();
+            issue_s<D, kHalf>(c, w, qs, st, sub * L::kKeys, gw);
+            mma_commit_warp(bar(c, (gw & 1 ? kBarSOdd : kBarSFull) + w));
+            if (last_sub)
+                mma_commit_warp(bar(c, kBarKEmpty + st));
+            if (j == n - 1)
+                mma_commit_warp(bar(c, kBarQEmpty + qs));
+            ++gw;
+        }
+        if (!mine) {
+            if (lane == 0)
+                mbar_arrive(bar(c, kBarQEmpty + qs));
+            __syncwarp();
+        }
+    }
+}
+
+// D = 128: issuer of query tile w's O += P V.
+template <int D, bool kHalf>
+__device__ void o_issuer(const Ctx &c, int w, int lane)
+{
+    using L = Layout<D>;
+    int *err = c.a.err;
+    Rec s;
+    uint32_t g = 0, gw = 0, sw = 0, masked = 0;
+    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
+        const int n = seg_steps<D>(s);
+        const bool mine = w == 0 || second_tile(s);
+        for (int j = 0; j < n; ++j) {
+            const int st = g % L::kStages, sub = j % L::kSteps;
+            const bool last_sub = sub == L::kSteps - 1 || j == n - 1;
+            if (sub == 0) {
+                if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
+                    return;
+                if (needs_mask(c, s, s.kb + j / L::kSteps)) {
+                    if (mine &&
+                        !mbar_wait(bar(c, kBarVClean + masked % kMaskSlots), (masked / kMaskSlots) & 1, err))
+                        return;
+                    ++masked;
+                }
+            }
+            g += last_sub;
+            if (!mine) {
+                if (lane == 0 && last_sub)
+                    mbar_arrive(bar(c, kBarVEmpty + st));
+                __syncwarp();
+                continue;
+            }
+            // one barrier per P buffer: the softmax may finish two steps, whose S
+            // are both there, before this wait
+            if (!mbar_wait(bar(c, (gw & 1 ? kBarPOdd : kBarPFull) + w), gw >> 1 & 1, err))
+                return;
+            if (j == 0 && sw > 0 && !mbar_wait(bar(c, kBarOFree + w), (sw - 1) & 1, err))
+                return;
+            __syncwarp();
+            tc_fence_after();
+            issue_o<D, kHalf>(c, w, st, sub * L::kKeys, gw, j > 0);
+            mma_commit_warp(bar(c, (gw & 1 ? kBarOOdd : kBarODone) + w));
+            if (last_sub)
+                mma_commit_warp(bar(c, kBarVEmpty + st));
+            ++gw;
+        }
+        sw += mine;
     }
 }
 
 // ---------------------------------------------------------------- masks
 // The visible keys of tile k as 4 words.
-__device__ __forceinline__ uint32_t tile_word(const Ctx &c, const Split::Seg &s, int k, int i)
+__device__ __forceinline__ uint32_t tile_word(const Ctx &c, const Rec &s, int k, int i)
 {
-    const int left = s.s.k_len - k * kBlockN - 32 * i;
+    const int left = s.k_len - k * kBlockN - 32 * i;
     uint32_t w = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
     if (w && c.a.key_bits)
-        w &= __ldg(c.a.key_bits + key_bit_word(s.s.k_row, s.seq) + 4 * k + i);
+        w &= __ldg(c.a.key_bits + key_bit_word(s.k_row, s.seq) + 4 * k + i);
     return w;
 }
 
@@ -311,10 +457,9 @@ __device__ void mask_stager(const Ctx &c, int lane)
 {
     using L = Layout<D>;
     int *err = c.a.err;
-    auto it = c.split.begin();
-    Split::Seg s;
+    Rec s;
     uint32_t g = 0, masked = 0;
-    for (uint32_t sg = 0; c.split.next(it, s); ++sg) {
+    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
         for (int k = s.kb; k < s.ke; ++k, ++g) {
             const int st = g % L::kStages;
             // every tile is waited for and handed back, seen or not, so that
@@ -380,26 +525,62 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return r;
 }
 
+// Two weights 2^(x scale - m): added to a packed row sum, packed to 16 bits.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t weights(float x0, float x1, uint64_t sc2, uint64_t nm2, uint64_t &acc)
+{
+    uint32_t pk;
+    if constexpr (kHalf)
+        asm("{\n\t.reg .b64 y, pp;\n\t.reg .f32 y0, y1, p0, p1;\n\t"
+            "mov.b64 y, {%2, %3};\n\t"
+            "fma.rn.f32x2 y, y, %4, %5;\n\t"
+            "mov.b64 {y0, y1}, y;\n\t"
+            "ex2.approx.ftz.f32 p0, y0;\n\t"
+            "ex2.approx.ftz.f32 p1, y1;\n\t"
+            "mov.b64 pp, {p0, p1};\n\t"
+            "add.f32x2 %1, %1, pp;\n\t"
+            "cvt.rn.f16x2.f32 %0, p1, p0;\n\t}"
+            : "=r"(pk), "+l"(acc)
+            : "f"(x0), "f"(x1), "l"(sc2), "l"(nm2));
+    else
+        asm("{\n\t.reg .b64 y, pp;\n\t.reg .f32 y0, y1, p0, p1;\n\t"
+            "mov.b64 y, {%2, %3};\n\t"
+            "fma.rn.f32x2 y, y, %4, %5;\n\t"
+            "mov.b64 {y0, y1}, y;\n\t"
+            "ex2.approx.ftz.f32 p0, y0;\n\t"
+            "ex2.approx.ftz.f32 p1, y1;\n\t"
+            "mov.b64 pp, {p0, p1};\n\t"
+            "add.f32x2 %1, %1, pp;\n\t"
+            "cvt.rn.bf16x2.f32 %0, p1, p0;\n\t}"
+            : "=r"(pk), "+l"(acc)
+            : "f"(x0), "f"(x1), "l"(sc2), "l"(nm2));
+    return pk;
+}
+
 template <int D, bool kHalf>
 __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, int cta)
 {
     using L = Layout<D>;
+    constexpr int kKeys = L::kKeys;
     constexpr float kLift = kHalf ? 7.f : 0.f;        // weights times 2^7 in fp16
     int *err = c.a.err;
     const uint32_t lane_off = static_cast<uint32_t>(32 * warp_in_group) << 16;
-    const uint32_t tS = c.tmem + L::col_s(w) + lane_off;
-    const uint32_t tP = c.tmem + L::col_p(w) + lane_off;
     const uint32_t tO = c.tmem + L::col_o(w) + lane_off;
     const int rr = kBlockM * w + 32 * warp_in_group + lane;      // row within the unit
     const float scale = c.a.scale_log2;
-    auto it = c.split.begin();
-    Split::Seg s;
+    // step's P V has completed.  (D = 128: S of a step stands for the P V two
+    // steps before, that is for the last phase of the same barrier.)
+    auto wait_o = [&](uint32_t step) -> bool {
+        return D == 64 ? mbar_wait(bar(c, kBarODone + w), step & 1, err)
+                       : mbar_wait(bar(c, step & 1 ? kBarOOdd + w : kBarODone + w), step >> 1 & 1, err);
+    };
+    Rec s;
     uint32_t gw = 0, masked = 0;
-    while (c.split.next(it, s)) {
-        const int n = s.ke - s.kb;
+    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
+        const int n = seg_steps<D>(s);
         if (w == 1 && !second_tile(s)) {
             // nothing to do but hand the key bits on
-            for (int t = 0; t < n; ++t) {
+            for (int t = 0; t < s.ke - s.kb; ++t) {
                 if (!needs_mask(c, s, s.kb + t))
                     continue;
                 if (c.a.key_bits) {
@@ -414,59 +595,69 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
         }
         float m = -INFINITY;    // reference (scaled, base 2)
         float l = 0.f;          // sum of exp2(score - m + kLift)
-        for (int t = 0; t < n; ++t, ++gw) {
-            if (!mbar_wait(bar(c, kBarSFull + w), gw & 1, err))
+        uint32_t bits[4] = {0u, 0u, 0u, 0u};   // the tile's key bits
+        for (int j = 0; j < n; ++j, ++gw) {
+            const int sub = j % L::kSteps;
+            const bool last_sub = sub == L::kSteps - 1 || j == n - 1;
+            if (!(D == 64 ? mbar_wait(bar(c, kBarSFull + w), gw & 1, err)
+                          : mbar_wait(bar(c, gw & 1 ? kBarSOdd + w : kBarSFull + w), gw >> 1 & 1, err)))
                 return;
             __syncwarp();
             tc_fence_after();
-            float sc[kBlockN];
+            float sc[kKeys];
             {
-                uint32_t r0[32], r1[32], r2[32], r3[32];
-                tmem_ld32(tS, r0);
-                tmem_ld32(tS + 32, r1);
-                tmem_ld32(tS + 64, r2);
-                tmem_ld32(tS + 96, r3);
+                const uint32_t tS = c.tmem + L::col_s(w, gw) + lane_off;
+                uint32_t r[kKeys / 32][32];
+#pragma unroll
+                for (int q = 0; q < kKeys / 32; ++q)
+                    tmem_ld32(tS + 32 * q, r[q]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    sc[i] = __uint_as_float(r0[i]);
-                    sc[32 + i] = __uint_as_float(r1[i]);
-                    sc[64 + i] = __uint_as_float(r2[i]);
-                    sc[96 + i] = __uint_as_float(r3[i]);
-                }
+                for (int q = 0; q < kKeys / 32; ++q)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        sc[32 * q + i] = __uint_as_float(r[q][i]);
             }
             tc_fence_before();
-            if constexpr (!L::kAlias)
+            if constexpr (D == 64)
                 mbar_arrive(bar(c, kBarSEmpty + w));   // S may be overwritten now
 
-            if (needs_mask(c, s, s.kb + t)) {
+            const int kt = s.kb + j / L::kSteps;
+            if (needs_mask(c, s, kt)) {
                 if (c.a.key_bits) {
-                    const uint32_t slot = masked % kMaskSlots;
-                    if (!mbar_wait(bar(c, kBarBitsFull + slot), (masked / kMaskSlots) & 1, err))
-                        return;
-                    const uint4 b = reinterpret_cast<const uint4 *>(c.sbase + L::kOffWords)[slot];
-                    mbar_arrive(bar(c, kBarBitsEmpty + slot));
-                    if ((b.x & b.y & b.z & b.w) != 0xffffffffu) {
+                    if (sub == 0) {
+                        const uint32_t slot = masked % kMaskSlots;
+                        if (!mbar_wait(bar(c, kBarBitsFull + slot), (masked / kMaskSlots) & 1, err))
+                            return;
+                        const uint4 b = reinterpret_cast<const uint4 *>(c.sbase + L::kOffWords)[slot];
+                        bits[0] = b.x, bits[1] = b.y, bits[2] = b.z, bits[3] = b.w;
+                        mbar_arrive(bar(c, kBarBitsEmpty + slot));
+                    }
+                    uint32_t all = 0xffffffffu;
+                    uint32_t mine[kKeys / 32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (!(b.x >> i & 1))
-                                sc[i] = -INFINITY;
-                            if (!(b.y >> i & 1))
-                                sc[32 + i] = -INFINITY;
-                            if (!(b.z >> i & 1))
-                                sc[64 + i] = -INFINITY;
-                            if (!(b.w >> i & 1))
-                                sc[96 + i] = -INFINITY;
-                        }
+                    for (int q = 0; q < kKeys / 32; ++q) {
+                        mine[q] = L::kSteps == 2 && sub ? bits[q + 2] : bits[q];
+                        all &= mine[q];
+                    }
+                    if (all != 0xffffffffu) {
+#pragma unroll
+                        for (int q = 0; q < kKeys / 32; ++q)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(mine[q] >> i & 1))
+                                    sc[32 * q + i] = -INFINITY;
                     }
                 } else {
-                    const int kvalid = s.s.k_len - (s.kb + t) * kBlockN;
+                    const int kvalid = s.k_len - kt * kBlockN - sub * kKeys;
+                    if (kvalid < kKeys) {
 #pragma unroll
-                    for (int i = 0; i < kBlockN; ++i)
-                        if (i >= kvalid)
-                            sc[i] = -INFINITY;
+                        for (int i = 0; i < kKeys; ++i)
+                            if (i >= kvalid)
+                                sc[i] = -INFINITY;
+                    }
                 }
-                ++masked;
+                masked += last_sub;
             }
             // row maximum: 8 independent chains
             float mp[8];
@@ -474,7 +665,7 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
             for (int k = 0; k < 8; ++k)
                 mp[k] = fmaxf(sc[k], sc[8 + k]);
 #pragma unroll
-            for (int i = 16; i < kBlockN; i += 16)
+            for (int i = 16; i < kKeys; i += 16)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     mp[k] = fmax3(mp[k], sc[i + k], sc[i + 8 + k]);
@@ -488,36 +679,12 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
 
             // p = 2^(s scale - m), packed to 16-bit pairs; the row sum in 4
             // packed fp32x2 accumulators
-            uint32_t pk[kBlockN / 2];
+            uint32_t pk[kKeys / 2];
             uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
             const uint64_t sc2 = f2(scale, scale), nm2 = f2(neg, neg);
 #pragma unroll
-            for (int i = 0; i < kBlockN / 2; ++i) {
-                if constexpr (kHalf)
-                    asm("{\n\t.reg .b64 y, pp;\n\t.reg .f32 y0, y1, p0, p1;\n\t"
-                        "mov.b64 y, {%2, %3};\n\t"
-                        "fma.rn.f32x2 y, y, %4, %5;\n\t"
-                        "mov.b64 {y0, y1}, y;\n\t"
-                        "ex2.approx.ftz.f32 p0, y0;\n\t"
-                        "ex2.approx.ftz.f32 p1, y1;\n\t"
-                        "mov.b64 pp, {p0, p1};\n\t"
-                        "add.f32x2 %1, %1, pp;\n\t"
-                        "cvt.rn.f16x2.f32 %0, p1, p0;\n\t}"
-                        : "=r"(pk[i]), "+l"(acc2[i & 3])
-                        : "f"(sc[2 * i]), "f"(sc[2 * i + 1]), "l"(sc2), "l"(nm2));
-                else
-                    asm("{\n\t.reg .b64 y, pp;\n\t.reg .f32 y0, y1, p0, p1;\n\t"
-                        "mov.b64 y, {%2, %3};\n\t"
-                        "fma.rn.f32x2 y, y, %4, %5;\n\t"
-                        "mov.b64 {y0, y1}, y;\n\t"
-                        "ex2.approx.ftz.f32 p0, y0;\n\t"
-                        "ex2.approx.ftz.f32 p1, y1;\n\t"
-                        "mov.b64 pp, {p0, p1};\n\t"
-                        "add.f32x2 %1, %1, pp;\n\t"
-                        "cvt.rn.bf16x2.f32 %0, p1, p0;\n\t}"
-                        : "=r"(pk[i]), "+l"(acc2[i & 3])
-                        : "f"(sc[2 * i]), "f"(sc[2 * i + 1]), "l"(sc2), "l"(nm2));
-            }
+            for (int i = 0; i < kKeys / 2; ++i)
+                pk[i] = weights<kHalf>(sc[2 * i], sc[2 * i + 1], sc2, nm2, acc2[i & 3]);
             uint64_t accs = acc2[0];
             asm("add.f32x2 %0, %0, %1;" : "+l"(accs) : "l"(acc2[1]));
             asm("add.f32x2 %0, %0, %1;" : "+l"(accs) : "l"(acc2[2]));
@@ -525,16 +692,17 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
             float acc0, acc1;
             f2_split(accs, acc0, acc1);
 
-            if (t > 0) {
-                // P and O are free once the last P V has completed (D = 128:
-                // S of this tile was only issued after that)
-                if constexpr (!L::kAlias) {
-                    if (!mbar_wait(bar(c, kBarODone + w), (gw - 1) & 1, err))
+            if (j > 0) {
+                // O under the new reference, once the last P V has completed
+                // (D = 64: which also frees P)
+                const bool any = __any_sync(0xffffffffu, need);
+                if (D == 64 || any) {
+                    if (!wait_o(gw - 1))
                         return;
                     __syncwarp();
                     tc_fence_after();
                 }
-                if (__any_sync(0xffffffffu, need)) {
+                if (any) {
 #pragma unroll
                     for (int h = 0; h < D / 32; ++h) {
                         uint32_t o[32];
@@ -549,24 +717,31 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
             }
             l = l * alpha + (acc0 + acc1);
             m = mn;
-            tmem_st64(tP, pk);
+            const uint32_t tP = c.tmem + L::col_p(w, gw) + lane_off;
+            if constexpr (D == 64)
+                tmem_st64(tP, pk);
+            else
+                tmem_st32(tP, pk);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(bar(c, kBarPFull + w));
+            mbar_arrive(bar(c, D == 128 && gw & 1 ? kBarPOdd + w : kBarPFull + w));
         }
 
         // ---- end of the segment: O / l to the output, or the state to this
         // CTA's part slot
-        if (!mbar_wait(bar(c, kBarODone + w), (gw - 1) & 1, err))
+        if (!wait_o(gw - 1))
             return;
         __syncwarp();
         tc_fence_after();
-        const bool whole = s.ke - s.kb == s.s.tiles;
-        const bool in = s.q0 + rr < s.s.q_len;
+        const bool whole = s.ke - s.kb == s.tiles;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         float *part = c.a.parts + (2ll * cta + (s.kb == 0)) * cross_slot_floats(kCrossBlockRows, D);
+        // this warp's rows of the output, those that the sequence has
+        const int warp_row = kBlockM * w + 32 * warp_in_group;
+        const int warp_rows = min(32, s.q_len - s.q0 - warp_row);
         uint16_t *out = static_cast<uint16_t *>(c.a.out) +
-                        (static_cast<long long>(s.s.q_row) + s.q0 + rr) * c.a.out_row + s.head * D;
+                        (static_cast<long long>(s.q_row) + s.q0 + warp_row) * c.a.out_row + s.head * D;
+        uint8_t *stage = c.sbase + L::kOffOut + (4 * w + warp_in_group) * 4096;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
             float o[64];
@@ -586,15 +761,25 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                 mbar_arrive(bar(c, kBarOFree + w));   // the next segment may reset O
             }
             if (whole) {
-                if (in) {
+                // through shared memory, so that a store instruction writes
+                // whole lines of 4 rows and not 16 bytes of 32 (chunk j of row
+                // r at j ^ (r & 7): no bank conflicts either way)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<uint4 *>(out)[8 * h + i] =
-                            make_uint4(pack2<kHalf>(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                       pack2<kHalf>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                       pack2<kHalf>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                       pack2<kHalf>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4 *>(stage + 128 * lane + 16 * (i ^ (lane & 7))) =
+                        make_uint4(pack2<kHalf>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                   pack2<kHalf>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                   pack2<kHalf>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                   pack2<kHalf>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 4 * i + lane / 8, part = lane % 8;
+                    if (row < warp_rows)
+                        *reinterpret_cast<uint4 *>(out + row * c.a.out_row + 64 * h + 8 * part) =
+                            *reinterpret_cast<const uint4 *>(stage + 128 * row + 16 * (part ^ (row & 7)));
                 }
+                __syncwarp();
             } else {
                 // [D/4][256 rows] float4: neighbouring rows side by side
 #pragma unroll
@@ -607,18 +792,18 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
             reinterpret_cast<float2 *>(part + kCrossBlockRows * D)[rr] = make_float2(m, l);
         if (!whole && s.kb == 0 && rr == 0) {
             CrossRecord rec;
-            rec.row0 = static_cast<long long>(s.s.q_row) + s.q0;
-            rec.rows = min(kCrossBlockRows, s.s.q_len - s.q0);
+            rec.row0 = static_cast<long long>(s.q_row) + s.q0;
+            rec.rows = min(kCrossBlockRows, s.q_len - s.q0);
             rec.head0 = s.head;
             rec.group = 1;
-            rec.parts = c.split.parts(s);
+            rec.parts = s.parts;
             c.a.records[cta] = rec;
         }
     }
 }
 
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Layout<D>::kThreads, 1)
 attn_cross_kernel(const __grid_constant__ CrossArgs a)
 {
     using L = Layout<D>;
@@ -632,11 +817,11 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
 
     if (threadIdx.x == 0)
         a.records[cta].parts = 0;
-    Split split(a, a.heads);
-    // at least 6 cost units (2 tiles of one unit) per CTA
-    const bool work = split.find(*reinterpret_cast<Split::Scratch *>(sbase + L::kOffScratch), gridDim.x, 6);
+    Split<D> split(a, a.heads);
+    // two tiles and a unit's fixed work per CTA at least
+    const bool work = split.find(*reinterpret_cast<typename Split<D>::Scratch *>(sbase + L::kOffScratch), gridDim.x, 22);
     if (work) {
-        Ctx c{base, 0u, sbase, a, split, base + L::kOffBar};
+        Ctx c{base, 0u, sbase, a, base + L::kOffBar};
         const int warp = threadIdx.x >> 5;
         const int lane = threadIdx.x & 31;
         if (threadIdx.x == 0) {
@@ -655,10 +840,16 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
             }
             for (int w = 0; w < 2; ++w) {
                 mbar_init(bar(c, kBarSFull + w), 1);
-                mbar_init(bar(c, kBarSEmpty + w), kBlockM);
+                mbar_init(bar(c, kBarSEmpty + w), D == 64 ? kBlockM : 1);   // (kBarSOdd: one commit)
                 mbar_init(bar(c, kBarPFull + w), kBlockM);
+                mbar_init(bar(c, kBarPOdd + w), kBlockM);
                 mbar_init(bar(c, kBarODone + w), 1);
+                mbar_init(bar(c, kBarOOdd + w), 1);
                 mbar_init(bar(c, kBarOFree + w), kBlockM);
+            }
+            for (int i = 0; i < kRecs; ++i) {
+                mbar_init(bar(c, kBarRecFull + i), 1);
+                mbar_init(bar(c, kBarRecEmpty + i), L::kRecReaders);
             }
             for (int i = 0; i < kMaskSlots; ++i) {
                 mbar_init(bar(c, kBarBitsFull + i), 1);
@@ -677,18 +868,24 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
         c.tmem = *slot;
 
         if (warp >= 8) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsControl));
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(L::kRegsControl));
             if (warp == 8) {
                 if (lane == 0)
-                    producer<D>(c);
-            } else if (warp == 9 || warp == 10) {
-                mma_issuer<D, kHalf>(c, warp - 9, lane);
-            } else {
+                    producer<D>(c, split);
+            } else if (warp == 9) {
                 mask_stager<D>(c, lane);
+            } else if (warp == 10 || warp == 11) {
+                if constexpr (L::kSplitIssuers)
+                    s_issuer<D, kHalf>(c, warp - 10, lane);
+                else
+                    so_issuer<kHalf>(c, warp - 10, lane);
+            } else if (warp == 12 || warp == 13) {
+                if constexpr (L::kSplitIssuers)
+                    o_issuer<D, kHalf>(c, warp - 12, lane);
             }
             __syncwarp();
         } else {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegsSoftmax));
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(L::kRegsSoftmax));
             softmax_group<D, kHalf>(c, warp >> 2, warp & 3, lane, cta);
             __syncwarp();
         }
@@ -710,7 +907,7 @@ cudaError_t launch(const CrossArgs &a, int ctas, cudaStream_t stream)
     cudaError_t e = smem_opt_in(smem_once, attn_cross_kernel<D, kHalf>, Layout<D>::kSmemBytes);
     if (e != cudaSuccess)
         return e;
-    return launch_chained(attn_cross_kernel<D, kHalf>, dim3(ctas), dim3(kThreads), Layout<D>::kSmemBytes, stream, a);
+    return launch_chained(attn_cross_kernel<D, kHalf>, dim3(ctas), dim3(Layout<D>::kThreads), Layout<D>::kSmemBytes, stream, a);
 }
 
 }  // namespace

@@ -29,7 +29,7 @@ constexpr uint32_t kBoxBytes = kTileKeys * 128;       // 64 keys x 64 columns
 
 // A unit's fixed work (the query rows, joining four states, the output) costs
 // about two tiles; units of up to 8 tiles (512 keys) are not cut.
-using Split = CrossSplit<kThreads, 0, kTileKeys, 2, 8>;
+using Split = CrossSplit<kThreads, 0, kTileKeys, 1, 1, 2, 8>;
 
 template <int D>
 struct Layout {

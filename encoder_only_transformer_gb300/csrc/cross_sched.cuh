@@ -2,9 +2,10 @@
 //
 // A unit is one (sequence, head, block of query rows); it takes tiles(s) key
 // tiles.  All units stand one after the other on a line of costs, in order of
-// sequence, head, block: a unit takes tiles + kAlpha of it (kAlpha for its
-// fixed work: the query load, the end of its softmax, its output).  CTA c of n
-// owns the tiles whose place lies in [c X / n, (c + 1) X / n), X the line's
+// sequence, head, block: a unit takes kFull for each tile (kHalf where only
+// half of its block holds rows: the last block of a sequence) and kAlpha for
+// its fixed work (the query load, the end of its softmax, its output).  CTA c
+// of n owns the tiles that begin in [c X / n, (c + 1) X / n), X the line's
 // length; so every CTA gets the same cost whatever the lengths of the
 // sequences, and a long unit among few is cut between many CTAs.  A border
 // that falls into a unit of kSnap tiles or fewer moves to that unit's start:
@@ -20,9 +21,10 @@
 namespace mbert {
 
 // kBlockQ: query rows of a unit (0: all of a sequence's); kTile: keys of a tile.
-template <int kThreads, int kBlockQ_, int kTile_, int kAlpha_, int kSnap_>
+template <int kThreads, int kBlockQ_, int kTile_, int kFull_, int kHalf_, int kAlpha_, int kSnap_>
 struct CrossSplit {
-    static constexpr int kBlockQ = kBlockQ_, kTile = kTile_, kAlpha = kAlpha_, kSnap = kSnap_;
+    static constexpr int kBlockQ = kBlockQ_, kTile = kTile_, kSnap = kSnap_;
+    static constexpr int kFull = kFull_, kHalf = kHalf_, kAlpha = kAlpha_;
     static constexpr int kWarps = kThreads / 32;
 
     struct Scratch {
@@ -31,12 +33,38 @@ struct CrossSplit {
         int seq[2];
     };
 
-    // What a sequence needs: rows, tiles and units.
+    // What a sequence needs: rows, tiles, blocks of query rows.
     struct Seq {
-        int q_row, q_len, k_row, k_all, k_len, tiles, blocks;   // k_len: up to the last visible key
-        long long units;
-        __device__ __forceinline__ long long cost() const { return units * (tiles + kAlpha); }
+        int q_row, q_len, k_row, k_all, k_len, tiles;   // k_len: up to the last visible key
+        int whole;              // blocks of cost kFull a tile
+        int half;               // 1: the last block costs kHalf a tile
+        // costs of a whole block, of one head, of the sequence
+        __device__ __forceinline__ long long block() const { return static_cast<long long>(tiles) * kFull + kAlpha; }
+        __device__ __forceinline__ long long head() const
+        {
+            return whole * block() + half * (static_cast<long long>(tiles) * kHalf + kAlpha);
+        }
     };
+
+    // Where a place x of a sequence lies: its unit, and that unit's start.
+    struct Place {
+        int head, b;            // head, block
+        int per;                // cost of a tile
+        long long xa, end;      // the unit's start and the next one's
+    };
+    __device__ __forceinline__ Place place(const Seq &q, long long base, long long x) const
+    {
+        const long long ch = q.head(), cb = q.block();
+        Place p;
+        p.head = static_cast<int>((x - base) / ch);
+        const long long h0 = base + p.head * ch;
+        const long long b = (x - h0) / cb;
+        p.b = b < q.whole ? static_cast<int>(b) : q.whole;
+        p.per = p.b < q.whole ? kFull : kHalf;
+        p.xa = h0 + p.b * cb;
+        p.end = p.b < q.whole ? p.xa + cb : h0 + ch;
+        return p;
+    }
 
     const CrossArgs &a;
     int unit_heads;         // heads that units are made for
@@ -67,10 +95,18 @@ struct CrossSplit {
         }
         q.k_len = a.key_len ? min(q.k_all, __ldg(a.key_len + s)) : q.k_all;
         q.tiles = max(1, (q.k_len + kTile - 1) / kTile);
-        q.blocks = kBlockQ ? (q.q_len + (kBlockQ ? kBlockQ : 1) - 1) / (kBlockQ ? kBlockQ : 1) : (q.q_len > 0);
-        q.units = static_cast<long long>(unit_heads) * q.blocks;
+        if constexpr (kBlockQ > 0) {
+            const int rest = q.q_len % kBlockQ;
+            q.half = kHalf != kFull && rest > 0 && rest <= kBlockQ / 2;
+            q.whole = q.q_len / kBlockQ + (rest > 0 && !q.half);
+        } else {
+            q.half = 0;
+            q.whole = q.q_len > 0;
+        }
         return q;
     }
+
+    __device__ __forceinline__ long long cost(const Seq &q) const { return unit_heads * q.head(); }
 
     __device__ __forceinline__ long long border(int c) const
     {
@@ -83,8 +119,9 @@ struct CrossSplit {
         return static_cast<int>(((x + 1) * ctas - 1) / total);
     }
 
-    // Every thread of the block.  False: nothing to do for this CTA (or the
-    // offsets are bad, then *a.err says so and no CTA does anything).
+    // Every thread of the block.  min_cost: of a CTA, at least kFull, so that
+    // every CTA inside a unit's tiles has one.  False: nothing to do for this
+    // CTA (or the offsets are bad, then *a.err says so and no CTA does anything).
     __device__ bool find(Scratch &sm, int max_ctas, int min_cost)
     {
         const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -99,7 +136,7 @@ struct CrossSplit {
             else if (q.q_len > a.max_q)
                 bad |= kErrTooLong;
             else
-                sum += q.cost();
+                sum += cost(q);
         }
         if (tid == 0 && ((a.cu_q && a.cu_q[0] != 0) || (a.cu_k && a.cu_k[0] != 0)))
             bad |= kErrBadCu;
@@ -122,8 +159,8 @@ struct CrossSplit {
             total += sm.warp[w];
         if (total == 0)
             return false;
-        const long long want = (total + min_cost - 1) / min_cost;
-        ctas = want < max_ctas ? static_cast<int>(want) : max_ctas;
+        const long long want = total / min_cost;
+        ctas = want < 1 ? 1 : want < max_ctas ? static_cast<int>(want) : max_ctas;
         if (static_cast<int>(blockIdx.x) >= ctas)
             return false;
         lo = border(blockIdx.x);
@@ -132,7 +169,7 @@ struct CrossSplit {
         long long carry = 0;
         for (int s0 = 0; s0 < a.n_seqs; s0 += kThreads) {
             const int s = s0 + tid;
-            const long long v = s < a.n_seqs ? load(s).cost() : 0;
+            const long long v = s < a.n_seqs ? cost(load(s)) : 0;
             long long incl = v;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -178,7 +215,7 @@ struct CrossSplit {
         const Seq q = load(s);
         if (q.tiles > kSnap)
             return x;
-        return x - (x - base) % (q.tiles + kAlpha);
+        return place(q, base, x).xa;
     }
 
     // A run of key tiles [kb, ke) of one unit.
@@ -186,6 +223,7 @@ struct CrossSplit {
         Seq s;
         int seq, head, q0;
         int kb, ke;
+        int per;            // cost of a tile
         long long xa;       // place of the unit's first tile
     };
 
@@ -209,31 +247,27 @@ struct CrossSplit {
     __device__ bool next(Iter &it, Seg &g) const
     {
         while (it.x < hi) {
-            const long long d = it.x - it.base, c = it.s.cost();
-            if (d >= c) {
-                it.base += c;
+            if (it.x - it.base >= cost(it.s)) {
+                it.base += cost(it.s);
                 if (++it.seq >= a.n_seqs)
                     return false;
                 it.s = load(it.seq);
                 continue;
             }
-            const int per = it.s.tiles + kAlpha;
-            const long long u = d / per;
-            const int r = static_cast<int>(d - u * per);
-            const long long after = it.base + (u + 1) * per;
-            if (r >= it.s.tiles) {
-                it.x = after;
-                continue;
-            }
-            const long long left = hi - it.x;
+            const Place p = place(it.s, it.base, it.x);
+            const int kb = static_cast<int>((it.x - p.xa + p.per - 1) / p.per);
+            const long long cut = (hi - p.xa + p.per - 1) / p.per;
+            g.ke = cut < it.s.tiles ? static_cast<int>(cut) : it.s.tiles;
+            it.x = p.end;
+            if (kb >= g.ke)
+                continue;       // x lies behind the unit's tiles, or hi before the next one
             g.s = it.s;
             g.seq = it.seq;
-            g.head = static_cast<int>(u / it.s.blocks);
-            g.q0 = static_cast<int>(u % it.s.blocks) * kBlockQ;
-            g.kb = r;
-            g.ke = left < it.s.tiles - r ? static_cast<int>(r + left) : it.s.tiles;
-            g.xa = it.base + u * per;
-            it.x = g.ke < it.s.tiles ? hi : after;
+            g.head = p.head;
+            g.q0 = p.b * kBlockQ;
+            g.kb = kb;
+            g.xa = p.xa;
+            g.per = p.per;
             return true;
         }
         return false;
@@ -242,7 +276,7 @@ struct CrossSplit {
     // Parts that a cut unit has.
     __device__ __forceinline__ int parts(const Seg &g) const
     {
-        return cta_of(g.xa + g.s.tiles - 1) - cta_of(g.xa) + 1;
+        return cta_of(g.xa + static_cast<long long>(g.s.tiles - 1) * g.per) - cta_of(g.xa) + 1;
     }
 };
 

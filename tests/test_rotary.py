@@ -3,14 +3,14 @@ against their formulas in 64 bits.
 
 Tolerances, from the arithmetic.  The output is rounded once to type t: at most
 u_t = eps_t / 2 relative to the value.  Before that everything is fp32 with
-u = 2^-24: a turned number is x0 c - x1 s with each of c, s off by at most 2 ulp
-of sincospif plus the rounding of its argument and of the amplitude (together
-below 8 u), two products and a sum (3 u), so below 11 u (|x0| + |x1|) a absolute.
-The angle's fraction is cut to fp32 after an exact product: 2 pi 2^-26 rad
-absolute at most, below 7 u.  18 u (|x0| + |x1|) a covers both.  A norm adds
+u = 2^-24: a turned number is x0 c - x1 s with each of c, s off by the function's
+own error (fp32 rows: 2 ulp of sincospif; 16-bit rows: 2^-20.9 = 8.6 u of the
+fast sine), the angle's (a fraction of turns exact to 2^-32, rounded to fp32:
+at most pi u + 0.1 u rad) and the amplitude's product (1 u), then two products
+and a sum (3 u): below 16.1 u (|x0| + |x1|) a absolute, 18 u taken.  A norm adds
 its factor: a mean of D <= 256 squares summed in D / lanes + 5 steps (below
-24 u), the root and the division (2 u), two products (2 u); relative 28 u on
-x0 and x1.  LayerNorm also subtracts the mean: 24 u max|x| absolute before the
+20 u), rsqrt (2 ulp, 4 u), two products (2 u); relative 28 u taken on x0 and x1.
+LayerNorm also subtracts the mean: 24 u max|x| absolute before the
 factor.
 """
 import ctypes
