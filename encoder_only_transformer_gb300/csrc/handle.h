@@ -73,9 +73,9 @@ namespace mbert {
 
 // 2-D tensor map of 16-bit elements over [rows][width], rows `pitch` elements
 // apart, box 64 columns x `box` rows, 128-byte swizzle, out-of-range reads
-// give 0.
+// give 0.  l2_bytes: what the L2 fetches at a time, 128 or 256.
 int encode_rows(const mbert_attn *h, CUtensorMap *tm, const void *ptr, int64_t width, int64_t rows,
-                int64_t pitch, int box);
+                int64_t pitch, int box, int l2_bytes);
 
 struct DeviceGuard {
     int prev = -1;

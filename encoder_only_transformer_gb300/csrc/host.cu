@@ -151,7 +151,7 @@ int encode_map(mbert_attn *h, CUtensorMap *tm, const void *ptr, int width, int64
         if (m.used < victim->used)
             victim = &m;
     }
-    if (encode_rows(h, tm, ptr, width, rows, width, kBlockM) != MBERT_OK)
+    if (encode_rows(h, tm, ptr, width, rows, width, kBlockM, 256) != MBERT_OK)
         return MBERT_ERR_CUDA;
     victim->ptr = ptr;
     victim->width = width;
@@ -201,15 +201,15 @@ Plan make_plan(mbert_attn *h, const int32_t *cu, int n_seqs, int64_t T, int max_
 }  // namespace
 
 int mbert::encode_rows(const mbert_attn *h, CUtensorMap *tm, const void *ptr, int64_t width, int64_t rows,
-                       int64_t pitch, int box_rows)
+                       int64_t pitch, int box_rows, int l2_bytes)
 {
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(kHeadDim), static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = h->encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims,
-                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           l2_bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MBERT_OK : MBERT_ERR_CUDA;
 }

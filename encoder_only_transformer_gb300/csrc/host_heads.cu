@@ -364,12 +364,16 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     CrossArgs a;
     const int kbox = p.token ? 64 : kBlockN;
+    // A head's part of a row is what a CTA reads of it: 128 bytes for D = 64.
+    // Fetching 256 brought the next head's in too, for nobody on a long cache
+    // (672 MB from DRAM for 488 MB of keys and values).
+    const int l2 = 2 * D;
     // without any key row the maps stand over q: all of it is masked
-    if ((!p.token && encode_rows(h, &a.tm_q, c.q, qw, c.rows_q, c.q_row, kBlockM) != MBERT_OK) ||
+    if ((!p.token && encode_rows(h, &a.tm_q, c.q, qw, c.rows_q, c.q_row, kBlockM, l2) != MBERT_OK) ||
         encode_rows(h, &a.tm_k, keys ? c.k : c.q, keys ? kw : qw, keys ? c.rows_k : c.rows_q,
-                    keys ? c.k_row : c.q_row, kbox) != MBERT_OK ||
+                    keys ? c.k_row : c.q_row, kbox, l2) != MBERT_OK ||
         encode_rows(h, &a.tm_v, keys ? c.v : c.q, keys ? kw : qw, keys ? c.rows_k : c.rows_q,
-                    keys ? c.v_row : c.q_row, kbox) != MBERT_OK)
+                    keys ? c.v_row : c.q_row, kbox, l2) != MBERT_OK)
         return MBERT_ERR_CUDA;
     a.q = c.q;
     a.out = c.out;
