@@ -403,22 +403,21 @@ class Attention:
                                  or t.dtype != like.dtype):
             raise TypeError(f"{name} must have the rows, head size and type of the other tensor")
 
-    def _heads(self, src, dst, name, weight=None):
-        """-> (dst, Heads) of a [T, H, D] tensor and its result"""
-        if dst is None:
-            dst = torch.empty(src.shape, dtype=src.dtype, device=self.device)
-        elif dst is not src:
-            self._check_heads(dst, name, src)
-            if dst.shape != src.shape:
-                raise TypeError(f"{name} must have the shape {list(src.shape)}")
+    def _heads_template(self, src, dst):
+        """The Heads of a [T, H, D] tensor and its result (None: a new one)
+        without the pointers."""
         T, H, D = src.shape
-        (a, b, _), (c, d, _) = src.stride(), dst.stride()
+        (a, b, _), (c, d, _) = src.stride(), (H * D, D, 1) if dst is None else dst.stride()
         if T <= 1 or H <= 1:
             # a dimension of one element has no stride that matters
             a, c = (a, c) if T > 1 else (H * D, H * D)
             b, d = (b, d) if H > 1 else (D, D)
-        return dst, Heads(src.data_ptr(), dst.data_ptr(), None if weight is None else weight.data_ptr(),
-                          H, a, b, c, d)
+        return bytes(Heads(None, None, None, H, a, b, c, d))
+
+    def _check_out(self, out, name, like):
+        self._check_heads(out, name, like)
+        if out.shape != like.shape:
+            raise TypeError(f"{name} must have the shape {list(like.shape)}")
 
     def _positions(self, positions, cu_seqlens, tokens):
         """-> (positions pointer, bits, cu_seqlens pointer, sequences)"""
@@ -441,17 +440,23 @@ class Attention:
         last sequence are left as they were).  x may be strided (a view of fused
         rows); out may be x.  inverse=True turns the other way (the transpose:
         the gradient of a turned tensor goes back through it)."""
-        key = ("rotary", _layout(x))
+        key = ("rotary", _layout(x)) if out is None else ("rotary", _layout(x), _layout(out))
         known = self._known.get(key)
         if known is None:
             self._check_heads(x, "x")
-            known = self._remember(key, (x.shape[0], x.shape[2], _DTYPES[x.dtype]))
-        T, D, dtype = known
-        pos = self._positions(positions, cu_seqlens, T)
-        out, heads = self._heads(x, out, "out")
-        st = _lib.mbert_attn_rotary(self._h, ctypes.byref(heads), T, D, dtype, rope._ref, *pos, 1 if inverse else 0,
-                                    _stream_of(self.device))
-        _check(st, "rotary")
+            if out is not None:
+                self._check_out(out, "out", x)
+            known = self._remember(key, (x.shape[0], x.shape[2], _DTYPES[x.dtype], self._heads_template(x, out)))
+        T, D, dtype, template = known
+        pos, bits, cu, n = self._positions(positions, cu_seqlens, T)
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=self.device)
+        heads = Heads.from_buffer_copy(template)
+        heads.src, heads.dst = x.data_ptr(), out.data_ptr()
+        st = _lib.mbert_attn_rotary(self._h, ctypes.byref(heads), T, D, dtype, rope._ref, pos, bits, cu, n,
+                                    1 if inverse else 0, _stream_of(self.device))
+        if st != 0:
+            _check(st, "rotary")
         return out
 
     def qk_norm_rotary(self, q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
@@ -468,40 +473,60 @@ class Attention:
         first = q if q is not None else k
         if first is None:
             raise ValueError("give q, k or both")
-        for t, w, name in ((q, q_weight, "q"), (k, k_weight, "k")):
-            if t is not None and w is None:
+        sides = []
+        for t, w, o, name in ((q, q_weight, q_out, "q"), (k, k_weight, k_out, "k")):
+            if t is None:
+                sides.append(None)
+            elif w is None:
                 raise TypeError(f"{name}_weight is missing")
-        key = ("qk_norm_rotary", None if q is None else _layout(q, q_weight),
-               None if k is None else _layout(k, k_weight))
+            else:
+                sides.append(_layout(t, w) if o is None else _layout(t, w, o))
+        key = ("qk_norm_rotary", sides[0], sides[1])
         known = self._known.get(key)
         if known is None:
-            for t, w, name in ((q, q_weight, "q"), (k, k_weight, "k")):
+            templates = []
+            for t, w, o, name in ((q, q_weight, q_out, "q"), (k, k_weight, k_out, "k")):
                 if t is None:
+                    templates.append(None)
                     continue
                 self._check_heads(t, name, first)
                 if (w.dtype != t.dtype or tuple(w.shape) != (t.shape[2],)
                         or w.device != self.device or not w.is_contiguous()):
                     raise TypeError(f"{name}_weight must be a contiguous [{t.shape[2]}] tensor of {name}'s type")
-            known = self._remember(key, (first.shape[0], first.shape[2], _DTYPES[first.dtype]))
-        T, D, dtype = known
+                if o is not None:
+                    self._check_out(o, f"{name}_out", t)
+                templates.append(self._heads_template(t, o))
+            known = self._remember(key, (first.shape[0], first.shape[2], _DTYPES[first.dtype], *templates))
+        T, D, dtype, q_template, k_template = known
         if rope is None or rope.dim == 0:
             if positions is not None or cu_seqlens is not None:
                 raise ValueError("positions or cu_seqlens without a rotation")
-            pos = (None, 0, None, 0)
+            pos, bits, cu, n = None, 0, None, 0
         else:
-            pos = self._positions(positions, cu_seqlens, T)
-        qh = kh = None
-        if q is not None:
-            q_out, qh = self._heads(q, q_out, "q_out", q_weight)
-            qh = ctypes.byref(qh)
-        if k is not None:
-            k_out, kh = self._heads(k, k_out, "k_out", k_weight)
-            kh = ctypes.byref(kh)
+            pos, bits, cu, n = self._positions(positions, cu_seqlens, T)
+        q_ref = k_ref = None
+        if q is None:
+            q_out = None
+        else:
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+            heads = Heads.from_buffer_copy(q_template)
+            heads.src, heads.dst, heads.weight = q.data_ptr(), q_out.data_ptr(), q_weight.data_ptr()
+            q_ref = ctypes.byref(heads)
+        if k is None:
+            k_out = None
+        else:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=self.device)
+            heads = Heads.from_buffer_copy(k_template)
+            heads.src, heads.dst, heads.weight = k.data_ptr(), k_out.data_ptr(), k_weight.data_ptr()
+            k_ref = ctypes.byref(heads)
         st = _lib.mbert_attn_qk_norm_rotary(
-            self._h, qh, kh, T, D, dtype, _NORMS[norm], float(eps),
-            None if rope is None else rope._ref, *pos, _stream_of(self.device))
-        _check(st, "qk_norm_rotary")
-        return (q_out if q is not None else None), (k_out if k is not None else None)
+            self._h, q_ref, k_ref, T, D, dtype, _NORMS[norm], float(eps), None if rope is None else rope._ref,
+            pos, bits, cu, n, _stream_of(self.device))
+        if st != 0:
+            _check(st, "qk_norm_rotary")
+        return q_out, k_out
 
     def _check_cross(self, t, name, dims):
         """A [..., heads, head_dim] tensor whose heads lie side by side."""
@@ -526,7 +551,8 @@ class Attention:
         # captured ones never share it
         ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         st = _lib.mbert_attn_cross(self._h, ctypes.byref(args), ws.data_ptr(), need, _stream_of(self.device))
-        _check(st, "cross_attention")
+        if st != 0:
+            _check(st, "cross_attention")
         return out
 
     def _cross_known(self, key, q, k, v, out, rows_q, rows_k, pitches, n_seqs, packed, max_seqlen_q, key_mask, scale):

@@ -52,7 +52,8 @@ constexpr int kMaskSlots = 4;
 // (D = 64) or 2900 clocks (D = 128), for one 1900 (D = 128); a unit's fixed work
 // (the end of the softmax, the output, the refill) 2600 to 4600.
 template <int D>
-using Split = CrossSplit<D == 64 ? 384 : 512, kCrossBlockRows, kBlockN, 6, 4, 10, 4>;
+using Split = CrossSplit<D == 64 ? 384 : 512, kCrossBlockRows, kBlockN, 6, 4, 10,
+                         kCrossBlockWholeKeys / kBlockN>;
 
 template <int D>
 struct Layout {

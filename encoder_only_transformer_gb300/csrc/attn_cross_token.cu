@@ -13,7 +13,9 @@
 //
 // CTA: warps 0-3 take 16 keys of every tile each, with a softmax state of
 // their own; at the end of a segment the four states are joined in shared
-// memory.  Warp 4 is the TMA producer.
+// memory.  Warp 4 is the producer: it finds the segments (64-bit divisions and
+// global loads that would otherwise stand before each of them), hands them on
+// through a ring with their query rows, and keeps the K and V ring full.
 #include "common.cuh"
 #include "cross_sched.cuh"
 #include "internal.h"
@@ -28,8 +30,19 @@ constexpr int kRows = kCrossTokenRows;
 constexpr uint32_t kBoxBytes = kTileKeys * 128;       // 64 keys x 64 columns
 
 // A unit's fixed work (the query rows, joining four states, the output) costs
-// about two tiles; units of up to 8 tiles (512 keys) are not cut.
-using Split = CrossSplit<kThreads, 0, kTileKeys, 1, 1, 2, 8>;
+// about two tiles.
+using Split = CrossSplit<kThreads, 0, kTileKeys, 1, 1, 2, kCrossTokenWholeKeys / kTileKeys>;
+
+// A segment (a unit and a run of its key tiles) as the producer hands it on.
+struct alignas(16) Rec {
+    int q_row, q_len, k_row, k_len;
+    int kb, ke, tiles;      // key tiles [kb, ke) of tiles; ke = 0: no more segments
+    int head, seq;          // key head, sequence
+    int parts;              // of a cut unit whose first part this is
+    int pad[2];
+};
+static_assert(sizeof(Rec) == 48, "record");
+constexpr int kRecs = 2;
 
 template <int D>
 struct Layout {
@@ -38,8 +51,11 @@ struct Layout {
     static constexpr int kStages = D == 64 ? 3 : 2;
     static constexpr uint32_t kOffState = kStages * 2 * kTile;      // [4][16][D + 2] floats
     static constexpr int kStateRow = D + 4;                         // floats; rows 16 bytes aligned
-    static constexpr uint32_t kOffBar = kOffState + 4u * kWarps * kRows * kStateRow;
-    static constexpr uint32_t kOffScratch = kOffBar + 128;
+    static constexpr uint32_t kOffQ = kOffState + 4u * kWarps * kRows * kStateRow;   // [kRecs][16][D] query rows
+    static constexpr uint32_t kQBytes = kRows * D * 2;
+    static constexpr uint32_t kOffBar = kOffQ + kRecs * kQBytes;
+    static constexpr uint32_t kOffRecs = kOffBar + 128;
+    static constexpr uint32_t kOffScratch = kOffRecs + 48 * kRecs;
     static constexpr uint32_t kSmemBytes = kOffScratch + sizeof(Split::Scratch) + 1024;
 };
 
@@ -47,6 +63,8 @@ constexpr int kBarFull = 0;       // + stage: K and V of a tile
 constexpr int kBarEmpty = 3;      // + stage: read by the four warps
 constexpr int kBarStates = 6;     // the four states are in shared memory
 constexpr int kBarJoined = 7;     // they have been read
+constexpr int kBarRecFull = 8;    // + record slot: a segment and its query rows
+constexpr int kBarRecEmpty = 10;  // + record slot: read by the four warps
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4])
 {
@@ -99,32 +117,70 @@ struct Ctx {
     uint32_t base;
     uint8_t *sbase;
     const CrossArgs &a;
-    const Split &split;
     uint32_t bars;
 };
 
 __device__ __forceinline__ uint32_t bar(const Ctx &c, int i) { return c.bars + 8u * i; }
 
+// 16-byte aligned bulk copy of `bytes` (a multiple of 16) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(mbar) : "memory");
+}
+
 template <int D>
-__device__ void producer(const Ctx &c)
+__device__ void producer(const Ctx &c, const Split &split)
 {
     using L = Layout<D>;
-    auto it = c.split.begin();
-    Split::Seg s;
+    const CrossArgs &a = c.a;
+    auto it = split.begin();
+    Split::Seg seg;
     uint32_t g = 0;
-    while (c.split.next(it, s)) {
-        const int col = s.head * D;                  // s.head: key head
-        for (int k = s.kb; k < s.ke; ++k, ++g) {
+    for (uint32_t sg = 0;; ++sg) {
+        Rec r{};
+        const bool more = split.next(it, seg);
+        if (more) {
+            r.q_row = seg.s.q_row;
+            r.q_len = seg.s.q_len;
+            r.k_row = seg.s.k_row;
+            r.k_len = seg.s.k_len;
+            r.kb = seg.kb;
+            r.ke = seg.ke;
+            r.tiles = seg.s.tiles;
+            r.head = seg.head;
+            r.seq = seg.seq;
+            r.parts = seg.kb == 0 && seg.ke < seg.s.tiles ? split.parts(seg) : 0;
+        }
+        const int slot = sg % kRecs;
+        if (sg >= kRecs && !mbar_wait(bar(c, kBarRecEmpty + slot), (sg / kRecs - 1) & 1, a.err))
+            return;
+        reinterpret_cast<Rec *>(c.sbase + L::kOffRecs)[slot] = r;
+        if (!more) {
+            mbar_arrive(bar(c, kBarRecFull + slot));
+            return;
+        }
+        // row i: query i / group, head i % group of the key head's (a query's
+        // heads lie side by side); rows behind the last keep what they held
+        const uint32_t row = 2 * D * a.group;
+        mbar_arrive_expect_tx(bar(c, kBarRecFull + slot), r.q_len * row);
+        for (int i = 0; i < r.q_len; ++i)
+            bulk_load(c.base + L::kOffQ + slot * L::kQBytes + i * row,
+                      static_cast<const uint16_t *>(a.q) + (static_cast<long long>(r.q_row) + i) * a.q_row +
+                          static_cast<long long>(r.head) * a.group * D,
+                      row, bar(c, kBarRecFull + slot));
+        const int col = r.head * D;
+        for (int k = r.kb; k < r.ke; ++k, ++g) {
             const int st = g % L::kStages;
             const uint32_t u = g / L::kStages;
-            if (u > 0 && !mbar_wait(bar(c, kBarEmpty + st), (u - 1) & 1, c.a.err))
+            if (u > 0 && !mbar_wait(bar(c, kBarEmpty + st), (u - 1) & 1, a.err))
                 return;
             const uint32_t dst = c.base + st * 2 * L::kTile;
             mbar_arrive_expect_tx(bar(c, kBarFull + st), 2 * L::kTile);
             for (int h = 0; h < L::kHalves; ++h) {
-                tma_load_2d(dst + h * kBoxBytes, &c.a.tm_k, col + 64 * h, s.s.k_row + k * kTileKeys,
+                tma_load_2d(dst + h * kBoxBytes, &a.tm_k, col + 64 * h, r.k_row + k * kTileKeys,
                             bar(c, kBarFull + st));
-                tma_load_2d(dst + L::kTile + h * kBoxBytes, &c.a.tm_v, col + 64 * h, s.s.k_row + k * kTileKeys,
+                tma_load_2d(dst + L::kTile + h * kBoxBytes, &a.tm_v, col + 64 * h, r.k_row + k * kTileKeys,
                             bar(c, kBarFull + st));
             }
         }
@@ -132,13 +188,13 @@ __device__ void producer(const Ctx &c)
 }
 
 // The 16 keys of this warp in tile k that are visible, as bits.
-__device__ __forceinline__ uint32_t warp_keys(const Ctx &c, const Split::Seg &s, int k, int warp)
+__device__ __forceinline__ uint32_t warp_keys(const Ctx &c, const Rec &s, int k, int warp)
 {
     const int j0 = k * kTileKeys + 16 * warp;
-    const int left = s.s.k_len - j0;
+    const int left = s.k_len - j0;
     uint32_t b = left >= 16 ? 0xffffu : left > 0 ? (1u << left) - 1u : 0u;
     if (b && c.a.key_bits)
-        b &= __ldg(c.a.key_bits + key_bit_word(s.s.k_row, s.seq) + j0 / 32) >> (j0 & 31);
+        b &= __ldg(c.a.key_bits + key_bit_word(s.k_row, s.seq) + j0 / 32) >> (j0 & 31);
     return b;
 }
 
@@ -153,27 +209,27 @@ __device__ void compute(const Ctx &c, int warp, int lane, int cta)
     const int group = a.group;
     const float scale = a.scale_log2;
     float *states = reinterpret_cast<float *>(c.sbase + L::kOffState);
-    auto it = c.split.begin();
-    Split::Seg s;
     uint32_t g = 0;
-    for (uint32_t sg = 0; c.split.next(it, s); ++sg) {
-        const int rows = s.s.q_len * group;         // <= 16 (checked: q_len <= max_q)
-        // query rows as A fragments, straight from global memory
+    for (uint32_t sg = 0;; ++sg) {
+        const int slot = sg % kRecs;
+        if (!mbar_wait(bar(c, kBarRecFull + slot), (sg / kRecs) & 1, a.err))
+            return;
+        const Rec s = reinterpret_cast<const Rec *>(c.sbase + L::kOffRecs)[slot];
+        if (s.ke == 0)
+            return;
+        const int rows = s.q_len * group;           // <= 16 (checked: q_len <= max_q)
+        // query rows as A fragments: lane i addresses row i % 16 and the
+        // 16-byte chunk 2 step + i / 16
         uint32_t qf[kSteps][4];
         {
-            const uint16_t *q = static_cast<const uint16_t *>(a.q);
+            const uint32_t addr = c.base + L::kOffQ + slot * L::kQBytes + (lane & 15) * 2 * D + (lane >> 4) * 16;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = gr + 8 * h;
-                const uint16_t *src = q + (static_cast<long long>(s.s.q_row) + r / group) * a.q_row +
-                                      static_cast<long long>(s.head * group + r % group) * D + 2 * cq;
-#pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    qf[k][h] = r < rows ? *reinterpret_cast<const uint32_t *>(src + 16 * k) : 0u;
-                    qf[k][h + 2] = r < rows ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8) : 0u;
-                }
-            }
+            for (int k = 0; k < kSteps; ++k)
+                ldmatrix_x4(addr + 32 * k, qf[k]);
         }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar(c, kBarRecEmpty + slot));
         float o[D / 8][4];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
@@ -304,7 +360,7 @@ __device__ void compute(const Ctx &c, int warp, int lane, int cta)
         if (!mbar_wait(bar(c, kBarStates), sg & 1, a.err))
             return;
         __syncwarp();
-        const bool whole = s.ke - s.kb == s.s.tiles;
+        const bool whole = s.ke - s.kb == s.tiles;
         float *part = a.parts + (2ll * cta + (s.kb == 0)) * cross_slot_floats(kRows, D);
         // eight numbers of a row per thread
         for (int i = 32 * warp + lane; i < rows * (D / 8); i += 32 * kWarps) {
@@ -329,7 +385,7 @@ __device__ void compute(const Ctx &c, int warp, int lane, int cta)
             if (whole) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 uint16_t *dst = static_cast<uint16_t *>(a.out) +
-                                (static_cast<long long>(s.s.q_row) + r / group) * a.out_row +
+                                (static_cast<long long>(s.q_row) + r / group) * a.out_row +
                                 static_cast<long long>(s.head * group + r % group) * D + 8 * chunk;
                 *reinterpret_cast<uint4 *>(dst) =
                     make_uint4(pack2<kHalf>(x[0] * inv, x[1] * inv), pack2<kHalf>(x[2] * inv, x[3] * inv),
@@ -347,11 +403,11 @@ __device__ void compute(const Ctx &c, int warp, int lane, int cta)
             mbar_arrive(bar(c, kBarJoined));
         if (!whole && s.kb == 0 && warp == 0 && lane == 0) {
             CrossRecord rec;
-            rec.row0 = s.s.q_row;
+            rec.row0 = s.q_row;
             rec.rows = rows;
             rec.head0 = s.head * group;
             rec.group = group;
-            rec.parts = c.split.parts(s);
+            rec.parts = s.parts;
             a.records[cta] = rec;
         }
     }
@@ -373,11 +429,15 @@ attn_cross_token_kernel(const __grid_constant__ CrossArgs a)
     Split split(a, a.heads / a.group);
     const bool work = split.find(*reinterpret_cast<Split::Scratch *>(sbase + L::kOffScratch), gridDim.x, 4);
     if (work) {
-        const Ctx c{base, sbase, a, split, base + L::kOffBar};
+        const Ctx c{base, sbase, a, base + L::kOffBar};
         if (threadIdx.x == 0) {
             for (int st = 0; st < L::kStages; ++st) {
                 mbar_init(bar(c, kBarFull + st), 1);
                 mbar_init(bar(c, kBarEmpty + st), kWarps);
+            }
+            for (int i = 0; i < kRecs; ++i) {
+                mbar_init(bar(c, kBarRecFull + i), 1);
+                mbar_init(bar(c, kBarRecEmpty + i), kWarps);
             }
             mbar_init(bar(c, kBarStates), kWarps);
             mbar_init(bar(c, kBarJoined), kWarps);
@@ -386,7 +446,7 @@ attn_cross_token_kernel(const __grid_constant__ CrossArgs a)
         __syncthreads();
         if (warp == kWarps) {
             if (lane == 0)
-                producer<D>(c);
+                producer<D>(c, split);
         } else {
             compute<D, kHalf>(c, warp, lane, blockIdx.x);
         }

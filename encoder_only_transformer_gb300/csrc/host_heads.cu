@@ -407,9 +407,13 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     }
     if (e == cudaSuccess)
         e = p.token ? launch_cross_token(a, D, half, p.ctas, st) : launch_cross_blocks(a, D, half, p.ctas, st);
-    if (e == cudaSuccess)
+    h->launches += 1;
+    // no sequence can be long enough to be cut: nothing to join
+    const int64_t longest = c.cu_k ? c.rows_k : a.len_k;
+    if (e == cudaSuccess && longest > (p.token ? kCrossTokenWholeKeys : kCrossBlockWholeKeys)) {
         e = launch_cross_join(a, D, half, p.token ? p.max_q * p.group : kCrossBlockRows, p.ctas, st);
-    h->launches += 2;
+        h->launches += 1;
+    }
     h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : MBERT_ERR_CUDA;
 }

@@ -308,6 +308,12 @@ struct CrossRecord {
 constexpr int kCrossBlockRows = 256;    // rows of a unit of attn_cross.cu
 constexpr int kCrossTokenRows = 16;     // rows of a unit of attn_cross_token.cu
 
+// Units of at most this many keys are never cut between CTAs (blocks of
+// queries, single tokens): up to there joining parts costs more than it evens
+// out, and a call with no more key rows needs no joining kernel.
+constexpr int kCrossBlockWholeKeys = 512;
+constexpr int kCrossTokenWholeKeys = 1024;
+
 // First word of sequence s's key bits: every sequence starts a new word.
 __host__ __device__ inline long long key_bit_word(long long k_row, int s) { return k_row / 32 + s; }
 
