@@ -549,8 +549,9 @@ class Attention:
             args.key_mask = key_mask.data_ptr()
         # of the call's own, from torch's allocator: calls on other streams and
         # captured ones never share it
-        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        st = _lib.mbert_attn_cross(self._h, ctypes.byref(args), ws.data_ptr(), need, _stream_of(self.device))
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        st = _lib.mbert_attn_cross(self._h, ctypes.byref(args), None if ws is None else ws.data_ptr(), need,
+                                   _stream_of(self.device))
         if st != 0:
             _check(st, "cross_attention")
         return out

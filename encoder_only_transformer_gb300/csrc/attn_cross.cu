@@ -816,7 +816,7 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
     uint32_t *slot = reinterpret_cast<uint32_t *>(sbase + L::kOffBar + kSlotInBars);
     const int cta = blockIdx.x;
 
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0 && a.records)
         a.records[cta].parts = 0;
     Split<D> split(a, a.heads);
     // two tiles and a unit's fixed work per CTA at least

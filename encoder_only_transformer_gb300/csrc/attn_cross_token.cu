@@ -424,7 +424,7 @@ attn_cross_token_kernel(const __grid_constant__ CrossArgs a)
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *sbase = smem_raw + (base - raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0 && a.records)
         a.records[blockIdx.x].parts = 0;
     Split split(a, a.heads / a.group);
     const bool work = split.find(*reinterpret_cast<Split::Scratch *>(sbase + L::kOffScratch), gridDim.x, 4);

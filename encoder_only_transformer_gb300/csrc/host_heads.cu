@@ -252,6 +252,7 @@ namespace {
 // How a cross-attention call runs: the kernel, its CTAs and the workspace.
 struct CrossPlan {
     bool token;             // few rows per sequence and key head
+    bool join;              // a sequence may be long enough to be cut
     int group, max_q, ctas, unit_rows;
     int64_t records, parts, lens, bits, bytes;      // offsets and the total
 };
@@ -286,9 +287,11 @@ int cross_plan(const mbert_attn *h, const mbert_attn_cross_args *c, CrossPlan *p
     p->token = most * p->group <= kCrossTokenRows;
     p->ctas = p->token ? h->num_sms * cross_token_ctas(c->head_dim) : h->num_sms;
     p->unit_rows = p->token ? kCrossTokenRows : kCrossBlockRows;
+    const int64_t longest = c->cu_k || c->n_seqs == 0 ? c->rows_k : c->rows_k / c->n_seqs;
+    p->join = longest > (p->token ? kCrossTokenWholeKeys : kCrossBlockWholeKeys);
     p->records = 0;
-    p->parts = align256(static_cast<int64_t>(sizeof(CrossRecord)) * p->ctas);
-    p->lens = align256(p->parts + 2 * p->ctas * cross_slot_floats(p->unit_rows, c->head_dim) * 4);
+    p->parts = p->join ? align256(static_cast<int64_t>(sizeof(CrossRecord)) * p->ctas) : 0;
+    p->lens = p->join ? align256(p->parts + 2 * p->ctas * cross_slot_floats(p->unit_rows, c->head_dim) * 4) : 0;
     p->bits = c->key_mask ? align256(p->lens + 4ll * c->n_seqs) : p->lens;
     p->bytes = c->key_mask ? align256(p->bits + 4 * (key_bit_word(c->rows_k, c->n_seqs) + 1)) : p->lens;
     return MBERT_OK;
@@ -318,7 +321,7 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     if (c.rows_q == 0)
         return MBERT_OK;
     const bool keys = c.rows_k > 0;
-    if (!c.q || !c.out || !workspace || workspace_bytes < p.bytes || (keys && (!c.k || !c.v)))
+    if (!c.q || !c.out || (p.bytes > 0 && !workspace) || workspace_bytes < p.bytes || (keys && (!c.k || !c.v)))
         return MBERT_ERR_BAD_ARG;
     for (const void *ptr : {c.q, c.k, c.v, static_cast<const void *>(c.out), static_cast<const void *>(workspace)})
         if (reinterpret_cast<uintptr_t>(ptr) & 15)
@@ -344,7 +347,8 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
         const uintptr_t lo = reinterpret_cast<uintptr_t>(ptr);
         return Extent{lo, lo + static_cast<uintptr_t>(bytes)};
     };
-    const Extent oe = rows(c.out, c.rows_q, c.out_row, qw), we = flat(workspace, p.bytes);
+    const Extent oe = rows(c.out, c.rows_q, c.out_row, qw);
+    const Extent we = p.bytes > 0 ? flat(workspace, p.bytes) : Extent{0, 0};
     auto meet = [](Extent x, Extent y) { return x.lo < y.hi && y.lo < x.hi; };
     if (may_overlap(oe, c.out_row, qw, rows(c.q, c.rows_q, c.q_row, qw), c.q_row, qw, 2) || meet(oe, we) ||
         meet(we, rows(c.q, c.rows_q, c.q_row, qw)))
@@ -393,8 +397,10 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
                                       1.4426950408889634);
     a.err = h->err;
     char *ws = static_cast<char *>(workspace);
-    a.records = reinterpret_cast<CrossRecord *>(ws + p.records);
-    a.parts = reinterpret_cast<float *>(ws + p.parts);
+    if (p.join) {
+        a.records = reinterpret_cast<CrossRecord *>(ws + p.records);
+        a.parts = reinterpret_cast<float *>(ws + p.parts);
+    }
     const bool half = c.dtype == MBERT_F16;
     cudaError_t e = cudaSuccess;
     if (c.key_mask && keys) {
@@ -408,9 +414,7 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     if (e == cudaSuccess)
         e = p.token ? launch_cross_token(a, D, half, p.ctas, st) : launch_cross_blocks(a, D, half, p.ctas, st);
     h->launches += 1;
-    // no sequence can be long enough to be cut: nothing to join
-    const int64_t longest = c.cu_k ? c.rows_k : a.len_k;
-    if (e == cudaSuccess && longest > (p.token ? kCrossTokenWholeKeys : kCrossBlockWholeKeys)) {
+    if (e == cudaSuccess && p.join) {
         e = launch_cross_join(a, D, half, p.token ? p.max_q * p.group : kCrossBlockRows, p.ctas, st);
         h->launches += 1;
     }

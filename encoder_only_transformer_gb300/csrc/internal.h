@@ -292,7 +292,8 @@ struct CrossArgs {
     const uint32_t *key_bits = nullptr;
     const int32_t *key_len = nullptr;
     int32_t *err = nullptr;
-    // units cut between CTAs: a record and two part slots per CTA
+    // units cut between CTAs: a record and two part slots per CTA (null where
+    // no sequence can be long enough)
     struct CrossRecord *records = nullptr;
     float *parts = nullptr;
 };

@@ -363,8 +363,8 @@ typedef struct {
  * (pointers need only be NULL or not).  Host only. */
 int mbert_attn_cross_workspace(mbert_attn *h, const mbert_attn_cross_args *args, int64_t *bytes);
 
-/* Enqueue the call.  workspace: device memory of that size, 16-byte aligned,
- * contents irrelevant; it may be used again once the call's work is done, so
+/* Enqueue the call.  workspace: device memory of that size (NULL for 0),
+ * 16-byte aligned, contents irrelevant; it may be used again once the call's work is done, so
  * calls that may overlap on the GPU need one each.  When the device-side
  * checks of cu_q and cu_k fail nothing is written and the error is reported by
  * mbert_attn_get_error().  Results do not depend on timing: the parts of a

@@ -472,11 +472,29 @@ def test_refusals(built):
     # the workspace is checked too
     import ctypes
     lib, h = binding.load_library(), binding._default(q.device)
+    q, k, v = (x.cuda() for x in make([3], [2000], 4, 2, 64, "bf16"))
+    ck = cu_of([2000])
     a = binding.CrossArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), torch.empty_like(q).data_ptr(), 256, 128, 128,
-                          256, 3, 10, 4, 2, 64, 0, 0.0, 1, cq.data_ptr(), ck.data_ptr(), 0, None)
+                          256, 3, 2000, 4, 2, 64, 0, 0.0, 1, cq.data_ptr(), ck.data_ptr(), 0, None)
     n = ctypes.c_int64()
     assert lib.mbert_attn_cross_workspace(h.handle, ctypes.byref(a), ctypes.byref(n)) == 0 and n.value > 0
     ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
     assert lib.mbert_attn_cross(h.handle, ctypes.byref(a), ws.data_ptr(), n.value - 1, None) == -1
     assert lib.mbert_attn_cross(h.handle, ctypes.byref(a), None, n.value, None) == -1
+    a.rows_k = 500              # too short to be cut: no workspace
+    assert lib.mbert_attn_cross_workspace(h.handle, ctypes.byref(a), ctypes.byref(n)) == 0 and n.value == 0
     assert h.get_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hk,D,dtype,kl", [
+    (4, 4, 64, "bf16", [50000, 17, 0, 20000]), (12, 12, 64, "f16", [9000, 15000, 1]),
+    (16, 4, 128, "bf16", [33000]), (6, 2, 64, "bf16", [70000, 70000]), (10, 10, 128, "f16", [14000, 300])])
+@pytest.mark.parametrize("masked", [False, True])
+def test_tokens_over_long_caches(built, H, Hk, D, dtype, kl, masked):
+    """Every CTA with whole and cut units of several heads and sequences."""
+    mask = None
+    if masked:
+        mask = torch.rand(sum(kl), generator=torch.Generator().manual_seed(1)) < 0.7
+        mask[:4000] = False
+    run_packed([1, 2, 1, 2][:len(kl)], kl, H, Hk, D, dtype, max_q=2, seed=3, behind=5, mask=mask)
