@@ -127,7 +127,7 @@ struct alignas(16) Rec {
     int kb, ke, tiles;      // key tiles [kb, ke) of tiles; ke = 0: no more segments
     int head, seq;
     int parts;              // of a cut unit whose first part this is
-    int pad;
+    int k_full;             // keys before the first hidden one
 };
 constexpr int kRecs = 4;
 
@@ -155,11 +155,10 @@ __device__ __forceinline__ bool read_rec(const Ctx &c, uint32_t sg, int lane, Re
     return r.ke > 0;
 }
 
-// A tile whose keys are not all visible (or not known to be).
-__device__ __forceinline__ bool needs_mask(const Ctx &c, const Rec &s, int k)
-{
-    return c.a.key_bits != nullptr || s.k_len - k * kBlockN < kBlockN;
-}
+// A tile whose keys are not all known to be visible, and one of a sequence with
+// hidden keys among the visible ones, which needs their bits.
+__device__ __forceinline__ bool needs_mask(const Rec &s, int k) { return s.k_full - k * kBlockN < kBlockN; }
+__device__ __forceinline__ bool needs_bits(const Rec &s) { return s.k_full < s.k_len; }
 
 // The unit's second query tile holds rows.
 __device__ __forceinline__ bool second_tile(const Rec &s) { return s.q_len - s.q0 > kBlockM; }
@@ -189,6 +188,7 @@ __device__ void producer(const Ctx &c, const Split<D> &split)
             s.q0 = seg.q0;
             s.k_row = seg.s.k_row;
             s.k_len = seg.s.k_len;
+            s.k_full = seg.s.k_full;
             s.kb = seg.kb;
             s.ke = seg.ke;
             s.tiles = seg.s.tiles;
@@ -316,7 +316,7 @@ __device__ void so_issuer(const Ctx &c, int w, int lane)
                 const int st = g % L::kStages;
                 if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
                     return;
-                if (needs_mask(c, s, s.kb + t - 1)) {
+                if (needs_mask(s, s.kb + t - 1)) {
                     if (mine &&
                         !mbar_wait(bar(c, kBarVClean + masked % kMaskSlots), (masked / kMaskSlots) & 1, err))
                         return;
@@ -410,7 +410,7 @@ __device__ void o_issuer(const Ctx &c, int w, int lane)
             if (sub == 0) {
                 if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
                     return;
-                if (needs_mask(c, s, s.kb + j / L::kSteps)) {
+                if (needs_mask(s, s.kb + j / L::kSteps)) {
                     if (mine &&
                         !mbar_wait(bar(c, kBarVClean + masked % kMaskSlots), (masked / kMaskSlots) & 1, err))
                         return;
@@ -448,7 +448,7 @@ __device__ __forceinline__ uint32_t tile_word(const Ctx &c, const Rec &s, int k,
 {
     const int left = s.k_len - k * kBlockN - 32 * i;
     uint32_t w = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
-    if (w && c.a.key_bits)
+    if (w && needs_bits(s))
         w &= __ldg(c.a.key_bits + key_bit_word(s.k_row, s.seq) + 4 * k + i);
     return w;
 }
@@ -459,13 +459,13 @@ __device__ void mask_stager(const Ctx &c, int lane)
     using L = Layout<D>;
     int *err = c.a.err;
     Rec s;
-    uint32_t g = 0, masked = 0;
+    uint32_t g = 0, masked = 0, with_bits = 0;
     for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
         for (int k = s.kb; k < s.ke; ++k, ++g) {
             const int st = g % L::kStages;
             // every tile is waited for and handed back, seen or not, so that
             // this warp neither runs ahead of the ring nor falls behind it
-            if (!needs_mask(c, s, k)) {
+            if (!needs_mask(s, k)) {
                 if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
                     return;
                 if (lane == 0)
@@ -473,10 +473,12 @@ __device__ void mask_stager(const Ctx &c, int lane)
                 __syncwarp();
                 continue;
             }
-            const uint32_t slot = masked % kMaskSlots, u = masked / kMaskSlots;
+            const uint32_t clean = masked % kMaskSlots;
             ++masked;
             const uint32_t mine = lane < 4 ? tile_word(c, s, k, lane) : 0u;
-            if (c.a.key_bits) {
+            if (needs_bits(s)) {
+                const uint32_t slot = with_bits % kMaskSlots, u = with_bits / kMaskSlots;
+                ++with_bits;
                 if (u > 0 && !mbar_wait(bar(c, kBarBitsEmpty + slot), (u - 1) & 1, err))
                     return;
                 if (lane < 4)
@@ -506,7 +508,7 @@ __device__ void mask_stager(const Ctx &c, int lane)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(bar(c, kBarVClean + slot));
+                mbar_arrive(bar(c, kBarVClean + clean));
                 mbar_arrive(bar(c, kBarVEmpty + st));
             }
             __syncwarp();
@@ -576,21 +578,19 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                        : mbar_wait(bar(c, step & 1 ? kBarOOdd + w : kBarODone + w), step >> 1 & 1, err);
     };
     Rec s;
-    uint32_t gw = 0, masked = 0;
+    uint32_t gw = 0, with_bits = 0;
     for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
         const int n = seg_steps<D>(s);
         if (w == 1 && !second_tile(s)) {
             // nothing to do but hand the key bits on
-            for (int t = 0; t < s.ke - s.kb; ++t) {
-                if (!needs_mask(c, s, s.kb + t))
+            for (int k = s.kb; k < s.ke && needs_bits(s); ++k) {
+                if (!needs_mask(s, k))
                     continue;
-                if (c.a.key_bits) {
-                    const uint32_t slot = masked % kMaskSlots;
-                    if (!mbar_wait(bar(c, kBarBitsFull + slot), (masked / kMaskSlots) & 1, err))
-                        return;
-                    mbar_arrive(bar(c, kBarBitsEmpty + slot));
-                }
-                ++masked;
+                const uint32_t slot = with_bits % kMaskSlots;
+                if (!mbar_wait(bar(c, kBarBitsFull + slot), (with_bits / kMaskSlots) & 1, err))
+                    return;
+                mbar_arrive(bar(c, kBarBitsEmpty + slot));
+                ++with_bits;
             }
             continue;
         }
@@ -599,7 +599,6 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
         uint32_t bits[4] = {0u, 0u, 0u, 0u};   // the tile's key bits
         for (int j = 0; j < n; ++j, ++gw) {
             const int sub = j % L::kSteps;
-            const bool last_sub = sub == L::kSteps - 1 || j == n - 1;
             if (!(D == 64 ? mbar_wait(bar(c, kBarSFull + w), gw & 1, err)
                           : mbar_wait(bar(c, gw & 1 ? kBarSOdd + w : kBarSFull + w), gw >> 1 & 1, err)))
                 return;
@@ -624,12 +623,13 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                 mbar_arrive(bar(c, kBarSEmpty + w));   // S may be overwritten now
 
             const int kt = s.kb + j / L::kSteps;
-            if (needs_mask(c, s, kt)) {
-                if (c.a.key_bits) {
+            if (needs_mask(s, kt)) {
+                if (needs_bits(s)) {
                     if (sub == 0) {
-                        const uint32_t slot = masked % kMaskSlots;
-                        if (!mbar_wait(bar(c, kBarBitsFull + slot), (masked / kMaskSlots) & 1, err))
+                        const uint32_t slot = with_bits % kMaskSlots;
+                        if (!mbar_wait(bar(c, kBarBitsFull + slot), (with_bits / kMaskSlots) & 1, err))
                             return;
+                        ++with_bits;
                         const uint4 b = reinterpret_cast<const uint4 *>(c.sbase + L::kOffWords)[slot];
                         bits[0] = b.x, bits[1] = b.y, bits[2] = b.z, bits[3] = b.w;
                         mbar_arrive(bar(c, kBarBitsEmpty + slot));
@@ -658,7 +658,6 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                                 sc[i] = -INFINITY;
                     }
                 }
-                masked += last_sub;
             }
             // row maximum: 8 independent chains
             float mp[8];

@@ -39,7 +39,8 @@ struct alignas(16) Rec {
     int kb, ke, tiles;      // key tiles [kb, ke) of tiles; ke = 0: no more segments
     int head, seq;          // key head, sequence
     int parts;              // of a cut unit whose first part this is
-    int pad[2];
+    int k_full;             // keys before the first hidden one
+    int pad;
 };
 static_assert(sizeof(Rec) == 48, "record");
 constexpr int kRecs = 2;
@@ -145,6 +146,7 @@ __device__ void producer(const Ctx &c, const Split &split)
             r.q_len = seg.s.q_len;
             r.k_row = seg.s.k_row;
             r.k_len = seg.s.k_len;
+            r.k_full = seg.s.k_full;
             r.kb = seg.kb;
             r.ke = seg.ke;
             r.tiles = seg.s.tiles;
@@ -193,7 +195,7 @@ __device__ __forceinline__ uint32_t warp_keys(const Ctx &c, const Rec &s, int k,
     const int j0 = k * kTileKeys + 16 * warp;
     const int left = s.k_len - j0;
     uint32_t b = left >= 16 ? 0xffffu : left > 0 ? (1u << left) - 1u : 0u;
-    if (b && c.a.key_bits)
+    if (b && j0 + 16 > s.k_full && s.k_full < s.k_len)
         b &= __ldg(c.a.key_bits + key_bit_word(s.k_row, s.seq) + j0 / 32) >> (j0 & 31);
     return b;
 }

@@ -10,16 +10,18 @@ namespace {
 
 constexpr int kBitThreads = 512;
 
-// One block per sequence: key_mask [rows_k] of int32 to one bit per key, and
-// the place after the sequence's last visible key.  Reads the mask once
-// (4 bytes a key), so that the attention kernels read 16 bytes a tile and
-// skip the tiles behind the last visible key.
+// One block per sequence: key_mask [rows_k] of int32 to one bit per key, the
+// place after the sequence's last visible key, and the number of visible keys
+// before its first hidden one.  Reads the mask once (4 bytes a key), so that
+// the attention kernels skip the tiles behind the last visible key, take those
+// before the first hidden one without a mask, and read 16 bytes for each of
+// the rest; a right-padded row needs no bits at all.
 __global__ void __launch_bounds__(kBitThreads)
 key_bits_kernel(const int32_t *__restrict__ cu_k, int len_k, long long rows_k,
-                const int32_t *__restrict__ mask, uint32_t *__restrict__ bits, int32_t *__restrict__ len)
+                const int32_t *__restrict__ mask, uint32_t *__restrict__ bits, int2 *__restrict__ len)
 {
     pdl_wait();
-    __shared__ int s_last[kBitThreads / 32];
+    __shared__ int s_last[kBitThreads / 32], s_full[kBitThreads / 32];
     const int s = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row0 = cu_k ? cu_k[s] : static_cast<long long>(s) * len_k;
     long long end = cu_k ? cu_k[s + 1] : row0 + len_k;
@@ -27,7 +29,7 @@ key_bits_kernel(const int32_t *__restrict__ cu_k, int len_k, long long rows_k,
     // the mask (nor, as words are counted from them, outside the bits)
     const bool bad = row0 < 0 || end < row0 || end > rows_k;
     const int n = bad ? 0 : static_cast<int>(end - row0);
-    int last = 0;
+    int last = 0, full = n;
     for (int j0 = 32 * warp; j0 < n; j0 += kBitThreads) {
         const int j = j0 + lane;
         const uint32_t b = __ballot_sync(0xffffffffu, j < n && mask[row0 + j] != 0);
@@ -35,15 +37,20 @@ key_bits_kernel(const int32_t *__restrict__ cu_k, int len_k, long long rows_k,
             bits[key_bit_word(row0, s) + j0 / 32] = b;
         if (b)
             last = j0 + 32 - __clz(b);
+        if (b != 0xffffffffu)
+            full = min(full, j0 + __ffs(~b) - 1);
     }
-    if (lane == 0)
+    if (lane == 0) {
         s_last[warp] = last;
+        s_full[warp] = full;
+    }
     __syncthreads();
     if (threadIdx.x < 32) {
-        int v = lane < kBitThreads / 32 ? s_last[lane] : 0;
-        v = __reduce_max_sync(0xffffffffu, v);
+        const bool mine = lane < kBitThreads / 32;
+        const int v = __reduce_max_sync(0xffffffffu, mine ? s_last[lane] : 0);
+        const int f = __reduce_min_sync(0xffffffffu, mine ? s_full[lane] : n);
         if (lane == 0)
-            len[s] = v;
+            len[s] = make_int2(v, f);
     }
     pdl_trigger();
 }
@@ -113,8 +120,8 @@ cross_join_kernel(const CrossRecord *__restrict__ records, const float *__restri
     }
     if constexpr (kGroups > 1) {
         // the groups' states, in order of the groups
-        __shared__ float s_state[kGroups][kChunks][10];
-        float *mine_s = s_state[group][chunk];
+        __shared__ float s_state[kGroups][kChunks][kRows][10];
+        float *mine_s = s_state[group][chunk][tid % kRows];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             mine_s[i] = o[i];
@@ -123,7 +130,7 @@ cross_join_kernel(const CrossRecord *__restrict__ records, const float *__restri
         __syncthreads();
         if (group == 0) {
             for (int g = 1; g < kGroups; ++g) {
-                const float *x = s_state[g][chunk];
+                const float *x = s_state[g][chunk][tid % kRows];
                 const float mn = fmaxf(m, x[8]);
                 const float wa = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_approx(m - mn);
                 const float wb = x[8] == -INFINITY ? (x[9] == 0.f ? 0.f : 1.f) : ex2_approx(x[8] - mn);
@@ -148,11 +155,17 @@ cross_join_kernel(const CrossRecord *__restrict__ records, const float *__restri
 template <int D, bool kHalf>
 cudaError_t join(const CrossArgs &a, int rows, int ctas, cudaStream_t stream)
 {
+    constexpr int kGroups = 128 / (D / 8);      // 128 threads for one row's parts
     if (rows > kCrossTokenRows)
         return launch_chained(cross_join_kernel<D, kHalf, kCrossBlockRows, 32, 1>,
                               dim3(ctas, kCrossBlockRows / 32), dim3(32 * (D / 8)), 0, stream, a.records,
                               a.parts, a.out, a.out_row);
-    constexpr int kGroups = 128 / (D / 8);
+    // more than a few rows: four to a block, with a quarter of the threads each
+    // (a block per row would be mostly blocks without work)
+    if (rows > 4)
+        return launch_chained(cross_join_kernel<D, kHalf, kCrossTokenRows, 4, kGroups / 4>,
+                              dim3(ctas, (rows + 3) / 4), dim3(128), 0, stream, a.records, a.parts, a.out,
+                              a.out_row);
     return launch_chained(cross_join_kernel<D, kHalf, kCrossTokenRows, 1, kGroups>,
                           dim3(ctas, rows), dim3(128), 0, stream, a.records, a.parts, a.out,
                           a.out_row);
@@ -160,7 +173,7 @@ cudaError_t join(const CrossArgs &a, int rows, int ctas, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t launch_key_bits(const CrossArgs &a, const int32_t *key_mask, uint32_t *bits, int32_t *len,
+cudaError_t launch_key_bits(const CrossArgs &a, const int32_t *key_mask, uint32_t *bits, int2 *len,
                             cudaStream_t stream)
 {
     return launch_chained(key_bits_kernel, dim3(a.n_seqs), dim3(kBitThreads), 0, stream, a.cu_k, a.len_k,

@@ -35,7 +35,8 @@ struct CrossSplit {
 
     // What a sequence needs: rows, tiles, blocks of query rows.
     struct Seq {
-        int q_row, q_len, k_row, k_all, k_len, tiles;   // k_len: up to the last visible key
+        int q_row, q_len, k_row, k_all, tiles;
+        int k_len, k_full;      // up to the last visible key, before the first hidden one
         int whole;              // blocks of cost kFull a tile
         int half;               // 1: the last block costs kHalf a tile
         // costs of a whole block, of one head, of the sequence
@@ -93,7 +94,12 @@ struct CrossSplit {
             q.k_row = s * a.len_k;
             q.k_all = a.len_k;
         }
-        q.k_len = a.key_len ? min(q.k_all, __ldg(a.key_len + s)) : q.k_all;
+        q.k_len = q.k_full = q.k_all;
+        if (a.key_len) {
+            const int2 v = __ldg(a.key_len + s);
+            q.k_len = min(q.k_all, v.x);
+            q.k_full = min(q.k_len, v.y);
+        }
         q.tiles = max(1, (q.k_len + kTile - 1) / kTile);
         if constexpr (kBlockQ > 0) {
             const int rest = q.q_len % kBlockQ;

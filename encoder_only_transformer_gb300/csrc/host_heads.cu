@@ -292,7 +292,7 @@ int cross_plan(const mbert_attn *h, const mbert_attn_cross_args *c, CrossPlan *p
     p->records = 0;
     p->parts = p->join ? align256(static_cast<int64_t>(sizeof(CrossRecord)) * p->ctas) : 0;
     p->lens = p->join ? align256(p->parts + 2 * p->ctas * cross_slot_floats(p->unit_rows, c->head_dim) * 4) : 0;
-    p->bits = c->key_mask ? align256(p->lens + 4ll * c->n_seqs) : p->lens;
+    p->bits = c->key_mask ? align256(p->lens + 8ll * c->n_seqs) : p->lens;
     p->bytes = c->key_mask ? align256(p->bits + 4 * (key_bit_word(c->rows_k, c->n_seqs) + 1)) : p->lens;
     return MBERT_OK;
 }
@@ -404,7 +404,7 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     const bool half = c.dtype == MBERT_F16;
     cudaError_t e = cudaSuccess;
     if (c.key_mask && keys) {
-        int32_t *lens = reinterpret_cast<int32_t *>(ws + p.lens);
+        int2 *lens = reinterpret_cast<int2 *>(ws + p.lens);
         uint32_t *bits = reinterpret_cast<uint32_t *>(ws + p.bits);
         e = launch_key_bits(a, c.key_mask, bits, lens, st);
         a.key_len = lens;

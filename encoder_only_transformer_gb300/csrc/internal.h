@@ -288,9 +288,10 @@ struct CrossArgs {
     int heads = 0, group = 1;           // query heads, query heads per key head
     float scale_log2 = 0.f;             // softmax scale in base 2
     // with a key mask: per sequence the visible keys as bits (sequence s from
-    // word key_bit_word(s) on) and the place after the last visible one
+    // word key_bit_word(s) on), the place after the last visible one, and the
+    // number of visible keys before the first hidden one
     const uint32_t *key_bits = nullptr;
-    const int32_t *key_len = nullptr;
+    const int2 *key_len = nullptr;
     int32_t *err = nullptr;
     // units cut between CTAs: a record and two part slots per CTA (null where
     // no sequence can be long enough)
@@ -324,7 +325,7 @@ constexpr long long cross_slot_floats(int rows, int dim) { return static_cast<lo
 constexpr int cross_token_ctas(int dim) { return dim == 64 ? 3 : 2; }
 
 // key_mask [rows_k] (non-zero: visible) to bits and lengths per sequence.
-cudaError_t launch_key_bits(const CrossArgs &a, const int32_t *key_mask, uint32_t *bits, int32_t *len,
+cudaError_t launch_key_bits(const CrossArgs &a, const int32_t *key_mask, uint32_t *bits, int2 *len,
                             cudaStream_t stream);
 cudaError_t launch_cross_blocks(const CrossArgs &a, int dim, bool half, int ctas, cudaStream_t stream);
 cudaError_t launch_cross_token(const CrossArgs &a, int dim, bool half, int ctas, cudaStream_t stream);

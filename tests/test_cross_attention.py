@@ -186,7 +186,7 @@ def test_tokens(built, ql, kl, H, Hk, max_q, D, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "f16")])
 @pytest.mark.parametrize("kind", ["token", "blocks"])
-@pytest.mark.parametrize("pattern", ["holes", "first", "last", "none_in_some", "tiles", "all"])
+@pytest.mark.parametrize("pattern", ["holes", "first", "last", "none_in_some", "tiles", "all", "mixed"])
 def test_key_masks(built, pattern, kind, D, dtype):
     """Masked keys hold infinities and NaN; whole tiles, ends and rows of the
     batch masked away."""
@@ -206,6 +206,11 @@ def test_key_masks(built, pattern, kind, D, dtype):
     elif pattern == "none_in_some":
         for s in (0, 2, 4):
             mask[ko[s]:ko[s + 1]] = False
+    elif pattern == "mixed":        # right-padded, whole and holed sequences by turns
+        mask[ko[0] + 200:ko[1]] = False
+        mask[ko[3] + 400] = False
+        mask[ko[3] + 700:ko[4]] = False
+        mask[ko[4] + 128:] = False
     elif pattern == "tiles":
         mask[ko[3]:ko[3] + 128] = False
         mask[ko[3] + 256:ko[3] + 512] = False
