@@ -22,15 +22,28 @@
 //                left to warps 10 and 11
 // An issuer's waits and commits take 100 to 150 clocks each, completed or not.
 // For D = 128, with its steps of 64 keys, they came to the whole period of the
-// loop; with an issuer for each product an iteration went from 3600 clocks to
-// ###.  For D = 64, where the softmax bounds the loop, the larger block would
-// only take registers from it (217 us against 194 at 8192 x 8192 keys).
+// loop; with an issuer for each product a tile of both query tiles went from
+// 3600 clocks to 2900 (the tensor cores need 2560: S of 64 keys costs them 48
+// clocks per 16 of D instead of 32 for half of 128).  For D = 64, where the
+// softmax bounds the loop, the larger block only takes registers from it:
+// 217 us against 194 (8192 queries and keys, 12 heads).
+//
 // TMEM (512 columns), fp32 except P (16-bit pairs):
 //   D = 64:   S0 S1 (128 each), P0 P1 (64 each), O0 O1 (64 each); S of the next
 //             tile is computed while the softmax works on this one
 //   D = 128:  two S of 64 keys (64 each) per query tile, O0 O1 (128 each); P
 //             takes the first half of its own S, and S of the next 64 keys is
 //             computed into the other one meanwhile
+//
+// What bounds it.  D = 64: the softmax; a query tile alone takes 1750 clocks a
+// key tile (TMEM load 290, maximum 280, exponentials 710, the rest hand-offs),
+// two together 2100 to 2200, the tensor cores' products 1024.  8192 x 8192, 12
+// heads bf16: 189 us and 6 us of joining, 1060 TFLOP/s, 0.55 of the measured
+// peak.  Steps of 64 keys with three S buffers, which overlap more, took 231
+// us: their loads, stores and waits come twice as often.  D = 128: the tensor
+// cores and the hand-offs; ragged prompts of 16 heads over 4 (fp16): 173 us and
+// 10 us of joining for 214 GFLOP, of which rounding the queries up to blocks
+// leaves 0.84.
 //
 // Softmax: online, in base 2, held in fp32.  The reference m moves (and O is
 // rescaled) only when a tile's maximum passes it by more than 8, so weights
@@ -48,11 +61,11 @@ namespace {
 
 constexpr int kMaskSlots = 4;
 
-// Costs, by a fit over the CTAs' times: a key tile for both query tiles 2100
-// (D = 64) or 2900 clocks (D = 128), for one 1900 (D = 128); a unit's fixed work
-// (the end of the softmax, the output, the refill) 2600 to 4600.
+// Costs, by a fit over the CTAs' times in clocks: a key tile for both query
+// tiles 2200 (D = 64) and 2900 (D = 128), for one 1750 and 1850; a unit's fixed
+// work (the end of the softmax, the output, the refill) 3500 and 4700.
 template <int D>
-using Split = CrossSplit<D == 64 ? 384 : 512, kCrossBlockRows, kBlockN, 6, 4, 10,
+using Split = CrossSplit<D == 64 ? 384 : 512, kCrossBlockRows, kBlockN, 6, D == 64 ? 5 : 4, 10,
                          kCrossBlockWholeKeys / kBlockN>;
 
 template <int D>

@@ -7,9 +7,14 @@
 // but for the 16; mma.sync's 16 x 8 tiles fit the rows, and their rate is far
 // above what the loads allow.  So everything serves the loads: a TMA warp
 // keeps a ring of 64-key tiles of K and V full across the borders of units,
-// three (D = 64) or two (D = 128) CTAs an SM, and the units (sequence, key head) are split by
-// cost over all CTAs (cross_sched.cuh), long ones into many parts, which a
-// second kernel joins.
+// three (D = 64) or two (D = 128) CTAs an SM (130 KB in flight), and the units
+// (sequence, key head) are split by cost over all CTAs (cross_sched.cuh), long
+// ones into many parts, which a second kernel joins.  32 sequences of 128 to
+// 8192 keys, 12 heads of 64 in rows of 24: 85 us and 4.5 us of joining for
+// 488 MB, 5.4 TB/s; the same keys with each head's rows together, 6.2 TB/s, so
+// what is left is DRAM's price for 128 bytes in every 3 KB.  (Four heads to a
+// CTA, 512 bytes in one place, gave 3 to 8 % there and lost up to 45 % on few
+// sequences, whose units then are cut into four times as many parts.)
 //
 // CTA: warps 0-3 take 16 keys of every tile each, with a softmax state of
 // their own; at the end of a segment the four states are joined in shared

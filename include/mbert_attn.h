@@ -315,7 +315,8 @@ enum {
 /* Norm of every query and key head, then the rotation, in one pass and one
  * kernel.  q and k share the rows; either may be NULL (the other is then done
  * alone).  rope == NULL (or rope->dim == 0): the norm alone, without
- * positions.  0 <= eps <= 1; statistics in fp32.  Else as mbert_attn_rotary. */
+ * positions.  0 <= eps <= 1; statistics in fp32 (numbers beyond 2^63, whose
+ * squares fp32 does not hold, give 0).  Else as mbert_attn_rotary. */
 int mbert_attn_qk_norm_rotary(mbert_attn *h, const mbert_attn_heads *q, const mbert_attn_heads *k,
                               int64_t tokens, int head_dim, int dtype, int norm, float eps,
                               const mbert_attn_rotary_spec *rope, const void *positions,
@@ -328,8 +329,8 @@ int mbert_attn_qk_norm_rotary(mbert_attn *h, const mbert_attn_heads *q, const mb
  *   out[i, h] = sum_j softmax_j(scale q[i, h] . k[j, h / g]) v[j, h / g],
  * j over the visible keys of i's sequence, g = heads / kv_heads query heads
  * sharing a key head.  No rotation, no causal mask.  A row without a visible
- * key is 0.  What invisible and other sequences' rows hold, infinities and NaN
- * included, does not matter.
+ * key (or whose visible scores are all -infinity) is 0.  What invisible and
+ * other sequences' rows hold, infinities and NaN included, does not matter.
  *   q, out       device [rows_q][heads][head_dim], rows q_row / out_row elements apart
  *   k, v         device [rows_k][kv_heads][head_dim], rows k_row / v_row apart
  *                (16-byte aligned, pitches multiples of 8 and at least the
