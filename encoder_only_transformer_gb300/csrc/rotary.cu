@@ -26,11 +26,12 @@
 // a row share its cosines and sines: the block computes its rows' once into
 // shared memory, laid out so that the lanes' 16-byte reads have no conflicts.
 //
-// Measured: 65536 rows x 12 heads of 64 bf16 32.4 us, 6.2 TB/s (0.91 of the
-// copy bandwidth); queries and keys with RMS norm 64.1 us, 6.3 TB/s; LayerNorm,
-// interleaved pairs, 96 of 128, fp16, 9001 rows x 36 heads 39.3 us, 4.2 TB/s,
-// where instructions bind (72 % of the issue slots: interleaved pairs rotate
-// one by one, LayerNorm sums twice).
+// Measured: 65536 rows x 12 heads of 64 bf16 32.3 us, 6.2 TB/s (0.92 of the
+// copy bandwidth); queries and keys with RMS norm 63.2 us, 6.4 TB/s; LayerNorm,
+// interleaved pairs, 96 of 128, fp16, 9001 rows x 36 heads 38.8 us, 4.3 TB/s,
+// where the chain of a row binds (two sums over a head's lanes, then the
+// rotation pair by pair: 280 instructions a step, 55 % of the issue slots, and
+// 64 registers leave 25 warps an SM to hide it).
 #include <cuda_fp16.h>
 
 #include "mbert_attn.h"
@@ -41,13 +42,13 @@ namespace mbert {
 namespace {
 
 // Block shape, by sweeps over the cases above: 192 threads at 64 registers and
-// two rows in flight (four: 3 to 8 % slower, fewer blocks fit; 256 threads:
-// equal on long rows, 10 % slower on 5003), and at least 16 blocks an SM (6:
-// 10 to 20 % slower, the last wave shows; 24: equal).
+// two rows in flight (four: 1 to 14 % slower, fewer blocks fit; 256 threads:
+// equal on long rows, 13 % slower on 5003), and at least 24 blocks an SM (16:
+// 1 to 2 % slower, 10: 4 to 9 %, the last wave shows).
 constexpr int kMaxThreads = 192;
 constexpr int kMinBlocks = 5;
 constexpr int kAhead = 2;               // rows in flight per thread
-constexpr int kBlocksPerSm = 16;        // blocks that the rows are cut into, at least
+constexpr int kBlocksPerSm = 24;        // blocks that the rows are cut into, at least
 constexpr int kTableBytes = 16384;      // cosines and sines of a block's rows, at most
 constexpr int kMaxRows = 64;            // rows of a block
 
@@ -56,47 +57,147 @@ struct alignas(sizeof(T) * N) Vec {
     T v[N];
 };
 
+// N numbers in fp32: neighbours share a 64-bit register pair, so that products
+// and sums take two at a time (N = 1: one by one).
+template <int N>
+struct Nums {
+    uint64_t v[N / 2];
+    __device__ __forceinline__ float get(int i) const
+    {
+        float lo, hi;
+        f2_split(v[i / 2], lo, hi);
+        return i & 1 ? hi : lo;
+    }
+    __device__ __forceinline__ void pair(int i, float lo, float hi) { v[i] = f2(lo, hi); }
+    static __device__ __forceinline__ Nums splat(float x)
+    {
+        Nums r;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            r.v[i] = f2(x, x);
+        return r;
+    }
+    __device__ __forceinline__ float sum() const
+    {
+        uint64_t t = v[0];
+#pragma unroll
+        for (int i = 1; i < N / 2; ++i)
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(v[i]));
+        float lo, hi;
+        f2_split(t, lo, hi);
+        return lo + hi;
+    }
+};
+template <>
+struct Nums<1> {
+    float v;
+    __device__ __forceinline__ float get(int) const { return v; }
+    static __device__ __forceinline__ Nums splat(float x) { return {x}; }
+    __device__ __forceinline__ float sum() const { return v; }
+};
+
+template <int N>
+__device__ __forceinline__ Nums<N> operator*(const Nums<N> &a, const Nums<N> &b)
+{
+    Nums<N> r;
+    if constexpr (N == 1)
+        r.v = a.v * b.v;
+    else
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            r.v[i] = fmul2(a.v[i], b.v[i]);
+    return r;
+}
+template <int N>
+__device__ __forceinline__ Nums<N> operator+(const Nums<N> &a, const Nums<N> &b)
+{
+    Nums<N> r;
+    if constexpr (N == 1)
+        r.v = a.v + b.v;
+    else
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v[i]) : "l"(a.v[i]), "l"(b.v[i]));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ Nums<N> operator-(const Nums<N> &a, const Nums<N> &b)
+{
+    Nums<N> r;
+    if constexpr (N == 1)
+        r.v = a.v - b.v;
+    else
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v[i]) : "l"(a.v[i]), "l"(b.v[i]));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ Nums<N> fma(const Nums<N> &a, const Nums<N> &b, const Nums<N> &c)
+{
+    Nums<N> r;
+    if constexpr (N == 1)
+        r.v = fmaf(a.v, b.v, c.v);
+    else
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            r.v[i] = ffma2(a.v[i], b.v[i], c.v[i]);
+    return r;
+}
+
+// Pairs of a type's numbers as 32 (64 for fp32) bits, to and from fp32.
+template <typename T> __device__ __forceinline__ uint64_t pair_f32(const T *x);
+template <> __device__ __forceinline__ uint64_t pair_f32(const __nv_bfloat16 *x)
+{
+    return bf16x2_to_f2(*reinterpret_cast<const uint32_t *>(x));
+}
+template <> __device__ __forceinline__ uint64_t pair_f32(const __half *x)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(x));
+    return f2(f.x, f.y);
+}
+template <> __device__ __forceinline__ uint64_t pair_f32(const float *x) { return *reinterpret_cast<const uint64_t *>(x); }
+
+__device__ __forceinline__ void pair_store(__nv_bfloat16 *x, uint64_t v) { *reinterpret_cast<uint32_t *>(x) = f2_to_bf16x2(v); }
+__device__ __forceinline__ void pair_store(__half *x, uint64_t v)
+{
+    float lo, hi;
+    f2_split(v, lo, hi);
+    *reinterpret_cast<__half2 *>(x) = __floats2half2_rn(lo, hi);
+}
+__device__ __forceinline__ void pair_store(float *x, uint64_t v) { *reinterpret_cast<uint64_t *>(x) = v; }
+
 template <typename T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32(float v) { return v; }
 template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f32(float &x, float v) { x = v; }
+__device__ __forceinline__ void from_f32(__half &x, float v) { x = __float2half_rn(v); }
+__device__ __forceinline__ void from_f32(__nv_bfloat16 &x, float v) { x = __float2bfloat16_rn(v); }
 
 template <typename T, int N>
-__device__ __forceinline__ void unpack(const Vec<T, N> &x, float (&f)[N])
+__device__ __forceinline__ Nums<N> unpack(const Vec<T, N> &x)
 {
+    Nums<N> r;
+    if constexpr (N == 1)
+        r.v = to_f32<T>(x.v[0]);
+    else
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        f[i] = to_f32<T>(x.v[i]);
+        for (int i = 0; i < N / 2; ++i)
+            r.v[i] = pair_f32<T>(&x.v[2 * i]);
+    return r;
 }
-
-template <int N>
-__device__ __forceinline__ void pack(const float (&f)[N], Vec<float, N> &x)
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> pack(const Nums<N> &f)
 {
+    Vec<T, N> x;
+    if constexpr (N == 1)
+        from_f32(x.v[0], f.v);
+    else
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        x.v[i] = f[i];
-}
-template <int N>
-__device__ __forceinline__ void pack(const float (&f)[N], Vec<__half, N> &x)
-{
-    if constexpr (N == 1) {
-        x.v[0] = __float2half_rn(f[0]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 2)
-            *reinterpret_cast<__half2 *>(&x.v[i]) = __floats2half2_rn(f[i], f[i + 1]);
-    }
-}
-template <int N>
-__device__ __forceinline__ void pack(const float (&f)[N], Vec<__nv_bfloat16, N> &x)
-{
-    if constexpr (N == 1) {
-        x.v[0] = __float2bfloat16_rn(f[0]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 2)
-            *reinterpret_cast<__nv_bfloat162 *>(&x.v[i]) = __floats2bfloat162_rn(f[i], f[i + 1]);
-    }
+        for (int i = 0; i < N / 2; ++i)
+            pair_store(&x.v[2 * i], f.v[i]);
+    return x;
 }
 
 // One vector of a thread from global to shared memory, without a register:
@@ -115,46 +216,6 @@ __device__ __forceinline__ void fetch(void *smem, const void *gmem)
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
 __device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kPending) : "memory"); }
-
-// Two fp32 products or sums per instruction where N is even.
-template <int N>
-__device__ __forceinline__ void mul_to(float (&y)[N], const float (&a)[N], const float (&b)[N])
-{
-    if constexpr (N == 1) {
-        y[0] = a[0] * b[0];
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 2)
-            f2_split(fmul2(f2(a[i], a[i + 1]), f2(b[i], b[i + 1])), y[i], y[i + 1]);
-    }
-}
-template <int N>
-__device__ __forceinline__ void fma_to(float (&y)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N])
-{
-    if constexpr (N == 1) {
-        y[0] = fmaf(a[0], b[0], c[0]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 2)
-            f2_split(ffma2(f2(a[i], a[i + 1]), f2(b[i], b[i + 1]), f2(c[i], c[i + 1])), y[i], y[i + 1]);
-    }
-}
-
-template <int N>
-__device__ __forceinline__ void add_to(float (&y)[N], const float (&a)[N], const float (&b)[N])
-{
-    if constexpr (N == 1) {
-        y[0] = a[0] + b[0];
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            float p = a[i], q = a[i + 1];
-            fadd2(p, q, b[i], b[i + 1]);
-            y[i] = p;
-            y[i + 1] = q;
-        }
-    }
-}
 
 // Sum over the `lanes` (a power of two) neighbouring lanes of a head.
 __device__ __forceinline__ float head_sum(float s, int lanes)
@@ -219,16 +280,22 @@ __device__ __forceinline__ int table_place(int m, int rot_slots)
 }
 
 template <int VW>
-__device__ __forceinline__ void table_read(const float *t, int slot, int rot_slots, float (&c)[VW])
+__device__ __forceinline__ Nums<VW> table_read(const float *t, int slot, int rot_slots)
 {
-    if constexpr (VW == 8) {
-        *reinterpret_cast<float4 *>(&c[0]) = *reinterpret_cast<const float4 *>(t + 4 * slot);
-        *reinterpret_cast<float4 *>(&c[4]) = *reinterpret_cast<const float4 *>(t + 4 * (rot_slots + slot));
-    } else {
+    Nums<VW> c;
+    if constexpr (VW >= 4) {
 #pragma unroll
-        for (int i = 0; i < VW; ++i)
-            c[i] = t[VW * slot + i];
+        for (int q = 0; q < VW / 4; ++q) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(t + 4 * (q * rot_slots + slot));
+            c.v[2 * q] = x.x;
+            c.v[2 * q + 1] = x.y;
+        }
+    } else if constexpr (VW == 2) {
+        c.v[0] = *reinterpret_cast<const uint64_t *>(t + 2 * slot);
+    } else {
+        c.v = t[slot];
     }
+    return c;
 }
 
 // VW numbers per vector; SPL slots per lane (more than one only where a head
@@ -282,6 +349,16 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
         fetch_commit();
         src += src_step;
     };
+    // places that no row fills hold zeros, so that sums need no selection
+#pragma unroll
+    for (int j = 0; j < SPL; ++j)
+        if (!placed || slot0 + 32 * j >= slots) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                s_rows[((u * SPL + j) * 2) * threads + tid] = V{};
+                s_rows[((u * SPL + j) * 2 + 1) * threads + tid] = V{};
+            }
+        }
     // the first rows are on their way while the table is made
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
@@ -319,7 +396,7 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
     }
     __syncthreads();
 
-    float w0[SPL][VW], w1[SPL][VW];
+    Nums<VW> w0[SPL], w1[SPL];
     if constexpr (kNorm) {
 #pragma unroll
         for (int j = 0; j < SPL; ++j) {
@@ -328,133 +405,89 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
                 w = *reinterpret_cast<const V *>(static_cast<const T *>(x.weight) + off0[j]);
                 z = *reinterpret_cast<const V *>(static_cast<const T *>(x.weight) + off1[j]);
             }
-            unpack(w, w0[j]);
-            unpack(z, w1[j]);
+            w0[j] = unpack(w);
+            w1[j] = unpack(z);
         }
     }
     const float inv_dim = 1.f / a.dim;
     const int lanes = 1 << a.lanes_log2;
+    const float *trow = s_table + 2 * half * team;          // of the step's row
+    const int tstep = 2 * half * a.teams;
     auto step = [&](int r0, int u) {
-            const int r = r0 + team;
-            float f0[SPL][VW], f1[SPL][VW];
-            fetch_wait<kAhead - 1>();
+        const int r = r0 + team;
+        Nums<VW> f0[SPL], f1[SPL];
+        fetch_wait<kAhead - 1>();
+#pragma unroll
+        for (int j = 0; j < SPL; ++j) {
+            f0[j] = unpack(s_rows[((u * SPL + j) * 2) * threads + tid]);
+            f1[j] = unpack(s_rows[((u * SPL + j) * 2 + 1) * threads + tid]);
+        }
+        // the place is free for a later row
+        load(r + kAhead * a.teams, u);
+        if constexpr (kNorm) {
+            // statistics in fp32 over the head's lanes; LayerNorm in two passes
+            // (mean, then squared deviations)
+            if (a.norm == MBERT_NORM_LAYER) {
+                Nums<VW> t = f0[0] + f1[0];
+#pragma unroll
+                for (int j = 1; j < SPL; ++j)
+                    t = t + (f0[j] + f1[j]);
+                const Nums<VW> mean = Nums<VW>::splat(head_sum(t.sum(), lanes) * inv_dim);
+#pragma unroll
+                for (int j = 0; j < SPL; ++j)
+                    if (slot0 + 32 * j < slots) {
+                        f0[j] = f0[j] - mean;
+                        f1[j] = f1[j] - mean;
+                    }
+            }
+            Nums<VW> q = f0[0] * f0[0];
+            q = fma(f1[0], f1[0], q);
+#pragma unroll
+            for (int j = 1; j < SPL; ++j) {
+                q = fma(f0[j], f0[j], q);
+                q = fma(f1[j], f1[j], q);
+            }
+            const Nums<VW> inv = Nums<VW>::splat(rsqrtf(fmaf(head_sum(q.sum(), lanes), inv_dim, a.eps)));
 #pragma unroll
             for (int j = 0; j < SPL; ++j) {
-                V x0{}, x1{};
-                if (placed && slot0 + 32 * j < slots) {
-                    x0 = s_rows[((u * SPL + j) * 2) * threads + tid];
-                    x1 = s_rows[((u * SPL + j) * 2 + 1) * threads + tid];
-                }
-                unpack(x0, f0[j]);
-                unpack(x1, f1[j]);
+                f0[j] = f0[j] * inv * w0[j];
+                f1[j] = f1[j] * inv * w1[j];
             }
-            // the place is free for a later row
-            load(r + kAhead * a.teams, u);
-            if constexpr (kNorm) {
-                // statistics in fp32 over the head's lanes; LayerNorm in two
-                // passes (mean, then squared deviations)
-                float q[VW];
-                if (a.norm == MBERT_NORM_LAYER) {
-                    add_to(q, f0[0], f1[0]);
+        }
+        if (placed && r < rows && s_live[r]) {
 #pragma unroll
-                    for (int j = 1; j < SPL; ++j) {
-                        add_to(q, q, f0[j]);
-                        add_to(q, q, f1[j]);
-                    }
-                    float s = q[0];
+            for (int j = 0; j < SPL; ++j) {
+                const int s = slot0 + 32 * j;
+                if (s >= slots)
+                    continue;
+                if (s < rot_slots) {
+                    const Nums<VW> c = table_read<VW>(trow, s, rot_slots);
+                    const Nums<VW> sn = table_read<VW>(trow + half, s, rot_slots);
+                    if constexpr (!kInterleaved) {
+                        const Nums<VW> y = f0[j] * c - f1[j] * sn;
+                        f1[j] = fma(f0[j], sn, f1[j] * c);
+                        f0[j] = y;
+                    } else if constexpr (VW == 1) {
+                        const float y = f0[j].v * c.v - f1[j].v * sn.v;
+                        f1[j].v = f1[j].v * c.v + f0[j].v * sn.v;
+                        f0[j].v = y;
+                    } else {
+                        // pairs are neighbours: (0, 1), (2, 3), ... over both vectors
 #pragma unroll
-                    for (int i = 1; i < VW; ++i)
-                        s += q[i];
-                    const float mean = head_sum(s, lanes) * inv_dim;
-#pragma unroll
-                    for (int i = 0; i < VW; ++i)
-                        q[i] = -mean;
-#pragma unroll
-                    for (int j = 0; j < SPL; ++j)
-                        if (slot0 + 32 * j < slots) {
-                            add_to(f0[j], f0[j], q);
-                            add_to(f1[j], f1[j], q);
-                        }
-                }
-                mul_to(q, f0[0], f0[0]);
-                fma_to(q, f1[0], f1[0], q);
-#pragma unroll
-                for (int j = 1; j < SPL; ++j) {
-                    fma_to(q, f0[j], f0[j], q);
-                    fma_to(q, f1[j], f1[j], q);
-                }
-                float sum = q[0];
-#pragma unroll
-                for (int i = 1; i < VW; ++i)
-                    sum += q[i];
-                sum = head_sum(sum, lanes);
-                const float inv = rsqrtf(fmaf(sum, inv_dim, a.eps));
-                float scale[VW];
-#pragma unroll
-                for (int i = 0; i < VW; ++i)
-                    scale[i] = inv;
-#pragma unroll
-                for (int j = 0; j < SPL; ++j) {
-                    mul_to(f0[j], f0[j], scale);
-                    mul_to(f1[j], f1[j], scale);
-                    mul_to(f0[j], f0[j], w0[j]);
-                    mul_to(f1[j], f1[j], w1[j]);
-                }
-            }
-            if (placed && r < rows && s_live[r]) {
-                const float *row = s_table + 2 * half * r;
-#pragma unroll
-                for (int j = 0; j < SPL; ++j) {
-                    const int s = slot0 + 32 * j;
-                    if (s >= slots)
-                        continue;
-                    if (s < rot_slots) {
-                        float c[VW], sn[VW];
-                        table_read<VW>(row, s, rot_slots, c);
-                        table_read<VW>(row + half, s, rot_slots, sn);
-                        if constexpr (kInterleaved) {
-                            // pairs are neighbours: (0, 1), (2, 3), ... over both vectors
-                            float y[2 * VW];
-#pragma unroll
-                            for (int i = 0; i < VW; ++i) {
-                                y[i] = f0[j][i];
-                                y[VW + i] = f1[j][i];
-                            }
-#pragma unroll
-                            for (int m = 0; m < VW; ++m) {
-                                const float p = y[2 * m], q2 = y[2 * m + 1];
-                                y[2 * m] = p * c[m] - q2 * sn[m];
-                                y[2 * m + 1] = q2 * c[m] + p * sn[m];
-                            }
-#pragma unroll
-                            for (int i = 0; i < VW; ++i) {
-                                f0[j][i] = y[i];
-                                f1[j][i] = y[VW + i];
-                            }
-                        } else {
-                            float p[VW], q2[VW], ns[VW];
-#pragma unroll
-                            for (int i = 0; i < VW; ++i)
-                                ns[i] = -sn[i];
-                            mul_to(p, f0[j], c);
-                            mul_to(q2, f1[j], c);
-                            fma_to(p, f1[j], ns, p);
-                            fma_to(q2, f0[j], sn, q2);
-#pragma unroll
-                            for (int i = 0; i < VW; ++i) {
-                                f0[j][i] = p[i];
-                                f1[j][i] = q2[i];
-                            }
+                        for (int m = 0; m < VW; ++m) {
+                            Nums<VW> &f = m < VW / 2 ? f0[j] : f1[j];
+                            const int at = m % (VW / 2);
+                            const float p = f.get(2 * at), q = f.get(2 * at + 1), cm = c.get(m), sm = sn.get(m);
+                            f.pair(at, p * cm - q * sm, q * cm + p * sm);
                         }
                     }
-                    V o0, o1;
-                    pack(f0[j], o0);
-                    pack(f1[j], o1);
-                    *reinterpret_cast<V *>(dst + off0[j]) = o0;
-                    *reinterpret_cast<V *>(dst + off1[j]) = o1;
                 }
+                *reinterpret_cast<V *>(dst + off0[j]) = pack<T, VW>(f0[j]);
+                *reinterpret_cast<V *>(dst + off1[j]) = pack<T, VW>(f1[j]);
             }
-            dst += dst_step;
+        }
+        dst += dst_step;
+        trow += tstep;
     };
 #pragma unroll 1
     for (int r0 = 0, u = 0; r0 < rows; r0 += a.teams, u = (u + 1) % kAhead)
