@@ -7,8 +7,12 @@
 // Work: a unit is 256 query rows of one sequence and head (two tiles of 128);
 // units and their 128-key tiles are split among one CTA per SM by cost
 // (cross_sched.cuh), and units cut between CTAs are joined by a second kernel
-// (cross_join.cu) in a fixed order.  Query heads that share a key head read
-// the same key columns; the copies after the first come from L2.
+// (cross_join.cu) in a fixed order.  Query heads that share a key head share
+// the blocks too: with F the largest power of two that divides their number,
+// row r of a unit is query r / F, head r % F (a 3-D tensor map fetches them
+// so), which leaves fewer rows empty at a sequence's end (ragged prompts of 16
+// heads over 4: 179 -> 170 us) and makes few rows of many heads one unit
+// instead of F.
 //
 // CTA (12 warps for D = 64, 16 for D = 128):
 //   warps 0-3    softmax group 0 (query tile 0, TMEM lanes 0..127, a thread a row)
@@ -38,12 +42,11 @@
 // What bounds it.  D = 64: the softmax; a query tile alone takes 1750 clocks a
 // key tile (TMEM load 290, maximum 280, exponentials 710, the rest hand-offs),
 // two together 2100 to 2200, the tensor cores' products 1024.  8192 x 8192, 12
-// heads bf16: 189 us and 6 us of joining, 1060 TFLOP/s, 0.55 of the measured
+// heads bf16: 185 us and 6 us of joining, 1080 TFLOP/s, 0.56 of the measured
 // peak.  Steps of 64 keys with three S buffers, which overlap more, took 231
 // us: their loads, stores and waits come twice as often.  D = 128: the tensor
-// cores and the hand-offs; ragged prompts of 16 heads over 4 (fp16): 173 us and
-// 10 us of joining for 214 GFLOP, of which rounding the queries up to blocks
-// leaves 0.84.
+// cores and the hand-offs; ragged prompts of 16 heads over 4 (fp16): 160 us and
+// 10 us of joining for 214 GFLOP, 1260 TFLOP/s, 0.65 of the peak.
 //
 // Softmax: online, in base 2, held in fp32.  The reference m moves (and O is
 // rescaled) only when a tile's maximum passes it by more than 8, so weights
@@ -136,9 +139,9 @@ __device__ __forceinline__ constexpr uint32_t idesc(int M, int N, bool b_mn_majo
 // loads and 64-bit divisions, 3500 clocks that stood between the segments when
 // every warp did it for itself.
 struct alignas(16) Rec {
-    int q_row, q_len, q0, k_row, k_len;
+    int q_row, rows, q0, k_row, k_len;  // first query, rows (queries times F), the unit's first row
     int kb, ke, tiles;      // key tiles [kb, ke) of tiles; ke = 0: no more segments
-    int head, seq;
+    int head, seq;          // first query head of the unit, sequence
     int parts;              // of a cut unit whose first part this is
     int k_full;             // keys before the first hidden one
 };
@@ -174,7 +177,7 @@ __device__ __forceinline__ bool needs_mask(const Rec &s, int k) { return s.k_ful
 __device__ __forceinline__ bool needs_bits(const Rec &s) { return s.k_full < s.k_len; }
 
 // The unit's second query tile holds rows.
-__device__ __forceinline__ bool second_tile(const Rec &s) { return s.q_len - s.q0 > kBlockM; }
+__device__ __forceinline__ bool second_tile(const Rec &s) { return s.rows - s.q0 > kBlockM; }
 
 // Steps of a segment: a last tile of at most 64 keys takes one step of 64.
 template <int D>
@@ -197,7 +200,7 @@ __device__ void producer(const Ctx &c, const Split<D> &split)
         Rec s{};
         if (split.next(it, seg)) {
             s.q_row = seg.s.q_row;
-            s.q_len = seg.s.q_len;
+            s.rows = seg.s.rows;
             s.q0 = seg.q0;
             s.k_row = seg.s.k_row;
             s.k_len = seg.s.k_len;
@@ -205,7 +208,7 @@ __device__ void producer(const Ctx &c, const Split<D> &split)
             s.kb = seg.kb;
             s.ke = seg.ke;
             s.tiles = seg.s.tiles;
-            s.head = seg.head;
+            s.head = seg.head << c.a.fold_log2;
             s.seq = seg.seq;
             s.parts = seg.kb == 0 && seg.ke < seg.s.tiles ? split.parts(seg) : 0;
         }
@@ -220,14 +223,14 @@ __device__ void producer(const Ctx &c, const Split<D> &split)
         const bool two = second_tile(s);
         if (sg >= L::kQSets && !mbar_wait(bar(c, kBarQEmpty + qs), (sg / L::kQSets - 1) & 1, err))
             return;
-        const int col_q = s.head * D, col_k = s.head / c.a.group * D;
-        const int qrow = s.q_row + s.q0;
+        const int col_k = s.head / c.a.group * D;
+        const int fold = c.a.fold_log2, qrow = s.q_row + (s.q0 >> fold);
         const uint32_t qdst = c.base + qs * 2 * L::kTile;
         mbar_arrive_expect_tx(bar(c, kBarQFull + qs), (two ? 2 : 1) * L::kTile);
         for (int w = 0; w < (two ? 2 : 1); ++w)
             for (int h = 0; h < L::kHalves; ++h)
-                tma_load_2d(qdst + w * L::kTile + h * kTileBytes, &c.a.tm_q, col_q + 64 * h, qrow + w * kBlockM,
-                            bar(c, kBarQFull + qs));
+                tma_load_3d(qdst + w * L::kTile + h * kTileBytes, &c.a.tm_q, 64 * h, s.head,
+                            qrow + w * (kBlockM >> fold), bar(c, kBarQFull + qs));
         for (int k = s.kb; k < s.ke; ++k, ++g) {
             const int st = g % L::kStages;
             const uint32_t u = g / L::kStages;
@@ -751,9 +754,10 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
         float *part = c.a.parts + (2ll * cta + (s.kb == 0)) * cross_slot_floats(kCrossBlockRows, D);
         // this warp's rows of the output, those that the sequence has
         const int warp_row = kBlockM * w + 32 * warp_in_group;
-        const int warp_rows = min(32, s.q_len - s.q0 - warp_row);
-        uint16_t *out = static_cast<uint16_t *>(c.a.out) +
-                        (static_cast<long long>(s.q_row) + s.q0 + warp_row) * c.a.out_row + s.head * D;
+        const int warp_rows = min(32, s.rows - s.q0 - warp_row);
+        const int fold = c.a.fold_log2;
+        uint16_t *out = static_cast<uint16_t *>(c.a.out) + static_cast<long long>(s.q_row) * c.a.out_row +
+                        static_cast<long long>(s.head) * D;
         uint8_t *stage = c.sbase + L::kOffOut + (4 * w + warp_in_group) * 4096;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -785,11 +789,13 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                                    pack2<kHalf>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
                                    pack2<kHalf>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
                 __syncwarp();
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < 8; ++i) {
                     const int row = 4 * i + lane / 8, part = lane % 8;
+                    const int at = s.q0 + warp_row + row;       // row of the sequence
                     if (row < warp_rows)
-                        *reinterpret_cast<uint4 *>(out + row * c.a.out_row + 64 * h + 8 * part) =
+                        *reinterpret_cast<uint4 *>(out + (at >> fold) * c.a.out_row +
+                                                   (at & ((1 << fold) - 1)) * D + 64 * h + 8 * part) =
                             *reinterpret_cast<const uint4 *>(stage + 128 * row + 16 * (part ^ (row & 7)));
                 }
                 __syncwarp();
@@ -805,10 +811,10 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
             reinterpret_cast<float2 *>(part + kCrossBlockRows * D)[rr] = make_float2(m, l);
         if (!whole && s.kb == 0 && rr == 0) {
             CrossRecord rec;
-            rec.row0 = static_cast<long long>(s.q_row) + s.q0;
-            rec.rows = min(kCrossBlockRows, s.q_len - s.q0);
+            rec.row0 = static_cast<long long>(s.q_row) + (s.q0 >> fold);
+            rec.rows = min(kCrossBlockRows, s.rows - s.q0);
             rec.head0 = s.head;
-            rec.group = 1;
+            rec.group = 1 << fold;
             rec.parts = s.parts;
             c.a.records[cta] = rec;
         }
@@ -830,7 +836,7 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
 
     if (threadIdx.x == 0 && a.records)
         a.records[cta].parts = 0;
-    Split<D> split(a, a.heads);
+    Split<D> split(a, a.heads >> a.fold_log2);
     // two tiles and a unit's fixed work per CTA at least
     const bool work = split.find(*reinterpret_cast<typename Split<D>::Scratch *>(sbase + L::kOffScratch), gridDim.x, 22);
     if (work) {

@@ -20,7 +20,8 @@
 
 namespace mbert {
 
-// kBlockQ: query rows of a unit (0: all of a sequence's); kTile: keys of a tile.
+// kBlockQ: query rows of a unit (0: all of a sequence's), each the rows of
+// 2^fold_log2 heads, side by side; kTile: keys of a tile.
 template <int kThreads, int kBlockQ_, int kTile_, int kFull_, int kHalf_, int kAlpha_, int kSnap_>
 struct CrossSplit {
     static constexpr int kBlockQ = kBlockQ_, kTile = kTile_, kSnap = kSnap_;
@@ -36,6 +37,7 @@ struct CrossSplit {
     // What a sequence needs: rows, tiles, blocks of query rows.
     struct Seq {
         int q_row, q_len, k_row, k_all, tiles;
+        int rows;               // q_len times the heads that share a block
         int k_len, k_full;      // up to the last visible key, before the first hidden one
         int whole;              // blocks of cost kFull a tile
         int half;               // 1: the last block costs kHalf a tile
@@ -102,10 +104,12 @@ struct CrossSplit {
         }
         q.tiles = max(1, (q.k_len + kTile - 1) / kTile);
         if constexpr (kBlockQ > 0) {
-            const int rest = q.q_len % kBlockQ;
+            q.rows = q.q_len << a.fold_log2;
+            const int rest = q.rows % kBlockQ;
             q.half = kHalf != kFull && rest > 0 && rest <= kBlockQ / 2;
-            q.whole = q.q_len / kBlockQ + (rest > 0 && !q.half);
+            q.whole = q.rows / kBlockQ + (rest > 0 && !q.half);
         } else {
+            q.rows = q.q_len;
             q.half = 0;
             q.whole = q.q_len > 0;
         }

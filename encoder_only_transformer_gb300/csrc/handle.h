@@ -77,6 +77,12 @@ namespace mbert {
 int encode_rows(const mbert_attn *h, CUtensorMap *tm, const void *ptr, int64_t width, int64_t rows,
                 int64_t pitch, int box, int l2_bytes);
 
+// 3-D tensor map of 16-bit elements over [rows][heads][dim], box 64 columns x
+// `fold` heads x 128 / fold rows (128 rows of shared memory, a row's heads side
+// by side); otherwise as encode_rows.
+int encode_heads(const mbert_attn *h, CUtensorMap *tm, const void *ptr, int dim, int64_t heads, int64_t rows,
+                 int64_t pitch, int fold);
+
 struct DeviceGuard {
     int prev = -1;
     bool changed = false;

@@ -214,6 +214,20 @@ int mbert::encode_rows(const mbert_attn *h, CUtensorMap *tm, const void *ptr, in
     return r == CUDA_SUCCESS ? MBERT_OK : MBERT_ERR_CUDA;
 }
 
+int mbert::encode_heads(const mbert_attn *h, CUtensorMap *tm, const void *ptr, int dim, int64_t heads,
+                        int64_t rows, int64_t pitch, int fold)
+{
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(dim) * 2, static_cast<cuuint64_t>(pitch) * 2};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(kHeadDim), static_cast<cuuint32_t>(fold),
+                         static_cast<cuuint32_t>(kBlockM / fold)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = h->encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MBERT_OK : MBERT_ERR_CUDA;
+}
+
 MBERT_API int mbert_attn_default_config(mbert_attn_config *cfg)
 {
     if (!cfg)

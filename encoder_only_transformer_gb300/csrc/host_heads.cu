@@ -254,6 +254,7 @@ struct CrossPlan {
     bool token;             // few rows per sequence and key head
     bool join;              // a sequence may be long enough to be cut
     int group, max_q, ctas, unit_rows;
+    int fold_log2;          // blocks: query heads that share a block's rows
     int64_t records, parts, lens, bits, bytes;      // offsets and the total
 };
 
@@ -287,6 +288,11 @@ int cross_plan(const mbert_attn *h, const mbert_attn_cross_args *c, CrossPlan *p
     p->token = most * p->group <= kCrossTokenRows;
     p->ctas = p->token ? h->num_sms * cross_token_ctas(c->head_dim) : h->num_sms;
     p->unit_rows = p->token ? kCrossTokenRows : kCrossBlockRows;
+    p->fold_log2 = 0;
+    while (!p->token && p->fold_log2 < 7 && (p->group >> p->fold_log2) % 2 == 0)
+        ++p->fold_log2;
+    if (most << p->fold_log2 > INT32_MAX)
+        return MBERT_ERR_BAD_ARG;   // (more than any device holds)
     const int64_t longest = c->cu_k || c->n_seqs == 0 ? c->rows_k : c->rows_k / c->n_seqs;
     p->join = longest > (p->token ? kCrossTokenWholeKeys : kCrossBlockWholeKeys);
     p->records = 0;
@@ -373,7 +379,8 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     // (672 MB from DRAM for 488 MB of keys and values).
     const int l2 = 2 * D;
     // without any key row the maps stand over q: all of it is masked
-    if ((!p.token && encode_rows(h, &a.tm_q, c.q, qw, c.rows_q, c.q_row, kBlockM, l2) != MBERT_OK) ||
+    if ((!p.token &&
+         encode_heads(h, &a.tm_q, c.q, D, c.heads, c.rows_q, c.q_row, 1 << p.fold_log2) != MBERT_OK) ||
         encode_rows(h, &a.tm_k, keys ? c.k : c.q, keys ? kw : qw, keys ? c.rows_k : c.rows_q,
                     keys ? c.k_row : c.q_row, kbox, l2) != MBERT_OK ||
         encode_rows(h, &a.tm_v, keys ? c.v : c.q, keys ? kw : qw, keys ? c.rows_k : c.rows_q,
@@ -393,6 +400,7 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     a.max_q = p.max_q;
     a.heads = c.heads;
     a.group = p.group;
+    a.fold_log2 = p.fold_log2;
     a.scale_log2 = static_cast<float>((c.scale > 0.f ? c.scale : 1.0 / std::sqrt(static_cast<double>(D))) *
                                       1.4426950408889634);
     a.err = h->err;

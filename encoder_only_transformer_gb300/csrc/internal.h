@@ -277,7 +277,8 @@ cudaError_t launch_rotary(RotaryArgs &a, int num_sms, cudaStream_t stream);
 // (attn_cross.cu: blocks of queries; attn_cross_token.cu: few rows a
 // sequence; cross_join.cu: what goes before and after).
 struct CrossArgs {
-    CUtensorMap tm_q, tm_k, tm_v;       // [rows][heads * D], box 64 columns
+    CUtensorMap tm_q;                   // [rows][heads][D], box 64 columns x 2^fold_log2 heads (blocks)
+    CUtensorMap tm_k, tm_v;             // [rows][heads * D], box 64 columns
     const void *q = nullptr;
     void *out = nullptr;
     long long q_row = 0, out_row = 0;   // row strides in elements
@@ -286,6 +287,7 @@ struct CrossArgs {
     long long rows_q = 0, rows_k = 0;
     int max_q = 0;                      // longest query sequence accepted
     int heads = 0, group = 1;           // query heads, query heads per key head
+    int fold_log2 = 0;                  // query heads that share a block's rows (blocks)
     float scale_log2 = 0.f;             // softmax scale in base 2
     // with a key mask: per sequence the visible keys as bits (sequence s from
     // word key_bit_word(s) on), the place after the last visible one, and the

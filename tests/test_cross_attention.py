@@ -150,6 +150,12 @@ BLOCKS = [
     ([17], [2500], 12, 12),
     ([513, 20], [900, 1300], 6, 3),
     ([20] * 40, list(range(0, 400, 10)), 2, 1),
+    ([21, 1, 0, 65, 33], [300, 500, 10, 129, 0], 8, 1),         # eight heads share a block's rows
+    ([5, 11], [700, 900], 32, 1),
+    ([1, 3, 130], [200, 64, 90], 256, 1),                       # 128 of 256 heads share them
+    ([50, 7], [130, 400], 12, 2),                               # two of six
+    ([40], [333], 9, 3),                                        # none of three
+    ([300, 129], [140, 700], 16, 4),
 ]
 
 
