@@ -8,8 +8,9 @@
 // of n owns the tiles that begin in [c X / n, (c + 1) X / n), X the line's
 // length; so every CTA gets the same cost whatever the lengths of the
 // sequences, and a long unit among few is cut between many CTAs.  A border
-// that falls into a unit of kSnap tiles or fewer moves to that unit's start:
-// joining its parts would cost more than it evens out.
+// that falls into a unit of kSnap tiles or fewer (into any, where the call has
+// no records of cut units) moves to that unit's start: joining its parts would
+// cost more than it evens out.
 //
 // No list of the work is made: each CTA sums the sequences' costs and finds
 // its own range, one thread per sequence.
@@ -223,7 +224,7 @@ struct CrossSplit {
         if (s < 0)
             return x;
         const Seq q = load(s);
-        if (q.tiles > kSnap)
+        if (a.records && q.tiles > kSnap)
             return x;
         return place(q, base, x).xa;
     }

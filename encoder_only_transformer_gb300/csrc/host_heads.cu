@@ -294,7 +294,7 @@ int cross_plan(const mbert_attn *h, const mbert_attn_cross_args *c, CrossPlan *p
     if (most << p->fold_log2 > INT32_MAX)
         return MBERT_ERR_BAD_ARG;   // (more than any device holds)
     const int64_t longest = c->cu_k || c->n_seqs == 0 ? c->rows_k : c->rows_k / c->n_seqs;
-    p->join = longest > (p->token ? kCrossTokenWholeKeys : kCrossBlockWholeKeys);
+    p->join = longest > (p->token ? kCrossTokenWholeRows : kCrossBlockWholeRows);
     p->records = 0;
     p->parts = p->join ? align256(static_cast<int64_t>(sizeof(CrossRecord)) * p->ctas) : 0;
     p->lens = p->join ? align256(p->parts + 2 * p->ctas * cross_slot_floats(p->unit_rows, c->head_dim) * 4) : 0;

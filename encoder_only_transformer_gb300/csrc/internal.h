@@ -312,11 +312,17 @@ struct CrossRecord {
 constexpr int kCrossBlockRows = 256;    // rows of a unit of attn_cross.cu
 constexpr int kCrossTokenRows = 16;     // rows of a unit of attn_cross_token.cu
 
-// Units of at most this many keys are never cut between CTAs (blocks of
-// queries, single tokens): up to there joining parts costs more than it evens
-// out, and a call with no more key rows needs no joining kernel.
-constexpr int kCrossBlockWholeKeys = 512;
-constexpr int kCrossTokenWholeKeys = 1024;
+// Units of at most this many keys are not cut between CTAs (blocks of queries,
+// single tokens): up to there joining parts costs more than it evens out
+// (ragged blocks over 300 to 700 keys 24.8 us against 27.6 with 512; tokens over
+// four times 1000 keys 10.3 us against 15.0 with 1024).
+constexpr int kCrossBlockWholeKeys = 256;
+constexpr int kCrossTokenWholeKeys = 512;
+// In a call whose sequences can have no more keys than this none is cut, which
+// saves the joining kernel and the workspace (tokens over four times 200 keys 6.7 us
+// against 9.7).
+constexpr int kCrossBlockWholeRows = 512;
+constexpr int kCrossTokenWholeRows = 1024;
 
 // First word of sequence s's key bits: every sequence starts a new word.
 __host__ __device__ inline long long key_bit_word(long long k_row, int s) { return k_row / 32 + s; }
