@@ -523,9 +523,13 @@ cudaError_t launch(RotaryArgs &a, int num_sms, cudaStream_t stream)
     const int fit = kMaxThreads / lanes;
     const int shares = (heads + fit - 1) / fit;
     a.block_heads = (heads + shares - 1) / shares;
+    // (no more than a block may have rows: heads of up to 32 numbers, one or two
+    // of them, would fit more)
+    int most = a.rot ? kTableBytes / (4 * a.rot) : kMaxRows;
+    most = most > kMaxRows ? kMaxRows : most;
     int threads = 0;
     double best = -1.0;
-    for (int t = 1; t * a.block_heads * lanes <= kMaxThreads && t <= a.tokens; ++t) {
+    for (int t = 1; t * a.block_heads * lanes <= kMaxThreads && t <= a.tokens && t <= most; ++t) {
         const int th = (t * a.block_heads * lanes + 31) / 32 * 32;
         const double use = static_cast<double>(t * a.block_heads * lanes) / th + (th >= 192 ? 0.5 : th / 384.0);
         if (use > best + 1e-9) {
@@ -537,17 +541,13 @@ cudaError_t launch(RotaryArgs &a, int num_sms, cudaStream_t stream)
     // Rows of a block: what the table holds, fewer while that leaves less than
     // kBlocksPerSm blocks per SM (and at least kAhead per team while that leaves two)
     const int step = a.teams * kAhead;
-    int rows = a.rot ? kTableBytes / (4 * a.rot) : kMaxRows;
-    rows = rows > kMaxRows ? kMaxRows : rows;
+    int rows = most;
     const long long even = (a.tokens * shares + num_sms * kBlocksPerSm - 1) / (num_sms * kBlocksPerSm);
     if (even < rows)
         rows = static_cast<int>(even);
     if (rows > step)
         rows = rows / step * step;
-    if (rows < a.teams)
-        rows = a.teams;
-    const int most = a.rot ? kTableBytes / (4 * a.rot) : kMaxRows;
-    a.block_rows = rows > most ? most : rows;
+    a.block_rows = rows < a.teams ? a.teams : rows;
     const dim3 grid(static_cast<unsigned>((a.tokens + a.block_rows - 1) / a.block_rows), shares);
     return a.norm ? (a.interleaved ? launch_as<T, VW, SPL, true, true>(a, grid, threads, stream)
                                    : launch_as<T, VW, SPL, false, true>(a, grid, threads, stream))

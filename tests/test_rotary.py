@@ -275,6 +275,25 @@ def test_qk_norm_rotary(built, T, Hq, Hk, D, R, layout, norm, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,H,D,R", [
+    (65, 1, 2, 2), (192, 1, 16, 16), (200, 1, 16, 4), (193, 2, 4, 2), (300, 1, 8, 8), (5003, 2, 16, 16),
+    (1000, 1, 32, 32), (97, 1, 32, 6), (30000, 1, 2, 2)])
+def test_small_heads(built, T, H, D, R, dtype):
+    """One or two heads of a few numbers: a block has room for more rows side by
+    side than it keeps positions for."""
+    x = rnd(T, H, D, seed=T + D, dtype=dtype).cuda()
+    pos = torch.arange(T) * 53 % 7919
+    f, amp = freqs(R, 10000.0)
+    rope = binding.Rotary(R)
+    p32 = pos.to(torch.int32).cuda()
+    check_typed(binding.rotary(x, rope, positions=p32), *reference(x, pos, f, amp, "half"))
+    w = (1 + 0.2 * rnd(D, seed=3, dtype="f32")).to(TYPES[dtype]).cuda()
+    got, _ = binding.qk_norm_rotary(x, None, w, None, rope, p32, eps=1e-2)
+    check_typed(got, *reference(x, pos, f, amp, "half", "rms", w, 1e-2))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("lens", [[1], [5, 0, 1, 300], [0, 0, 7], [1] * 70, [129, 64, 1000]])
 @pytest.mark.parametrize("behind", [0, 13])
 def test_positions_from_cu_seqlens(built, lens, behind):
