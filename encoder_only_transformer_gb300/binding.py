@@ -560,13 +560,13 @@ class Attention:
         """Remember the arguments (without pointers) and the workspace's size."""
         if scale is None:
             scale = 0.0
-        elif not 0.0 < scale < float("inf"):
-            raise ValueError("scale must be positive and finite")
+        elif not 0.0 < ctypes.c_float(scale).value < float("inf"):
+            raise ValueError("scale must be positive and finite (in fp32)")
         # the size depends on which pointers there are, not on where they point
         there = ctypes.addressof(ctypes.c_int(0))
         args = CrossArgs(None, None, None, None, *pitches, rows_q, rows_k, q.shape[-2], k.shape[-2], q.shape[-1],
                          _DTYPES[q.dtype], scale, n_seqs, there if packed else None, there if packed else None,
-                         int(max_seqlen_q), None if key_mask is None else there)
+                         max_seqlen_q, None if key_mask is None else there)
         need = _c_i64()
         _check(load_library().mbert_attn_cross_workspace(self._h, ctypes.byref(args), ctypes.byref(need)),
                "cross_attention")
@@ -587,6 +587,7 @@ class Attention:
         on the longest query sequence: give it for single tokens (at most
         16 / (Hq / Hk) rows a sequence), which then read k and v once.  scale
         None: 1 / sqrt(D).  Rows may be strided (views of fused rows)."""
+        max_seqlen_q, scale = int(max_seqlen_q), None if scale is None else float(scale)
         key = ("cross", _layout(q, k, v, cu_seqlens_q, cu_seqlens_k), None if out is None else _layout(out),
                None if key_mask is None else _layout(key_mask), max_seqlen_q, scale)
         known = self._known.get(key)
@@ -624,6 +625,7 @@ class Attention:
         out [B, Sq, Hq, D].  Every query row is computed; one whose keys are all
         pads is 0.  Rows may be strided, with the batch rows one pitch apart
         (views of fused rows).  Else as cross_attention."""
+        scale = None if scale is None else float(scale)
         key = ("cross_padded", _layout(q, k, v), None if out is None else _layout(out),
                None if key_mask is None else _layout(key_mask), scale)
         known = self._known.get(key)

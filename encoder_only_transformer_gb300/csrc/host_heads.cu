@@ -42,6 +42,16 @@ bool may_overlap(Extent a, long long arow, long long awidth, Extent b, long long
 }
 
 constexpr long long kMaxStride = 1ll << 40;
+// Elements from a tensor's first to its last, at most: beyond any device's
+// memory, and far from where extents in bytes would overflow.
+constexpr long long kMaxSpan = 1ll << 48;
+
+// (rows - 1) * pitch stays within kMaxSpan
+bool span_ok(long long rows, long long pitch) { return rows <= 1 || pitch <= kMaxSpan / (rows - 1); }
+
+// Rows of a packed tensor, at most: places up to a tile behind the last row
+// (and a block's stride behind that) still fit 32 bits.
+constexpr long long kMaxRows = INT32_MAX - 1024;
 
 int check_heads(const mbert_attn_heads &x, long long T, int dim, int es, bool weight)
 {
@@ -53,6 +63,9 @@ int check_heads(const mbert_attn_heads &x, long long T, int dim, int es, bool we
     for (int64_t s : {x.src_row, x.src_head, x.dst_row, x.dst_head})
         if (s < 0 || s > kMaxStride)
             return MBERT_ERR_BAD_ARG;
+    if (!span_ok(T, x.src_row) || !span_ok(T, x.dst_row) || !span_ok(x.heads, x.src_head) ||
+        !span_ok(x.heads, x.dst_head))
+        return MBERT_ERR_BAD_ARG;
     // the elements of dst are distinct: heads within rows, or rows within heads
     const bool heads_apart = x.heads == 1 || x.dst_head >= dim;
     const bool rows_apart = T == 1 || x.dst_row >= dim;
@@ -268,8 +281,8 @@ int cross_plan(const mbert_attn *h, const mbert_attn_cross_args *c, CrossPlan *p
     if ((c->head_dim != 64 && c->head_dim != 128) || (c->dtype != MBERT_BF16 && c->dtype != MBERT_F16))
         return MBERT_ERR_UNSUPPORTED;
     if (c->heads < 1 || c->heads > 65536 || c->kv_heads < 1 || c->heads % c->kv_heads ||
-        c->rows_q < 0 || c->rows_q > INT32_MAX || c->rows_k < 0 || c->rows_k > INT32_MAX || c->n_seqs < 0 ||
-        c->max_seqlen_q < 0 || !(c->scale >= 0.f) || !std::isfinite(c->scale))
+        c->rows_q < 0 || c->rows_q > kMaxRows || c->rows_k < 0 || c->rows_k > kMaxRows || c->n_seqs < 0 ||
+        c->max_seqlen_q < 0 || !(c->scale >= 0.f) || !std::isfinite(c->scale * 1.5f))
         return MBERT_ERR_BAD_ARG;
     if (c->n_seqs == 0 && (c->rows_q > 0 || c->rows_k > 0))
         return MBERT_ERR_BAD_ARG;
@@ -339,11 +352,11 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     const int D = c.head_dim;
     const int64_t qw = static_cast<int64_t>(c.heads) * D, kw = static_cast<int64_t>(c.kv_heads) * D;
     // rows of whole 16-byte vectors that do not run into each other
-    auto row_ok = [](int64_t pitch, int64_t width) {
-        return pitch >= width && pitch % 8 == 0 && pitch < (1ll << 38);
+    auto row_ok = [](int64_t pitch, int64_t width, int64_t n) {
+        return pitch >= width && pitch % 8 == 0 && pitch < (1ll << 38) && span_ok(n, pitch);
     };
-    if (!row_ok(c.q_row, qw) || !row_ok(c.out_row, qw) ||
-        (keys && (!row_ok(c.k_row, kw) || !row_ok(c.v_row, kw))))
+    if (!row_ok(c.q_row, qw, c.rows_q) || !row_ok(c.out_row, qw, c.rows_q) ||
+        (keys && (!row_ok(c.k_row, kw, c.rows_k) || !row_ok(c.v_row, kw, c.rows_k))))
         return MBERT_ERR_BAD_ARG;
     auto rows = [&](const void *ptr, int64_t n, int64_t pitch, int64_t width) {
         const uintptr_t lo = reinterpret_cast<uintptr_t>(ptr);

@@ -335,9 +335,10 @@ int mbert_attn_qk_norm_rotary(mbert_attn *h, const mbert_attn_heads *q, const mb
  *   k, v         device [rows_k][kv_heads][head_dim], rows k_row / v_row apart
  *                (16-byte aligned, pitches multiples of 8 and at least the
  *                row's width, so views of fused rows are fine; out overlaps
- *                nothing else; k and v unused for rows_k = 0).
+ *                nothing else; k and v unused for rows_k = 0).  Fewer than
+ *                2^31 - 1024 rows each.
  *   head_dim     64 or 128; dtype MBERT_BF16 or MBERT_F16, else MBERT_ERR_UNSUPPORTED.
- *   scale        > 0 and finite, or 0 for 1 / sqrt(head_dim).
+ *   scale        > 0 and at most 2e38, or 0 for 1 / sqrt(head_dim).
  *   cu_q, cu_k   device int32 [n_seqs + 1]: cu[0] = 0, non-decreasing, cu[n] <= rows; empty
  *                sequences are allowed on either side; rows of out from cu_q[n] on are left
  *                as they were.  NULL: n_seqs sequences of rows / n_seqs each (a padded batch).

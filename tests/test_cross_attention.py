@@ -509,3 +509,44 @@ def test_tokens_over_long_caches(built, H, Hk, D, dtype, kl, masked):
         mask = torch.rand(sum(kl), generator=torch.Generator().manual_seed(1)) < 0.7
         mask[:4000] = False
     run_packed([1, 2, 1, 2][:len(kl)], kl, H, Hk, D, dtype, max_q=2, seed=3, behind=5, mask=mask)
+
+
+@pytest.mark.gpu
+def test_limits(built):
+    """Sizes whose places or extents would not fit are refused on the host; a
+    scale that fp32 takes for zero is no default; a bound given as a tensor
+    counts by its value."""
+    import ctypes
+    lib, h = binding.load_library(), binding._default(torch.device("cuda", 0)).handle
+    need = ctypes.c_int64()
+    there = ctypes.addressof(need)      # never read: no call gets as far as a launch
+
+    def status(rows_q=4, rows_k=4, pitch=64, scale=1.0):
+        a = binding.CrossArgs(None, None, None, None, pitch, pitch, pitch, pitch, rows_q, rows_k, 1, 1, 64, 0,
+                              scale, 1, there, there, 0, None)
+        return lib.mbert_attn_cross_workspace(h, ctypes.byref(a), ctypes.byref(need))
+
+    assert status() == 0
+    assert status(rows_k=2 ** 31 - 2000) == 0
+    assert status(rows_k=2 ** 31 - 1000) == -1 and status(rows_k=2 ** 31 - 1) == -1
+    assert status(rows_q=2 ** 31 - 1) == -1
+    assert status(scale=3e38) == -1
+    q, k, v = (x.cuda() for x in make([3], [10], 1, 1, 64, "bf16"))
+    a = binding.CrossArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), torch.empty_like(q).data_ptr(),
+                          64, 1 << 37, 64, 64, 3, 2 ** 30, 1, 1, 64, 0, 1.0, 1,
+                          cu_of([3]).data_ptr(), cu_of([10]).data_ptr(), 3, None)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    assert lib.mbert_attn_cross(h, ctypes.byref(a), ws.data_ptr(), ws.numel(), None) == -1
+
+    cu = dict(cu_seqlens_q=cu_of([3]), cu_seqlens_k=cu_of([10]))
+    with pytest.raises(ValueError):
+        binding.cross_attention(q, k, v, scale=1e-50, **cu)
+    with pytest.raises(ValueError):
+        binding.cross_attention_padded(q[None], k[None], v[None], scale=1e-50)
+    bound = torch.tensor(3)
+    want = binding.cross_attention(q, k, v, max_seqlen_q=3, **cu)
+    assert torch.equal(binding.cross_attention(q, k, v, max_seqlen_q=bound, **cu), want)
+    bound.fill_(-1)
+    with pytest.raises(binding.MbertAttnError):
+        binding.cross_attention(q, k, v, max_seqlen_q=bound, **cu)
+    assert binding._default(q.device).get_error() == 0

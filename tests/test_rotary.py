@@ -446,3 +446,19 @@ def test_refusals(built):
     with pytest.raises(binding.MbertAttnError):                         # k read while q is written there
         binding.qk_norm_rotary(x, x, w, w, r, p, q_out=x)
     assert binding._default(x.device).get_error() == 0
+
+
+@pytest.mark.gpu
+def test_extents_beyond_any_memory(built):
+    """Strides whose extents would not fit 64 bits are refused on the host."""
+    import ctypes
+    lib = binding.load_library()
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out, p = torch.empty_like(x), torch.zeros(4, dtype=torch.int32, device="cuda")
+    rope = binding.Rotary(64)
+    h = binding._default(x.device).handle
+    for tokens, strides in ((2 ** 30, (1 << 40, 64, 128, 64)), (2 ** 30, (128, 64, 1 << 40, 64)),
+                            (4, (-128, 64, 128, 64)), (4, (1 << 41, 64, 128, 64))):
+        heads = binding.Heads(x.data_ptr(), out.data_ptr(), None, 2, *strides)
+        assert lib.mbert_attn_rotary(h, ctypes.byref(heads), tokens, 64, 0, rope._ref, p.data_ptr(), 32, None, 0,
+                                     0, None) == -1
