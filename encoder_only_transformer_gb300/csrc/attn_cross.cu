@@ -66,10 +66,12 @@ constexpr int kMaskSlots = 4;
 
 // Costs, by a fit over the CTAs' times in clocks: a key tile for both query
 // tiles 2200 (D = 64) and 2900 (D = 128), for one 1750 and 1850; a unit's fixed
-// work (the end of the softmax, the output, the refill) 3500 and 4700.
+// work (the end of the softmax, the output, the refill) 3500 and 4700.  Units
+// stay whole, up to four to a CTA, where that puts no more than 34 (6 us) on
+// top of a CTA's share.
 template <int D>
 using Split = CrossSplit<D == 64 ? 384 : 512, kCrossBlockRows, kBlockN, 6, D == 64 ? 5 : 4, 10,
-                         kCrossBlockWholeKeys / kBlockN>;
+                         kCrossBlockWholeKeys / kBlockN, 4, 34>;
 
 template <int D>
 struct Layout {
@@ -838,7 +840,8 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
         a.records[cta].parts = 0;
     Split<D> split(a, a.heads >> a.fold_log2);
     // two tiles and a unit's fixed work per CTA at least
-    const bool work = split.find(*reinterpret_cast<typename Split<D>::Scratch *>(sbase + L::kOffScratch), gridDim.x, 22);
+    const bool work = split.find(*reinterpret_cast<typename Split<D>::Scratch *>(sbase + L::kOffScratch), gridDim.x, 22,
+                                 reinterpret_cast<typename Split<D>::Deal *>(sbase + L::kOffOut));
     if (work) {
         Ctx c{base, 0u, sbase, a, base + L::kOffBar};
         const int warp = threadIdx.x >> 5;

@@ -14,6 +14,14 @@
 //
 // No list of the work is made: each CTA sums the sequences' costs and finds
 // its own range, one thread per sequence.
+//
+// Where the units are few (kRounds to a CTA at most), they are first dealt out
+// whole, the longest first, in rounds that run forth and back over the CTAs;
+// if the CTA with the most gets no more than the line's share and kJoin, what
+// cutting and joining costs, they stay so.  12 sequences of 250 queries over
+// 1000 keys, 12 heads of 64: 20.3 us, 24.6 cut; 24 over 600 to 1000: 31.9,
+// 35.7 cut; 32 heads over 8 of 128, 9 sequences: 41, 50 cut.  With the longest
+// unit 34 above the share (16 sequences of 118 to 1946 keys) both took 32.5.
 #pragma once
 
 #include "common.cuh"
@@ -22,17 +30,27 @@
 namespace mbert {
 
 // kBlockQ: query rows of a unit (0: all of a sequence's), each the rows of
-// 2^fold_log2 heads, side by side; kTile: keys of a tile.
-template <int kThreads, int kBlockQ_, int kTile_, int kFull_, int kHalf_, int kAlpha_, int kSnap_>
+// 2^fold_log2 heads, side by side; kTile: keys of a tile; kRounds 0: units are
+// never dealt out whole.
+template <int kThreads, int kBlockQ_, int kTile_, int kFull_, int kHalf_, int kAlpha_, int kSnap_, int kRounds = 0,
+          int kJoin = 0>
 struct CrossSplit {
     static constexpr int kBlockQ = kBlockQ_, kTile = kTile_, kSnap = kSnap_;
     static constexpr int kFull = kFull_, kHalf = kHalf_, kAlpha = kAlpha_;
     static constexpr int kWarps = kThreads / 32;
+    static constexpr int kDealSeqs = 128;       // sequences whose units are dealt out, at most
 
     struct Scratch {
         long long warp[kWarps];
         long long base[2];
         int seq[2];
+        int units[kWarps], most[kWarps];
+        int deal_seq[kRounds + 1], deal_unit[kRounds + 1];      // this CTA's whole units
+    };
+    // What dealing takes besides, while find() runs.
+    struct Deal {
+        int cost[kDealSeqs], last[kDealSeqs], blocks[kDealSeqs], units[kDealSeqs];
+        int sum[kThreads];
     };
 
     // What a sequence needs: rows, tiles, blocks of query rows.
@@ -77,6 +95,7 @@ struct CrossSplit {
     long long lo, hi;       // this CTA's range
     int seq0;               // the sequence that holds lo, and where it starts
     long long base0;
+    const Scratch *dealt = nullptr;     // whole units, dealt out
 
     __device__ explicit CrossSplit(const CrossArgs &args, int heads) : a(args), unit_heads(heads) {}
 
@@ -133,11 +152,12 @@ struct CrossSplit {
     // Every thread of the block.  min_cost: of a CTA, at least kFull, so that
     // every CTA inside a unit's tiles has one.  False: nothing to do for this
     // CTA (or the offsets are bad, then *a.err says so and no CTA does anything).
-    __device__ bool find(Scratch &sm, int max_ctas, int min_cost)
+    // work: memory for dealing, free again afterwards (kRounds > 0).
+    __device__ bool find(Scratch &sm, int max_ctas, int min_cost, Deal *work = nullptr)
     {
         const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
         long long sum = 0;
-        int bad = 0;
+        int bad = 0, units = 0, most = 0;       // most: tiles of a unit
         for (int s = tid; s < a.n_seqs; s += kThreads) {
             const Seq q = load(s);
             if (q.q_len < 0 || q.k_all < 0 || q.q_row < 0 || q.k_row < 0 ||
@@ -146,16 +166,27 @@ struct CrossSplit {
                 bad |= kErrBadCu;
             else if (q.q_len > a.max_q)
                 bad |= kErrTooLong;
-            else
+            else {
                 sum += cost(q);
+                // (only compared with few)
+                units = static_cast<int>(min(1ll << 20, units + static_cast<long long>(unit_heads) * (q.whole + q.half)));
+                most = max(most, q.whole ? q.tiles : 0);
+            }
         }
         if (tid == 0 && ((a.cu_q && a.cu_q[0] != 0) || (a.cu_k && a.cu_k[0] != 0)))
             bad |= kErrBadCu;
 #pragma unroll
         for (int d = 16; d; d >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0)
+        if constexpr (kRounds > 0) {
+            units = __reduce_add_sync(0xffffffffu, units);
+            most = __reduce_max_sync(0xffffffffu, most);
+        }
+        if (lane == 0) {
             sm.warp[warp] = sum;
+            sm.units[warp] = units;
+            sm.most[warp] = most;
+        }
         if (tid < 2)
             sm.seq[tid] = -1;
         const int any = __syncthreads_or(bad);
@@ -172,6 +203,20 @@ struct CrossSplit {
             return false;
         const long long want = total / min_cost;
         ctas = want < 1 ? 1 : want < max_ctas ? static_cast<int>(want) : max_ctas;
+        if constexpr (kRounds > 0) {
+            int all = 0, longest = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                all += sm.units[w];
+                longest = max(longest, sm.most[w]);
+            }
+            const long long limit = a.records ? total / ctas + kJoin : INT64_MAX;
+            if (a.n_seqs <= kDealSeqs && max_ctas <= kThreads && all <= kRounds * max_ctas &&
+                static_cast<long long>(longest) * kFull + kAlpha <= limit && deal(sm, *work, max_ctas, limit)) {
+                dealt = &sm;
+                return sm.deal_seq[0] >= 0;
+            }
+        }
         if (static_cast<int>(blockIdx.x) >= ctas)
             return false;
         lo = border(blockIdx.x);
@@ -219,6 +264,45 @@ struct CrossSplit {
         return lo < hi;
     }
 
+    // Deals the units out whole: true if no CTA gets more than `limit`.
+    __device__ bool deal(Scratch &sm, Deal &d, int n, long long limit)
+    {
+        const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+        if (tid < a.n_seqs) {
+            const Seq q = load(tid);
+            const int full = q.tiles * kFull + kAlpha, half = q.tiles * kHalf + kAlpha;
+            d.last[tid] = q.half ? half : full;
+            d.cost[tid] = q.whole ? full : half;
+            d.blocks[tid] = q.whole + q.half;
+            d.units[tid] = unit_heads * (q.whole + q.half);
+        }
+        if (tid < n)
+            d.sum[tid] = 0;
+        if (tid <= kRounds)
+            sm.deal_seq[tid] = -1;
+        __syncthreads();
+        // a warp per sequence: the units of those with longer ones come first
+        for (int s = warp; s < a.n_seqs; s += kWarps) {
+            const int mine = d.cost[s], last = d.last[s], blocks = d.blocks[s], units = d.units[s];
+            int start = 0;
+            for (int o = lane; o < a.n_seqs; o += 32)
+                if (d.cost[o] > mine || (d.cost[o] == mine && o < s))
+                    start += d.units[o];
+            start = __reduce_add_sync(0xffffffffu, start);
+            for (int j = lane; j < units; j += 32) {
+                const int round = (start + j) / n, at = start + j - round * n;
+                const int cta = round & 1 ? n - 1 - at : at;
+                atomicAdd(&d.sum[cta], j % blocks == blocks - 1 ? last : mine);
+                if (cta == static_cast<int>(blockIdx.x)) {
+                    sm.deal_seq[round] = s;
+                    sm.deal_unit[round] = j;
+                }
+            }
+        }
+        __syncthreads();
+        return !__syncthreads_or(tid < n && d.sum[tid] > limit);
+    }
+
     __device__ __forceinline__ long long snap(long long x, int s, long long base) const
     {
         if (s < 0)
@@ -240,7 +324,7 @@ struct CrossSplit {
 
     // Walks this CTA's segments in order.
     struct Iter {
-        int seq = -1;
+        int seq = -1;           // (dealt units: the round)
         long long base = 0, x = 0;
         Seq s;
     };
@@ -248,6 +332,10 @@ struct CrossSplit {
     __device__ __forceinline__ Iter begin() const
     {
         Iter it;
+        if (kRounds > 0 && dealt) {
+            it.seq = 0;
+            return it;
+        }
         it.seq = seq0;
         it.base = base0;
         it.x = lo;
@@ -257,6 +345,21 @@ struct CrossSplit {
 
     __device__ bool next(Iter &it, Seg &g) const
     {
+        if constexpr (kRounds > 0) {
+            if (dealt) {
+                g.seq = dealt->deal_seq[it.seq];
+                if (g.seq < 0)
+                    return false;
+                const int unit = dealt->deal_unit[it.seq++];
+                g.s = load(g.seq);
+                const int blocks = g.s.whole + g.s.half;
+                g.head = unit / blocks;
+                g.q0 = unit % blocks * kBlockQ;
+                g.kb = 0;
+                g.ke = g.s.tiles;
+                return true;
+            }
+        }
         while (it.x < hi) {
             if (it.x - it.base >= cost(it.s)) {
                 it.base += cost(it.s);

@@ -167,6 +167,24 @@ def test_blocks(built, ql, kl, H, Hk, D, dtype):
     run_packed(ql, kl, H, Hk, D, dtype, seed=len(ql) + D, behind=3)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "f16")])
+@pytest.mark.parametrize("ql,kl,H", [
+    ([250] * 12, [640] * 12, 12),                           # as many units as processors, near enough
+    ([100, 300, 0, 256, 257, 1] * 3, [600, 520, 900, 0, 530, 700] * 3, 9),      # two rounds, halves, empty ones
+    ([17] * 60, [520 + 3 * i for i in range(60)], 10),      # four rounds
+    ([17] * 61, [520 + 3 * i for i in range(61)], 10),      # one unit more than four rounds
+    ([200] * 9, [1400, 1300, 1200] + [600] * 6, 16),        # the longest beyond the others' share
+    ([5] * 129, [515 + i % 7 for i in range(129)], 1),      # more sequences than are dealt
+])
+def test_whole_units(built, ql, kl, H, D, dtype):
+    """Calls whose units are dealt out whole, and ones just beyond."""
+    mask = torch.ones(sum(kl), dtype=torch.bool)
+    mask[700:900] = False
+    got = run_packed(ql, kl, H, H, D, dtype, seed=len(ql), behind=2, mask=mask)
+    assert torch.equal(run_packed(ql, kl, H, H, D, dtype, seed=len(ql), behind=2, mask=mask), got)
+
+
 TOKENS = [
     # query lengths, key lengths, heads, key heads, longest query sequence
     ([1], [1], 1, 1, 1),
