@@ -4,8 +4,13 @@
 //   out_i = sum_j softmax_j(scale q_i . k_j) v_j,  j over the visible keys of
 //   i's sequence; 0 where there is none
 //
-// Work: a unit is 256 query rows of one sequence and head (two tiles of 128);
-// units and their 128-key tiles are split among one CTA per SM by cost
+// Work: a unit is 256 query rows of one sequence and head (two tiles of 128;
+// G = 2 below) or, for head size 64 in calls whose sequences have no more than
+// 128 rows, one such tile (G = 1, with two CTAs an SM: a unit's start and end
+// then lie beside the other one's tiles, and no softmax warps stand idle; 64
+// sequences of 30 queries over 600 keys 45 -> 32 us, 100 of 20 over 250 39 -> 30,
+// but for 256 rows and more 200 us against 195 and 35 against 33, as K and V are
+// fetched twice as often); units and their 128-key tiles are split among the CTAs by cost
 // (cross_sched.cuh), and units cut between CTAs are joined by a second kernel
 // (cross_join.cu) in a fixed order.  Query heads that share a key head share
 // the blocks too: with F the largest power of two that divides their number,
@@ -14,7 +19,8 @@
 // heads over 4: 179 -> 170 us) and makes few rows of many heads one unit
 // instead of F.
 //
-// CTA (12 warps for D = 64, 16 for D = 128):
+// CTA (12 warps for D = 64, 16 for D = 128; for G = 1 the four of group 0, then
+// those of warps 8 to 11):
 //   warps 0-3    softmax group 0 (query tile 0, TMEM lanes 0..127, a thread a row)
 //   warps 4-7    softmax group 1 (query tile 1)
 //   warp  8      TMA producer: Q, K and V rings
@@ -32,7 +38,7 @@
 // softmax bounds the loop, the larger block only takes registers from it:
 // 217 us against 194 (8192 queries and keys, 12 heads).
 //
-// TMEM (512 columns), fp32 except P (16-bit pairs):
+// TMEM (512 columns; half for G = 1), fp32 except P (16-bit pairs):
 //   D = 64:   S0 S1 (128 each), P0 P1 (64 each), O0 O1 (64 each); S of the next
 //             tile is computed while the softmax works on this one
 //   D = 128:  two S of 64 keys (64 each) per query tile, O0 O1 (128 each); P
@@ -65,42 +71,54 @@ namespace {
 constexpr int kMaskSlots = 4;
 
 // Costs, by a fit over the CTAs' times in clocks: a key tile for both query
-// tiles 2200 (D = 64) and 2900 (D = 128), for one 1750 and 1850; a unit's fixed
+// tiles 2200 (D = 64) and 2900 (D = 128), for one 1750 and 1850 (G = 1: 2150,
+// beside another CTA's); a unit's fixed
 // work (the end of the softmax, the output, the refill) 3500 and 4700.  Units
 // stay whole, up to four to a CTA, where that puts no more than 34 (6 us) on
 // top of a CTA's share.
-template <int D>
-using Split = CrossSplit<D == 64 ? 384 : 512, kCrossBlockRows, kBlockN, 6, D == 64 ? 5 : 4, 10,
-                         kCrossBlockWholeKeys / kBlockN, 4, 34>;
+template <int D, int G>
+using Split = CrossSplit<D == 128 ? 512 : G == 2 ? 384 : 256, kBlockM * G, kBlockN, 6, G == 1 ? 6 : D == 64 ? 5 : 4, 10,
+                         kCrossBlockWholeKeys / kBlockN, 4, 34, cross_block_ctas(kBlockM * G)>;
 
-template <int D>
+// G: query tiles of a unit, a softmax group for each.
+template <int D, int G>
 struct Layout {
     static constexpr bool kSplitIssuers = D == 128;     // S and P V issued by different warps
-    static constexpr int kThreads = D == 64 ? 384 : 512;
-    // registers a thread: 4 x 72 + 8 x 216 = 12 x 168, 8 x 56 + 8 x 200 = 16 x 128
-    static constexpr int kRegsSoftmax = D == 64 ? 216 : 200;
-    static constexpr int kRegsControl = D == 64 ? 72 : 56;
-    static constexpr int kRecReaders = kSplitIssuers ? 13 : 11;  // issuers, eight softmax warps, the mask warp
+    static constexpr bool kPair = D == 64 && G == 2;    // the one of 12 warps
+    static constexpr int kUnitRows = kBlockM * G;
+    static constexpr int kCtas = cross_block_ctas(kUnitRows);
+    static constexpr int kControl = 4 * G;              // first warp after the softmax groups
+    static constexpr int kThreads = kSplitIssuers ? 512 : 32 * (kControl + 4);
+    // registers a thread: 4 x 72 + 8 x 216 = 12 x 168, 8 x 56 + 8 x 200 = 16 x 128,
+    // 4 x 56 + 4 x 200 = 8 x 128
+    static constexpr int kRegsSoftmax = kPair ? 216 : 200;
+    static constexpr int kRegsControl = kPair ? 72 : 56;
+    static constexpr int kRecReaders = kSplitIssuers ? 13 : 5 * G + 1;   // issuers, softmax warps, the mask warp
     static constexpr int kKeys = D == 64 ? 128 : 64;    // keys of a step (an S)
     static constexpr int kSteps = kBlockN / kKeys;      // steps of a tile
     static constexpr int kHalves = D / 64;              // 64-column boxes of a tile
     static constexpr uint32_t kTile = kHalves * kTileBytes;
-    static constexpr int kQSets = D == 64 ? 2 : 1;      // of two query tiles
-    static constexpr int kStages = D == 64 ? 3 : 2;     // of K and of V
-    static constexpr uint32_t kOffK = kQSets * 2 * kTile;
+    static constexpr int kQSets = D == 64 ? 2 : 1;      // of G query tiles
+    static constexpr int kStages = kPair ? 3 : 2;     // of K and of V
+    static constexpr uint32_t kOffK = kQSets * G * kTile;
     static constexpr uint32_t kOffV = kOffK + kStages * kTile;
     static constexpr uint32_t kOffOut = kOffV + kStages * kTile;    // 4 KB per softmax warp: 32 rows x 64 columns
-    static constexpr uint32_t kOffBar = kOffOut + 8 * 4096;
+    static constexpr uint32_t kOutRows = kCtas == 2 ? 16 : 32;   // rows that a warp stages at a time
+    static constexpr uint32_t kOffBar = kOffOut + 4 * G * kOutRows * 128;
     static constexpr uint32_t kOffWords = kOffBar + 512;            // key bits, kMaskSlots x 4 words
     static constexpr uint32_t kOffRecs = kOffWords + 16 * kMaskSlots;
     static constexpr uint32_t kOffScratch = kOffRecs + 48 * 4;
-    static constexpr uint32_t kSmemBytes = kOffScratch + sizeof(typename Split<D>::Scratch) + 1024;
+    static constexpr uint32_t kSmemBytes = kOffScratch + sizeof(typename Split<D, G>::Scratch) + 1024;
     // S and P of query tile w's step (D = 128: two buffers in turn), O
     static constexpr uint32_t col_s(int w, uint32_t step) { return 128u * w + (D == 64 ? 0u : 64u * (step & 1)); }
-    static constexpr uint32_t col_p(int w, uint32_t step) { return D == 64 ? 256u + 64u * w : col_s(w, step); }
-    static constexpr uint32_t col_o(int w) { return D == 64 ? 384u + 64u * w : 256u + 128u * w; }
+    static constexpr uint32_t col_p(int w, uint32_t step) { return D == 64 ? 128u * G + 64u * w : col_s(w, step); }
+    static constexpr uint32_t col_o(int w) { return D == 64 ? 192u * G + 64u * w : 256u + 128u * w; }
+    static constexpr uint32_t kTmemCols = 256 * G;
 };
-static_assert(Layout<64>::kSmemBytes <= 232448 && Layout<128>::kSmemBytes <= 232448, "shared memory");
+// (1 KB of an SM's 228 is the system's for each CTA)
+static_assert(Layout<64, 2>::kSmemBytes <= 232448 && Layout<128, 2>::kSmemBytes <= 232448 &&
+                  Layout<64, 1>::kSmemBytes <= 115712,
+              "shared memory");
 
 // barrier slots (8 bytes each)
 constexpr int kBarQFull = 0;      // + set (2)
@@ -126,7 +144,6 @@ constexpr int kNumBars = 50;
 constexpr uint32_t kSlotInBars = 8 * kNumBars;                 // TMEM address
 static_assert(kSlotInBars + 4 <= 512, "barriers");
 
-constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;
 
 // kind::f16 instruction descriptor for either 16-bit type (A and B alike)
@@ -160,13 +177,13 @@ struct Ctx {
 __device__ __forceinline__ uint32_t bar(const Ctx &c, int i) { return c.bars + 8u * i; }
 
 // The CTA's segment sg (all lanes of a reading warp).  False: there is none.
-template <int D>
+template <int D, int G>
 __device__ __forceinline__ bool read_rec(const Ctx &c, uint32_t sg, int lane, Rec &r)
 {
     const int slot = sg % kRecs;
     if (!mbar_wait(bar(c, kBarRecFull + slot), (sg / kRecs) & 1, c.a.err))
         return false;
-    r = reinterpret_cast<const Rec *>(c.sbase + Layout<D>::kOffRecs)[slot];
+    r = reinterpret_cast<const Rec *>(c.sbase + Layout<D, G>::kOffRecs)[slot];
     __syncwarp();
     if (lane == 0)
         mbar_arrive(bar(c, kBarRecEmpty + slot));
@@ -182,21 +199,21 @@ __device__ __forceinline__ bool needs_bits(const Rec &s) { return s.k_full < s.k
 __device__ __forceinline__ bool second_tile(const Rec &s) { return s.rows - s.q0 > kBlockM; }
 
 // Steps of a segment: a last tile of at most 64 keys takes one step of 64.
-template <int D>
+template <int D, int G>
 __device__ __forceinline__ int seg_steps(const Rec &s)
 {
-    const int n = (s.ke - s.kb) * Layout<D>::kSteps;
-    return n - (Layout<D>::kSteps == 2 && s.k_len - (s.ke - 1) * kBlockN <= 64);
+    const int n = (s.ke - s.kb) * Layout<D, G>::kSteps;
+    return n - (Layout<D, G>::kSteps == 2 && s.k_len - (s.ke - 1) * kBlockN <= 64);
 }
 
 // ---------------------------------------------------------------- producer
-template <int D>
-__device__ void producer(const Ctx &c, const Split<D> &split)
+template <int D, int G>
+__device__ void producer(const Ctx &c, const Split<D, G> &split)
 {
-    using L = Layout<D>;
+    using L = Layout<D, G>;
     int *err = c.a.err;
     auto it = split.begin();
-    typename Split<D>::Seg seg;
+    typename Split<D, G>::Seg seg;
     uint32_t g = 0;          // key tiles issued by this CTA so far
     for (uint32_t sg = 0;; ++sg) {
         Rec s{};
@@ -222,12 +239,12 @@ __device__ void producer(const Ctx &c, const Split<D> &split)
         if (s.ke == 0)
             return;
         const int qs = sg % L::kQSets;
-        const bool two = second_tile(s);
+        const bool two = G == 2 && second_tile(s);
         if (sg >= L::kQSets && !mbar_wait(bar(c, kBarQEmpty + qs), (sg / L::kQSets - 1) & 1, err))
             return;
         const int col_k = s.head / c.a.group * D;
         const int fold = c.a.fold_log2, qrow = s.q_row + (s.q0 >> fold);
-        const uint32_t qdst = c.base + qs * 2 * L::kTile;
+        const uint32_t qdst = c.base + qs * G * L::kTile;
         mbar_arrive_expect_tx(bar(c, kBarQFull + qs), (two ? 2 : 1) * L::kTile);
         for (int w = 0; w < (two ? 2 : 1); ++w)
             for (int h = 0; h < L::kHalves; ++h)
@@ -255,12 +272,12 @@ __device__ void producer(const Ctx &c, const Split<D> &split)
 
 // ---------------------------------------------------------------- MMA issuers
 // S of 64 (D = 128) or 128 keys from key `key0` of the stage.
-template <int D, bool kHalf>
+template <int D, int G, bool kHalf>
 __device__ __forceinline__ void issue_s(const Ctx &c, int w, int qs, int st, int key0, uint32_t step)
 {
-    using L = Layout<D>;
+    using L = Layout<D, G>;
     constexpr uint32_t kIdesc = idesc(128, L::kKeys, false, kHalf);
-    const uint32_t q = c.base + (qs * 2 + w) * L::kTile;
+    const uint32_t q = c.base + (qs * G + w) * L::kTile;
     const uint32_t k = c.base + L::kOffK + st * L::kTile + 128 * key0;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
@@ -274,10 +291,10 @@ __device__ __forceinline__ void issue_s(const Ctx &c, int w, int qs, int st, int
 // MN-major operand: 64 columns (128 bytes) x 8 keys are one swizzle atom; atoms
 // follow each other by 1024 bytes along the keys (stride offset) and by a
 // 64-column box along the columns (leading offset).
-template <int D, bool kHalf>
+template <int D, int G, bool kHalf>
 __device__ __forceinline__ void issue_o(const Ctx &c, int w, int st, int key0, uint32_t step, bool accumulate)
 {
-    using L = Layout<D>;
+    using L = Layout<D, G>;
     constexpr uint32_t kIdesc = idesc(128, D, true, kHalf);
     const uint32_t v = c.base + L::kOffV + st * L::kTile + 128 * key0;
 #pragma unroll
@@ -292,15 +309,15 @@ __device__ __forceinline__ void issue_o(const Ctx &c, int w, int st, int key0, u
 // steps of this query tile (its S, P and O barriers), `g` all tiles of the CTA
 // (the rings).  In a segment whose second query tile is empty, issuer 1 only
 // hands the ring slots back as they fill (each phase only once it has begun).
-template <bool kHalf>
+template <int G, bool kHalf>
 __device__ void so_issuer(const Ctx &c, int w, int lane)
 {
     constexpr int D = 64;
-    using L = Layout<D>;
+    using L = Layout<D, G>;
     int *err = c.a.err;
     Rec s;
     uint32_t g0 = 0, gw0 = 0, sw = 0, masked = 0;
-    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
+    for (uint32_t sg = 0; read_rec<D, G>(c, sg, lane, s); ++sg) {
         const int qs = sg % L::kQSets;
         const int n = s.ke - s.kb;
         const bool mine = w == 0 || second_tile(s);
@@ -317,7 +334,7 @@ __device__ void so_issuer(const Ctx &c, int w, int lane)
                         return;
                     __syncwarp();
                     tc_fence_after();
-                    issue_s<D, kHalf>(c, w, qs, st, 0, gw);
+                    issue_s<D, G, kHalf>(c, w, qs, st, 0, gw);
                     mma_commit_warp(bar(c, kBarSFull + w));
                     mma_commit_warp(bar(c, kBarKEmpty + st));
                     if (t == n - 1)
@@ -347,7 +364,7 @@ __device__ void so_issuer(const Ctx &c, int w, int lane)
                         return;
                     __syncwarp();
                     tc_fence_after();
-                    issue_o<D, kHalf>(c, w, st, 0, gw, t > 1);
+                    issue_o<D, G, kHalf>(c, w, st, 0, gw, t > 1);
                     mma_commit_warp(bar(c, kBarODone + w));
                     mma_commit_warp(bar(c, kBarVEmpty + st));
                 } else if (lane == 0) {
@@ -365,16 +382,16 @@ __device__ void so_issuer(const Ctx &c, int w, int lane)
 }
 
 // D = 128: issuer of query tile w's S.
-template <int D, bool kHalf>
+template <int D, int G, bool kHalf>
 __device__ void s_issuer(const Ctx &c, int w, int lane)
 {
-    using L = Layout<D>;
+    using L = Layout<D, G>;
     int *err = c.a.err;
     Rec s;
     uint32_t g = 0, gw = 0;
-    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
+    for (uint32_t sg = 0; read_rec<D, G>(c, sg, lane, s); ++sg) {
         const int qs = sg % L::kQSets;
-        const int n = seg_steps<D>(s);
+        const int n = seg_steps<D, G>(s);
         const bool mine = w == 0 || second_tile(s);
         if (!mbar_wait(bar(c, kBarQFull + qs), (sg / L::kQSets) & 1, err))
             return;
@@ -395,7 +412,7 @@ __device__ void s_issuer(const Ctx &c, int w, int lane)
                 return;
             __syncwarp();
             tc_fence_after();
-            issue_s<D, kHalf>(c, w, qs, st, sub * L::kKeys, gw);
+            issue_s<D, G, kHalf>(c, w, qs, st, sub * L::kKeys, gw);
             mma_commit_warp(bar(c, (gw & 1 ? kBarSOdd : kBarSFull) + w));
             if (last_sub)
                 mma_commit_warp(bar(c, kBarKEmpty + st));
@@ -412,15 +429,15 @@ __device__ void s_issuer(const Ctx &c, int w, int lane)
 }
 
 // D = 128: issuer of query tile w's O += P V.
-template <int D, bool kHalf>
+template <int D, int G, bool kHalf>
 __device__ void o_issuer(const Ctx &c, int w, int lane)
 {
-    using L = Layout<D>;
+    using L = Layout<D, G>;
     int *err = c.a.err;
     Rec s;
     uint32_t g = 0, gw = 0, sw = 0, masked = 0;
-    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
-        const int n = seg_steps<D>(s);
+    for (uint32_t sg = 0; read_rec<D, G>(c, sg, lane, s); ++sg) {
+        const int n = seg_steps<D, G>(s);
         const bool mine = w == 0 || second_tile(s);
         for (int j = 0; j < n; ++j) {
             const int st = g % L::kStages, sub = j % L::kSteps;
@@ -450,7 +467,7 @@ __device__ void o_issuer(const Ctx &c, int w, int lane)
                 return;
             __syncwarp();
             tc_fence_after();
-            issue_o<D, kHalf>(c, w, st, sub * L::kKeys, gw, j > 0);
+            issue_o<D, G, kHalf>(c, w, st, sub * L::kKeys, gw, j > 0);
             mma_commit_warp(bar(c, (gw & 1 ? kBarOOdd : kBarODone) + w));
             if (last_sub)
                 mma_commit_warp(bar(c, kBarVEmpty + st));
@@ -471,14 +488,14 @@ __device__ __forceinline__ uint32_t tile_word(const Ctx &c, const Rec &s, int k,
     return w;
 }
 
-template <int D>
+template <int D, int G>
 __device__ void mask_stager(const Ctx &c, int lane)
 {
-    using L = Layout<D>;
+    using L = Layout<D, G>;
     int *err = c.a.err;
     Rec s;
     uint32_t g = 0, masked = 0, with_bits = 0;
-    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
+    for (uint32_t sg = 0; read_rec<D, G>(c, sg, lane, s); ++sg) {
         for (int k = s.kb; k < s.ke; ++k, ++g) {
             const int st = g % L::kStages;
             // every tile is waited for and handed back, seen or not, so that
@@ -578,10 +595,10 @@ __device__ __forceinline__ uint32_t weights(float x0, float x1, uint64_t sc2, ui
     return pk;
 }
 
-template <int D, bool kHalf>
+template <int D, int G, bool kHalf>
 __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, int cta)
 {
-    using L = Layout<D>;
+    using L = Layout<D, G>;
     constexpr int kKeys = L::kKeys;
     constexpr float kLift = kHalf ? 7.f : 0.f;        // weights times 2^7 in fp16
     int *err = c.a.err;
@@ -597,8 +614,8 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
     };
     Rec s;
     uint32_t gw = 0, with_bits = 0;
-    for (uint32_t sg = 0; read_rec<D>(c, sg, lane, s); ++sg) {
-        const int n = seg_steps<D>(s);
+    for (uint32_t sg = 0; read_rec<D, G>(c, sg, lane, s); ++sg) {
+        const int n = seg_steps<D, G>(s);
         if (w == 1 && !second_tile(s)) {
             // nothing to do but hand the key bits on
             for (int k = s.kb; k < s.ke && needs_bits(s); ++k) {
@@ -753,14 +770,14 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
         tc_fence_after();
         const bool whole = s.ke - s.kb == s.tiles;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        float *part = c.a.parts + (2ll * cta + (s.kb == 0)) * cross_slot_floats(kCrossBlockRows, D);
+        float *part = c.a.parts + (2ll * cta + (s.kb == 0)) * cross_slot_floats(L::kUnitRows, D);
         // this warp's rows of the output, those that the sequence has
         const int warp_row = kBlockM * w + 32 * warp_in_group;
         const int warp_rows = min(32, s.rows - s.q0 - warp_row);
         const int fold = c.a.fold_log2;
         uint16_t *out = static_cast<uint16_t *>(c.a.out) + static_cast<long long>(s.q_row) * c.a.out_row +
                         static_cast<long long>(s.head) * D;
-        uint8_t *stage = c.sbase + L::kOffOut + (4 * w + warp_in_group) * 4096;
+        uint8_t *stage = c.sbase + L::kOffOut + (4 * w + warp_in_group) * (L::kOutRows * 128);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
             float o[64];
@@ -784,37 +801,42 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                 // whole lines of 4 rows and not 16 bytes of 32 (chunk j of row
                 // r at j ^ (r & 7): no bank conflicts either way)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4 *>(stage + 128 * lane + 16 * (i ^ (lane & 7))) =
-                        make_uint4(pack2<kHalf>(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                   pack2<kHalf>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                   pack2<kHalf>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                   pack2<kHalf>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-                __syncwarp();
+                for (int r0 = 0; r0 < 32; r0 += L::kOutRows) {
+                    if (L::kOutRows == 32 || lane / L::kOutRows == r0 / L::kOutRows) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(stage + 128 * (lane % L::kOutRows) + 16 * (i ^ (lane & 7))) =
+                                make_uint4(pack2<kHalf>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                           pack2<kHalf>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                           pack2<kHalf>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                           pack2<kHalf>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                    }
+                    __syncwarp();
 #pragma unroll 2
-                for (int i = 0; i < 8; ++i) {
-                    const int row = 4 * i + lane / 8, part = lane % 8;
-                    const int at = s.q0 + warp_row + row;       // row of the sequence
-                    if (row < warp_rows)
-                        *reinterpret_cast<uint4 *>(out + (at >> fold) * c.a.out_row +
-                                                   (at & ((1 << fold) - 1)) * D + 64 * h + 8 * part) =
-                            *reinterpret_cast<const uint4 *>(stage + 128 * row + 16 * (part ^ (row & 7)));
+                    for (int i = 0; i < L::kOutRows / 4; ++i) {
+                        const int row = 4 * i + lane / 8, part = lane % 8;
+                        const int at = s.q0 + warp_row + r0 + row;       // row of the sequence
+                        if (r0 + row < warp_rows)
+                            *reinterpret_cast<uint4 *>(out + (at >> fold) * c.a.out_row +
+                                                       (at & ((1 << fold) - 1)) * D + 64 * h + 8 * part) =
+                                *reinterpret_cast<const uint4 *>(stage + 128 * row + 16 * (part ^ (row & 7)));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             } else {
                 // [D/4][256 rows] float4: neighbouring rows side by side
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    reinterpret_cast<float4 *>(part)[(16 * h + i) * kCrossBlockRows + rr] =
+                    reinterpret_cast<float4 *>(part)[(16 * h + i) * L::kUnitRows + rr] =
                         make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
         }
         if (!whole)
-            reinterpret_cast<float2 *>(part + kCrossBlockRows * D)[rr] = make_float2(m, l);
+            reinterpret_cast<float2 *>(part + L::kUnitRows * D)[rr] = make_float2(m, l);
         if (!whole && s.kb == 0 && rr == 0) {
             CrossRecord rec;
             rec.row0 = static_cast<long long>(s.q_row) + (s.q0 >> fold);
-            rec.rows = min(kCrossBlockRows, s.rows - s.q0);
+            rec.rows = min(L::kUnitRows, s.rows - s.q0);
             rec.head0 = s.head;
             rec.group = 1 << fold;
             rec.parts = s.parts;
@@ -823,11 +845,11 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
     }
 }
 
-template <int D, bool kHalf>
-__global__ void __launch_bounds__(Layout<D>::kThreads, 1)
+template <int D, int G, bool kHalf>
+__global__ void __launch_bounds__(Layout<D, G>::kThreads, Layout<D, G>::kCtas)
 attn_cross_kernel(const __grid_constant__ CrossArgs a)
 {
-    using L = Layout<D>;
+    using L = Layout<D, G>;
     pdl_wait();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -836,12 +858,19 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
     uint32_t *slot = reinterpret_cast<uint32_t *>(sbase + L::kOffBar + kSlotInBars);
     const int cta = blockIdx.x;
 
+    // TMEM first: the next CTA of this SM only starts once this one has given
+    // up its right to allocate
+    if (threadIdx.x < 32) {
+        tmem_alloc(smem_u32(slot), L::kTmemCols);
+        tmem_relinquish();
+    }
     if (threadIdx.x == 0 && a.records)
         a.records[cta].parts = 0;
-    Split<D> split(a, a.heads >> a.fold_log2);
+    static_assert(sizeof(typename Split<D, G>::Deal) <= 4 * G * L::kOutRows * 128, "dealing");
+    Split<D, G> split(a, a.heads >> a.fold_log2);
     // two tiles and a unit's fixed work per CTA at least
-    const bool work = split.find(*reinterpret_cast<typename Split<D>::Scratch *>(sbase + L::kOffScratch), gridDim.x, 22,
-                                 reinterpret_cast<typename Split<D>::Deal *>(sbase + L::kOffOut));
+    const bool work = split.find(*reinterpret_cast<typename Split<D, G>::Scratch *>(sbase + L::kOffScratch), gridDim.x, 22,
+                                 reinterpret_cast<typename Split<D, G>::Deal *>(sbase + L::kOffOut));
     if (work) {
         Ctx c{base, 0u, sbase, a, base + L::kOffBar};
         const int warp = threadIdx.x >> 5;
@@ -852,13 +881,13 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
             tma_prefetch_desc(&a.tm_v);
             for (int q = 0; q < L::kQSets; ++q) {
                 mbar_init(bar(c, kBarQFull + q), 1);
-                mbar_init(bar(c, kBarQEmpty + q), 2);   // one commit per issuer
+                mbar_init(bar(c, kBarQEmpty + q), G);   // one commit per issuer
             }
             for (int st = 0; st < L::kStages; ++st) {
                 mbar_init(bar(c, kBarKFull + st), 1);
-                mbar_init(bar(c, kBarKEmpty + st), 2);
+                mbar_init(bar(c, kBarKEmpty + st), G);
                 mbar_init(bar(c, kBarVFull + st), 1);
-                mbar_init(bar(c, kBarVEmpty + st), 3);  // and the mask warp
+                mbar_init(bar(c, kBarVEmpty + st), G + 1);  // and the mask warp
             }
             for (int w = 0; w < 2; ++w) {
                 mbar_init(bar(c, kBarSFull + w), 1);
@@ -875,70 +904,67 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
             }
             for (int i = 0; i < kMaskSlots; ++i) {
                 mbar_init(bar(c, kBarBitsFull + i), 1);
-                mbar_init(bar(c, kBarBitsEmpty + i), 2 * kBlockM);
+                mbar_init(bar(c, kBarBitsEmpty + i), L::kUnitRows);
                 mbar_init(bar(c, kBarVClean + i), 1);
             }
             fence_mbar_init();
-        }
-        if (warp == 0) {
-            tmem_alloc(smem_u32(slot), kTmemCols);
-            tmem_relinquish();
         }
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
         c.tmem = *slot;
 
-        if (warp >= 8) {
+        if (warp >= L::kControl) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(L::kRegsControl));
-            if (warp == 8) {
+            if (warp == L::kControl) {
                 if (lane == 0)
-                    producer<D>(c, split);
-            } else if (warp == 9) {
-                mask_stager<D>(c, lane);
-            } else if (warp == 10 || warp == 11) {
+                    producer<D, G>(c, split);
+            } else if (warp == L::kControl + 1) {
+                mask_stager<D, G>(c, lane);
+            } else if (warp < L::kControl + 2 + G) {
                 if constexpr (L::kSplitIssuers)
-                    s_issuer<D, kHalf>(c, warp - 10, lane);
+                    s_issuer<D, G, kHalf>(c, warp - L::kControl - 2, lane);
                 else
-                    so_issuer<kHalf>(c, warp - 10, lane);
-            } else if (warp == 12 || warp == 13) {
+                    so_issuer<G, kHalf>(c, warp - L::kControl - 2, lane);
+            } else if (warp < L::kControl + 2 + 2 * G) {
                 if constexpr (L::kSplitIssuers)
-                    o_issuer<D, kHalf>(c, warp - 12, lane);
+                    o_issuer<D, G, kHalf>(c, warp - L::kControl - 2 - G, lane);
             }
             __syncwarp();
         } else {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(L::kRegsSoftmax));
-            softmax_group<D, kHalf>(c, warp >> 2, warp & 3, lane, cta);
+            softmax_group<D, G, kHalf>(c, warp >> 2, warp & 3, lane, cta);
             __syncwarp();
         }
-
-        tc_fence_before();
-        __syncthreads();
-        if (warp == 0) {
-            tc_fence_after();
-            tmem_dealloc(c.tmem, kTmemCols);
-        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        tc_fence_after();
+        tmem_dealloc(*slot, L::kTmemCols);
     }
     pdl_trigger();
 }
 
-template <int D, bool kHalf>
+template <int D, int G, bool kHalf>
 cudaError_t launch(const CrossArgs &a, int ctas, cudaStream_t stream)
 {
     static PerDeviceOnce smem_once;
-    cudaError_t e = smem_opt_in(smem_once, attn_cross_kernel<D, kHalf>, Layout<D>::kSmemBytes);
+    cudaError_t e = smem_opt_in(smem_once, attn_cross_kernel<D, G, kHalf>, Layout<D, G>::kSmemBytes);
     if (e != cudaSuccess)
         return e;
-    return launch_chained(attn_cross_kernel<D, kHalf>, dim3(ctas), dim3(Layout<D>::kThreads), Layout<D>::kSmemBytes, stream, a);
+    return launch_chained(attn_cross_kernel<D, G, kHalf>, dim3(ctas), dim3(Layout<D, G>::kThreads), Layout<D, G>::kSmemBytes, stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_blocks(const CrossArgs &a, int dim, bool half, int ctas, cudaStream_t stream)
+cudaError_t launch_cross_blocks(const CrossArgs &a, int dim, bool half, int unit_rows, int ctas, cudaStream_t stream)
 {
+    if (dim == 64 && unit_rows == kCrossSmallRows)
+        return half ? launch<64, 1, true>(a, ctas, stream) : launch<64, 1, false>(a, ctas, stream);
     if (dim == 64)
-        return half ? launch<64, true>(a, ctas, stream) : launch<64, false>(a, ctas, stream);
-    return half ? launch<128, true>(a, ctas, stream) : launch<128, false>(a, ctas, stream);
+        return half ? launch<64, 2, true>(a, ctas, stream) : launch<64, 2, false>(a, ctas, stream);
+    return half ? launch<128, 2, true>(a, ctas, stream) : launch<128, 2, false>(a, ctas, stream);
 }
 
 }  // namespace mbert

@@ -156,6 +156,10 @@ template <int D, bool kHalf>
 cudaError_t join(const CrossArgs &a, int rows, int ctas, cudaStream_t stream)
 {
     constexpr int kGroups = 128 / (D / 8);      // 128 threads for one row's parts
+    if (rows == kCrossSmallRows)
+        return launch_chained(cross_join_kernel<D, kHalf, kCrossSmallRows, 32, 1>,
+                              dim3(ctas, kCrossSmallRows / 32), dim3(32 * (D / 8)), 0, stream, a.records,
+                              a.parts, a.out, a.out_row);
     if (rows > kCrossTokenRows)
         return launch_chained(cross_join_kernel<D, kHalf, kCrossBlockRows, 32, 1>,
                               dim3(ctas, kCrossBlockRows / 32), dim3(32 * (D / 8)), 0, stream, a.records,

@@ -29,16 +29,26 @@
 
 namespace mbert {
 
+// Quotient of numbers >= 0: most calls' costs fit 32 bits, whose division takes
+// a fifth of the instructions.
+__device__ __forceinline__ long long div_cost(long long x, long long y)
+{
+    if ((x | y) >> 32)
+        return x / y;
+    return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+}
+
 // kBlockQ: query rows of a unit (0: all of a sequence's), each the rows of
 // 2^fold_log2 heads, side by side; kTile: keys of a tile; kRounds 0: units are
-// never dealt out whole.
+// never dealt out whole; kPerSm: CTAs of an SM.
 template <int kThreads, int kBlockQ_, int kTile_, int kFull_, int kHalf_, int kAlpha_, int kSnap_, int kRounds = 0,
-          int kJoin = 0>
+          int kJoin = 0, int kPerSm = 1>
 struct CrossSplit {
     static constexpr int kBlockQ = kBlockQ_, kTile = kTile_, kSnap = kSnap_;
     static constexpr int kFull = kFull_, kHalf = kHalf_, kAlpha = kAlpha_;
     static constexpr int kWarps = kThreads / 32;
     static constexpr int kDealSeqs = 128;       // sequences whose units are dealt out, at most
+    static_assert(kRounds == 0 || 2 * kDealSeqs <= kThreads, "two threads per sequence");
 
     struct Scratch {
         long long warp[kWarps];
@@ -49,8 +59,9 @@ struct CrossSplit {
     };
     // What dealing takes besides, while find() runs.
     struct Deal {
-        int cost[kDealSeqs], last[kDealSeqs], blocks[kDealSeqs], units[kDealSeqs];
-        int sum[kThreads];
+        int2 need[kDealSeqs];           // cost of a whole block, units
+        int2 tail[kDealSeqs];           // cost of the last block, blocks
+        int2 order[kDealSeqs];          // by length: first unit, sequence
     };
 
     // What a sequence needs: rows, tiles, blocks of query rows.
@@ -78,9 +89,9 @@ struct CrossSplit {
     {
         const long long ch = q.head(), cb = q.block();
         Place p;
-        p.head = static_cast<int>((x - base) / ch);
+        p.head = static_cast<int>(div_cost(x - base, ch));
         const long long h0 = base + p.head * ch;
-        const long long b = (x - h0) / cb;
+        const long long b = div_cost(x - h0, cb);
         p.b = b < q.whole ? static_cast<int>(b) : q.whole;
         p.per = p.b < q.whole ? kFull : kHalf;
         p.xa = h0 + p.b * cb;
@@ -140,13 +151,13 @@ struct CrossSplit {
 
     __device__ __forceinline__ long long border(int c) const
     {
-        return static_cast<long long>(c) * total / ctas;
+        return div_cost(c * total, ctas);
     }
 
     // The CTA whose range holds x (borders inside long units do not move).
     __device__ __forceinline__ int cta_of(long long x) const
     {
-        return static_cast<int>(((x + 1) * ctas - 1) / total);
+        return static_cast<int>(div_cost((x + 1) * ctas - 1, total));
     }
 
     // Every thread of the block.  min_cost: of a CTA, at least kFull, so that
@@ -201,7 +212,7 @@ struct CrossSplit {
             total += sm.warp[w];
         if (total == 0)
             return false;
-        const long long want = total / min_cost;
+        const long long want = div_cost(total, min_cost);
         ctas = want < 1 ? 1 : want < max_ctas ? static_cast<int>(want) : max_ctas;
         if constexpr (kRounds > 0) {
             int all = 0, longest = 0;
@@ -210,9 +221,13 @@ struct CrossSplit {
                 all += sm.units[w];
                 longest = max(longest, sm.most[w]);
             }
-            const long long limit = a.records ? total / ctas + kJoin : INT64_MAX;
-            if (a.n_seqs <= kDealSeqs && max_ctas <= kThreads && all <= kRounds * max_ctas &&
-                static_cast<long long>(longest) * kFull + kAlpha <= limit && deal(sm, *work, max_ctas, limit)) {
+            // an SM gets its second unit when every one has a first (152 units over
+            // 512 keys: 14.1 -> 10.8 us)
+            if (kPerSm == 2 && all <= max_ctas / 2 && !a.records)
+                ctas = min(ctas, max_ctas / 2);
+            const long long limit = a.records ? div_cost(total, ctas) + kJoin : INT64_MAX;
+            if (a.n_seqs <= kDealSeqs && all <= kRounds * max_ctas &&
+                static_cast<long long>(longest) * kFull + kAlpha <= limit && deal(sm, *work, max_ctas, all, limit)) {
                 dealt = &sm;
                 return sm.deal_seq[0] >= 0;
             }
@@ -265,42 +280,77 @@ struct CrossSplit {
     }
 
     // Deals the units out whole: true if no CTA gets more than `limit`.
-    __device__ bool deal(Scratch &sm, Deal &d, int n, long long limit)
+    __device__ bool deal(Scratch &sm, Deal &d, int n, int all, long long limit)
     {
-        const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+        const int tid = threadIdx.x;
+        constexpr int kStep = 8;
         if (tid < a.n_seqs) {
             const Seq q = load(tid);
             const int full = q.tiles * kFull + kAlpha, half = q.tiles * kHalf + kAlpha;
-            d.last[tid] = q.half ? half : full;
-            d.cost[tid] = q.whole ? full : half;
-            d.blocks[tid] = q.whole + q.half;
-            d.units[tid] = unit_heads * (q.whole + q.half);
+            d.need[tid] = make_int2(q.whole ? full : half, unit_heads * (q.whole + q.half));
+            d.tail[tid] = make_int2(q.half ? half : full, q.whole + q.half);
+        } else if (tid < kDealSeqs) {
+            d.need[tid] = make_int2(-1, 0);             // shorter than any
+            d.order[tid] = make_int2(INT32_MAX, 0);     // behind all
         }
-        if (tid < n)
-            d.sum[tid] = 0;
         if (tid <= kRounds)
             sm.deal_seq[tid] = -1;
         __syncthreads();
-        // a warp per sequence: the units of those with longer ones come first
-        for (int s = warp; s < a.n_seqs; s += kWarps) {
-            const int mine = d.cost[s], last = d.last[s], blocks = d.blocks[s], units = d.units[s];
-            int start = 0;
-            for (int o = lane; o < a.n_seqs; o += 32)
-                if (d.cost[o] > mine || (d.cost[o] == mine && o < s))
-                    start += d.units[o];
-            start = __reduce_add_sync(0xffffffffu, start);
-            for (int j = lane; j < units; j += 32) {
-                const int round = (start + j) / n, at = start + j - round * n;
-                const int cta = round & 1 ? n - 1 - at : at;
-                atomicAdd(&d.sum[cta], j % blocks == blocks - 1 ? last : mine);
-                if (cta == static_cast<int>(blockIdx.x)) {
-                    sm.deal_seq[round] = s;
-                    sm.deal_unit[round] = j;
+        // two threads per sequence: the units of the longer ones come first
+        {
+            const int s = tid / 2, mine = s < a.n_seqs ? d.need[s].x : 0;
+            int rank = 0, start = 0;
+            for (int o = tid % 2 * kStep; o < a.n_seqs; o += 2 * kStep) {
+                int2 x[kStep];
+#pragma unroll
+                for (int i = 0; i < kStep; ++i)
+                    x[i] = d.need[o + i];
+#pragma unroll
+                for (int i = 0; i < kStep; ++i) {
+                    const bool before = x[i].x > mine || (x[i].x == mine && o + i < s);
+                    rank += before;
+                    start += before ? x[i].y : 0;
                 }
             }
+            rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+            start += __shfl_xor_sync(0xffffffffu, start, 1);
+            if (s < a.n_seqs && tid % 2 == 0)
+                d.order[rank] = make_int2(start, s);
         }
         __syncthreads();
-        return !__syncthreads_or(tid < n && d.sum[tid] > limit);
+        // a thread per CTA: its units, one of each round, of the last sequence
+        // that starts at them or before (the rounds' searches side by side)
+        int top = 1;
+        while (2 * top < a.n_seqs)
+            top *= 2;
+        bool over = false;
+        for (int c = tid; c < n; c += kThreads) {
+            int at[kRounds], lo[kRounds];
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r) {
+                at[r] = r * n + (r & 1 ? n - 1 - c : c);
+                lo[r] = 0;
+            }
+            for (int step = top; step > 0; step /= 2)
+#pragma unroll
+                for (int r = 0; r < kRounds; ++r)
+                    if (d.order[lo[r] + step].x <= at[r])
+                        lo[r] += step;
+            long long sum = 0;
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r)
+                if (at[r] < all) {
+                    const int2 x = d.order[lo[r]], tail = d.tail[x.y];
+                    const int unit = at[r] - x.x;
+                    sum += unit % tail.y == tail.y - 1 ? tail.x : d.need[x.y].x;
+                    if (c == static_cast<int>(blockIdx.x)) {
+                        sm.deal_seq[r] = x.y;
+                        sm.deal_unit[r] = unit;
+                    }
+                }
+            over |= sum > limit;
+        }
+        return !__syncthreads_or(over);
     }
 
     __device__ __forceinline__ long long snap(long long x, int s, long long base) const
@@ -369,8 +419,8 @@ struct CrossSplit {
                 continue;
             }
             const Place p = place(it.s, it.base, it.x);
-            const int kb = static_cast<int>((it.x - p.xa + p.per - 1) / p.per);
-            const long long cut = (hi - p.xa + p.per - 1) / p.per;
+            const int kb = static_cast<int>(div_cost(it.x - p.xa + p.per - 1, p.per));
+            const long long cut = div_cost(hi - p.xa + p.per - 1, p.per);
             g.ke = cut < it.s.tiles ? static_cast<int>(cut) : it.s.tiles;
             it.x = p.end;
             if (kb >= g.ke)

@@ -299,13 +299,14 @@ int cross_plan(const mbert_attn *h, const mbert_attn_cross_args *c, CrossPlan *p
     // up to 16 rows per (sequence, key head): the kernel that reads K and V
     // once for all of them
     p->token = most * p->group <= kCrossTokenRows;
-    p->ctas = p->token ? h->num_sms * cross_token_ctas(c->head_dim) : h->num_sms;
-    p->unit_rows = p->token ? kCrossTokenRows : kCrossBlockRows;
     p->fold_log2 = 0;
     while (!p->token && p->fold_log2 < 7 && (p->group >> p->fold_log2) % 2 == 0)
         ++p->fold_log2;
     if (most << p->fold_log2 > INT32_MAX)
         return MBERT_ERR_BAD_ARG;   // (more than any device holds)
+    const bool small = c->head_dim == 64 && most << p->fold_log2 <= kCrossSmallRows;
+    p->unit_rows = p->token ? kCrossTokenRows : small ? kCrossSmallRows : kCrossBlockRows;
+    p->ctas = h->num_sms * (p->token ? cross_token_ctas(c->head_dim) : cross_block_ctas(p->unit_rows));
     const int64_t longest = c->cu_k || c->n_seqs == 0 ? c->rows_k : c->rows_k / c->n_seqs;
     p->join = longest > (p->token ? kCrossTokenWholeRows : kCrossBlockWholeRows);
     p->records = 0;
@@ -433,10 +434,10 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
         h->launches += 1;
     }
     if (e == cudaSuccess)
-        e = p.token ? launch_cross_token(a, D, half, p.ctas, st) : launch_cross_blocks(a, D, half, p.ctas, st);
+        e = p.token ? launch_cross_token(a, D, half, p.ctas, st) : launch_cross_blocks(a, D, half, p.unit_rows, p.ctas, st);
     h->launches += 1;
     if (e == cudaSuccess && p.join) {
-        e = launch_cross_join(a, D, half, p.token ? p.max_q * p.group : kCrossBlockRows, p.ctas, st);
+        e = launch_cross_join(a, D, half, p.token ? p.max_q * p.group : p.unit_rows, p.ctas, st);
         h->launches += 1;
     }
     h->last_stream = st;

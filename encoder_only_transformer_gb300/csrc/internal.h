@@ -309,7 +309,10 @@ struct CrossRecord {
     int parts;          // 0: CTA c holds no first part
 };
 
-constexpr int kCrossBlockRows = 256;    // rows of a unit of attn_cross.cu
+// Rows of a unit of attn_cross.cu: two query tiles, or one for head size 64 in
+// calls whose sequences have no more (both measured there).
+constexpr int kCrossBlockRows = 256;
+constexpr int kCrossSmallRows = 128;
 constexpr int kCrossTokenRows = 16;     // rows of a unit of attn_cross_token.cu
 
 // Units of at most this many keys are not cut between CTAs (blocks of queries,
@@ -332,13 +335,16 @@ constexpr long long cross_slot_floats(int rows, int dim) { return static_cast<lo
 // CTAs of the token kernel on one SM (by shared memory and registers).
 constexpr int cross_token_ctas(int dim) { return dim == 64 ? 3 : 2; }
 
+// CTAs of the kernel for blocks of queries on one SM.
+constexpr int cross_block_ctas(int unit_rows) { return unit_rows == kCrossSmallRows ? 2 : 1; }
+
 // key_mask [rows_k] (non-zero: visible) to bits and lengths per sequence.
 cudaError_t launch_key_bits(const CrossArgs &a, const int32_t *key_mask, uint32_t *bits, int2 *len,
                             cudaStream_t stream);
-cudaError_t launch_cross_blocks(const CrossArgs &a, int dim, bool half, int ctas, cudaStream_t stream);
+cudaError_t launch_cross_blocks(const CrossArgs &a, int dim, bool half, int unit_rows, int ctas, cudaStream_t stream);
 cudaError_t launch_cross_token(const CrossArgs &a, int dim, bool half, int ctas, cudaStream_t stream);
-// Joins the parts of cut units; rows: those of a unit (kCrossBlockRows after
-// the first kernel, at most kCrossTokenRows after the second).
+// Joins the parts of cut units; rows: those of a unit (kCrossBlockRows or
+// kCrossSmallRows after the first kernel, at most kCrossTokenRows after the second).
 cudaError_t launch_cross_join(const CrossArgs &a, int dim, bool half, int rows, int ctas, cudaStream_t stream);
 
 // Number of sequences up to which the local kernel finds its blocks itself

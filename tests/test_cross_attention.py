@@ -185,6 +185,29 @@ def test_whole_units(built, ql, kl, H, D, dtype):
     assert torch.equal(run_packed(ql, kl, H, H, D, dtype, seed=len(ql), behind=2, mask=mask), got)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("ql,kl,H,Hk,max_q", [
+    ([128, 17, 0, 65], [300, 1, 50, 0], 2, 2, 128),
+    ([40, 100, 1], [129, 700, 640], 12, 12, 100),           # longer than what is never cut
+    ([17] * 3, [4000, 10, 2000], 3, 3, 17),                 # cut
+    ([16, 3, 11], [333, 1500, 64], 32, 8, 16),              # four heads share a block's rows
+    ([1], [900], 256, 1, 1),                                # 128 of 256 heads do
+    ([30] * 64, [520 + 2 * i for i in range(64)], 6, 6, 30),    # dealt out whole
+    ([20] * 130, [100 + i for i in range(130)], 10, 10, 20),
+])
+def test_small_blocks(built, ql, kl, H, Hk, max_q, masked, dtype):
+    """At most 128 rows a sequence: one query tile to a block."""
+    mask = None
+    if masked:
+        g = torch.Generator().manual_seed(len(ql))
+        mask = torch.rand(sum(kl), generator=g) < 0.7
+        mask[offsets(kl)[-2]:] = False                      # nothing of the last sequence
+    got = run_packed(ql, kl, H, Hk, 64, dtype, max_q=max_q, seed=len(ql), behind=2, mask=mask)
+    assert torch.equal(run_packed(ql, kl, H, Hk, 64, dtype, max_q=max_q, seed=len(ql), behind=2, mask=mask), got)
+
+
 TOKENS = [
     # query lengths, key lengths, heads, key heads, longest query sequence
     ([1], [1], 1, 1, 1),
