@@ -586,7 +586,7 @@ class Attention:
         last sequence are left as they were.  max_seqlen_q is the caller's bound
         on the longest query sequence: give it for single tokens (at most
         16 / (Hq / Hk) rows a sequence), which then read k and v once, and for
-        short ones (128 / (Hq / Hk) too, D 64).  scale
+        short ones (128 / (Hq / Hk)).  scale
         None: 1 / sqrt(D).  Rows may be strided (views of fused rows)."""
         max_seqlen_q, scale = int(max_seqlen_q), None if scale is None else float(scale)
         key = ("cross", _layout(q, k, v, cu_seqlens_q, cu_seqlens_k), None if out is None else _layout(out),

@@ -5,12 +5,13 @@
 //   i's sequence; 0 where there is none
 //
 // Work: a unit is 256 query rows of one sequence and head (two tiles of 128;
-// G = 2 below) or, for head size 64 in calls whose sequences have no more than
-// 128 rows, one such tile (G = 1, with two CTAs an SM: a unit's start and end
-// then lie beside the other one's tiles, and no softmax warps stand idle; 64
-// sequences of 30 queries over 600 keys 45 -> 32 us, 100 of 20 over 250 39 -> 30,
-// but for 256 rows and more 200 us against 195 and 35 against 33, as K and V are
-// fetched twice as often); units and their 128-key tiles are split among the CTAs by cost
+// G = 2 below) or, in calls whose sequences have no more than 128 rows, one such
+// tile (G = 1, with two CTAs an SM: a unit's start and end then lie beside the
+// other one's tiles, and no softmax warps stand idle; D = 64, 64 sequences of 30
+// queries over 600 keys 45 -> 32 us, 100 of 20 over 250 39 -> 30; D = 128, 24 of
+// 32 over 1000, 32 heads over 8, 36 -> 30; but for 256 rows and more, D = 64, 200
+// us against 195 and 35 against 33, as K and V are fetched twice as often); units
+// and their tiles of 128 keys (D = 128, G = 1: 64) are split among the CTAs by cost
 // (cross_sched.cuh), and units cut between CTAs are joined by a second kernel
 // (cross_join.cu) in a fixed order.  Query heads that share a key head share
 // the blocks too: with F the largest power of two that divides their number,
@@ -71,14 +72,18 @@ namespace {
 constexpr int kMaskSlots = 4;
 
 // Costs, by a fit over the CTAs' times in clocks: a key tile for both query
-// tiles 2200 (D = 64) and 2900 (D = 128), for one 1750 and 1850 (G = 1: 2150,
-// beside another CTA's); a unit's fixed
+// tiles 2200 (D = 64) and 2900 (D = 128), for one 1750 and 1850 (G = 1: beside
+// another CTA's 2150, and 1450 for 64 keys of D = 128); a unit's fixed
 // work (the end of the softmax, the output, the refill) 3500 and 4700.  Units
-// stay whole, up to four to a CTA, where that puts no more than 34 (6 us) on
-// top of a CTA's share.
+// stay whole, up to four to a CTA, where that puts no more than 34 (6 us; 72, 9
+// us, for G = 1 of D = 128, where joining the parts of 304 CTAs takes longer: 24
+// sequences of 32 over 1000, 43 above the share, 30 us, 36 cut) on top of a CTA's
+// share.
 template <int D, int G>
-using Split = CrossSplit<D == 128 ? 512 : G == 2 ? 384 : 256, kBlockM * G, kBlockN, 6, G == 1 ? 6 : D == 64 ? 5 : 4, 10,
-                         kCrossBlockWholeKeys / kBlockN, 4, 34, cross_block_ctas(kBlockM * G)>;
+using Split = CrossSplit<G == 1 ? 256 : D == 64 ? 384 : 512, kBlockM * G, cross_tile_keys(D, kBlockM * G), 6,
+                         G == 1 ? 6 : D == 64 ? 5 : 4, D == 128 && G == 1 ? 20 : 10,
+                         kCrossBlockWholeKeys / cross_tile_keys(D, kBlockM * G), 4, D == 128 && G == 1 ? 72 : 34,
+                         cross_block_ctas(kBlockM * G), D == 64 ? 5 : 2>;
 
 // G: query tiles of a unit, a softmax group for each.
 template <int D, int G>
@@ -88,19 +93,22 @@ struct Layout {
     static constexpr int kUnitRows = kBlockM * G;
     static constexpr int kCtas = cross_block_ctas(kUnitRows);
     static constexpr int kControl = 4 * G;              // first warp after the softmax groups
-    static constexpr int kThreads = kSplitIssuers ? 512 : 32 * (kControl + 4);
+    static constexpr int kThreads = 32 * (kControl + (kSplitIssuers && G == 2 ? 8 : 4));
     // registers a thread: 4 x 72 + 8 x 216 = 12 x 168, 8 x 56 + 8 x 200 = 16 x 128,
     // 4 x 56 + 4 x 200 = 8 x 128
     static constexpr int kRegsSoftmax = kPair ? 216 : 200;
     static constexpr int kRegsControl = kPair ? 72 : 56;
-    static constexpr int kRecReaders = kSplitIssuers ? 13 : 5 * G + 1;   // issuers, softmax warps, the mask warp
+    static constexpr int kRecReaders = (kSplitIssuers ? 6 : 5) * G + 1;   // issuers, softmax warps, the mask warp
     static constexpr int kKeys = D == 64 ? 128 : 64;    // keys of a step (an S)
-    static constexpr int kSteps = kBlockN / kKeys;      // steps of a tile
+    static constexpr int kTileKeys = cross_tile_keys(D, kUnitRows);
+    static constexpr int kSteps = kTileKeys / kKeys;    // steps of a tile
     static constexpr int kHalves = D / 64;              // 64-column boxes of a tile
-    static constexpr uint32_t kTile = kHalves * kTileBytes;
+    static constexpr uint32_t kQTile = kHalves * kTileBytes;
+    static constexpr uint32_t kBox = kTileKeys * 128;   // of K or V: 64 columns
+    static constexpr uint32_t kTile = kHalves * kBox;
     static constexpr int kQSets = D == 64 ? 2 : 1;      // of G query tiles
     static constexpr int kStages = kPair ? 3 : 2;     // of K and of V
-    static constexpr uint32_t kOffK = kQSets * G * kTile;
+    static constexpr uint32_t kOffK = kQSets * G * kQTile;
     static constexpr uint32_t kOffV = kOffK + kStages * kTile;
     static constexpr uint32_t kOffOut = kOffV + kStages * kTile;    // 4 KB per softmax warp: 32 rows x 64 columns
     static constexpr uint32_t kOutRows = kCtas == 2 ? 16 : 32;   // rows that a warp stages at a time
@@ -112,12 +120,12 @@ struct Layout {
     // S and P of query tile w's step (D = 128: two buffers in turn), O
     static constexpr uint32_t col_s(int w, uint32_t step) { return 128u * w + (D == 64 ? 0u : 64u * (step & 1)); }
     static constexpr uint32_t col_p(int w, uint32_t step) { return D == 64 ? 128u * G + 64u * w : col_s(w, step); }
-    static constexpr uint32_t col_o(int w) { return D == 64 ? 192u * G + 64u * w : 256u + 128u * w; }
+    static constexpr uint32_t col_o(int w) { return D == 64 ? 192u * G + 64u * w : 128u * G + 128u * w; }
     static constexpr uint32_t kTmemCols = 256 * G;
 };
 // (1 KB of an SM's 228 is the system's for each CTA)
 static_assert(Layout<64, 2>::kSmemBytes <= 232448 && Layout<128, 2>::kSmemBytes <= 232448 &&
-                  Layout<64, 1>::kSmemBytes <= 115712,
+                  Layout<64, 1>::kSmemBytes <= 115712 && Layout<128, 1>::kSmemBytes <= 115712,
               "shared memory");
 
 // barrier slots (8 bytes each)
@@ -192,7 +200,8 @@ __device__ __forceinline__ bool read_rec(const Ctx &c, uint32_t sg, int lane, Re
 
 // A tile whose keys are not all known to be visible, and one of a sequence with
 // hidden keys among the visible ones, which needs their bits.
-__device__ __forceinline__ bool needs_mask(const Rec &s, int k) { return s.k_full - k * kBlockN < kBlockN; }
+template <int kTileKeys>
+__device__ __forceinline__ bool needs_mask(const Rec &s, int k) { return s.k_full - k * kTileKeys < kTileKeys; }
 __device__ __forceinline__ bool needs_bits(const Rec &s) { return s.k_full < s.k_len; }
 
 // The unit's second query tile holds rows.
@@ -244,27 +253,27 @@ __device__ void producer(const Ctx &c, const Split<D, G> &split)
             return;
         const int col_k = s.head / c.a.group * D;
         const int fold = c.a.fold_log2, qrow = s.q_row + (s.q0 >> fold);
-        const uint32_t qdst = c.base + qs * G * L::kTile;
-        mbar_arrive_expect_tx(bar(c, kBarQFull + qs), (two ? 2 : 1) * L::kTile);
+        const uint32_t qdst = c.base + qs * G * L::kQTile;
+        mbar_arrive_expect_tx(bar(c, kBarQFull + qs), (two ? 2 : 1) * L::kQTile);
         for (int w = 0; w < (two ? 2 : 1); ++w)
             for (int h = 0; h < L::kHalves; ++h)
-                tma_load_3d(qdst + w * L::kTile + h * kTileBytes, &c.a.tm_q, 64 * h, s.head,
+                tma_load_3d(qdst + w * L::kQTile + h * kTileBytes, &c.a.tm_q, 64 * h, s.head,
                             qrow + w * (kBlockM >> fold), bar(c, kBarQFull + qs));
         for (int k = s.kb; k < s.ke; ++k, ++g) {
             const int st = g % L::kStages;
             const uint32_t u = g / L::kStages;
-            const int krow = s.k_row + k * kBlockN;
+            const int krow = s.k_row + k * L::kTileKeys;
             if (u > 0 && !mbar_wait(bar(c, kBarKEmpty + st), (u - 1) & 1, err))
                 return;
             mbar_arrive_expect_tx(bar(c, kBarKFull + st), L::kTile);
             for (int h = 0; h < L::kHalves; ++h)
-                tma_load_2d(c.base + L::kOffK + st * L::kTile + h * kTileBytes, &c.a.tm_k, col_k + 64 * h, krow,
+                tma_load_2d(c.base + L::kOffK + st * L::kTile + h * L::kBox, &c.a.tm_k, col_k + 64 * h, krow,
                             bar(c, kBarKFull + st));
             if (u > 0 && !mbar_wait(bar(c, kBarVEmpty + st), (u - 1) & 1, err))
                 return;
             mbar_arrive_expect_tx(bar(c, kBarVFull + st), L::kTile);
             for (int h = 0; h < L::kHalves; ++h)
-                tma_load_2d(c.base + L::kOffV + st * L::kTile + h * kTileBytes, &c.a.tm_v, col_k + 64 * h, krow,
+                tma_load_2d(c.base + L::kOffV + st * L::kTile + h * L::kBox, &c.a.tm_v, col_k + 64 * h, krow,
                             bar(c, kBarVFull + st));
         }
     }
@@ -277,13 +286,13 @@ __device__ __forceinline__ void issue_s(const Ctx &c, int w, int qs, int st, int
 {
     using L = Layout<D, G>;
     constexpr uint32_t kIdesc = idesc(128, L::kKeys, false, kHalf);
-    const uint32_t q = c.base + (qs * G + w) * L::kTile;
+    const uint32_t q = c.base + (qs * G + w) * L::kQTile;
     const uint32_t k = c.base + L::kOffK + st * L::kTile + 128 * key0;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk / 4) * kTileBytes + 32 * (kk % 4);
-        mma_bf16_ss_warp(c.tmem + L::col_s(w, step), make_sdesc_sw128(q + off, 16, 1024),
-                         make_sdesc_sw128(k + off, 16, 1024), kIdesc, kk > 0);
+        const uint32_t q_off = (kk / 4) * kTileBytes + 32 * (kk % 4), k_off = (kk / 4) * L::kBox + 32 * (kk % 4);
+        mma_bf16_ss_warp(c.tmem + L::col_s(w, step), make_sdesc_sw128(q + q_off, 16, 1024),
+                         make_sdesc_sw128(k + k_off, 16, 1024), kIdesc, kk > 0);
     }
 }
 
@@ -300,7 +309,7 @@ __device__ __forceinline__ void issue_o(const Ctx &c, int w, int st, int key0, u
 #pragma unroll
     for (int kk = 0; kk < L::kKeys / 16; ++kk)
         mma_bf16_ts_warp(c.tmem + L::col_o(w), c.tmem + L::col_p(w, step) + 8 * kk,
-                         make_sdesc_sw128(v + 2048 * kk, kTileBytes, 1024), kIdesc,
+                         make_sdesc_sw128(v + 2048 * kk, L::kBox, 1024), kIdesc,
                          (accumulate || kk > 0) ? 1u : 0u);
 }
 
@@ -351,7 +360,7 @@ __device__ void so_issuer(const Ctx &c, int w, int lane)
                 const int st = g % L::kStages;
                 if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
                     return;
-                if (needs_mask(s, s.kb + t - 1)) {
+                if (needs_mask<L::kTileKeys>(s, s.kb + t - 1)) {
                     if (mine &&
                         !mbar_wait(bar(c, kBarVClean + masked % kMaskSlots), (masked / kMaskSlots) & 1, err))
                         return;
@@ -445,7 +454,7 @@ __device__ void o_issuer(const Ctx &c, int w, int lane)
             if (sub == 0) {
                 if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
                     return;
-                if (needs_mask(s, s.kb + j / L::kSteps)) {
+                if (needs_mask<L::kTileKeys>(s, s.kb + j / L::kSteps)) {
                     if (mine &&
                         !mbar_wait(bar(c, kBarVClean + masked % kMaskSlots), (masked / kMaskSlots) & 1, err))
                         return;
@@ -478,13 +487,14 @@ __device__ void o_issuer(const Ctx &c, int w, int lane)
 }
 
 // ---------------------------------------------------------------- masks
-// The visible keys of tile k as 4 words.
+// The visible keys of tile k as words.
+template <int kTileKeys>
 __device__ __forceinline__ uint32_t tile_word(const Ctx &c, const Rec &s, int k, int i)
 {
-    const int left = s.k_len - k * kBlockN - 32 * i;
+    const int left = s.k_len - k * kTileKeys - 32 * i;
     uint32_t w = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
     if (w && needs_bits(s))
-        w &= __ldg(c.a.key_bits + key_bit_word(s.k_row, s.seq) + 4 * k + i);
+        w &= __ldg(c.a.key_bits + key_bit_word(s.k_row, s.seq) + kTileKeys / 32 * k + i);
     return w;
 }
 
@@ -492,6 +502,7 @@ template <int D, int G>
 __device__ void mask_stager(const Ctx &c, int lane)
 {
     using L = Layout<D, G>;
+    constexpr int kWords = L::kTileKeys / 32;
     int *err = c.a.err;
     Rec s;
     uint32_t g = 0, masked = 0, with_bits = 0;
@@ -500,7 +511,7 @@ __device__ void mask_stager(const Ctx &c, int lane)
             const int st = g % L::kStages;
             // every tile is waited for and handed back, seen or not, so that
             // this warp neither runs ahead of the ring nor falls behind it
-            if (!needs_mask(s, k)) {
+            if (!needs_mask<L::kTileKeys>(s, k)) {
                 if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
                     return;
                 if (lane == 0)
@@ -510,13 +521,13 @@ __device__ void mask_stager(const Ctx &c, int lane)
             }
             const uint32_t clean = masked % kMaskSlots;
             ++masked;
-            const uint32_t mine = lane < 4 ? tile_word(c, s, k, lane) : 0u;
+            const uint32_t mine = lane < kWords ? tile_word<L::kTileKeys>(c, s, k, lane) : 0u;
             if (needs_bits(s)) {
                 const uint32_t slot = with_bits % kMaskSlots, u = with_bits / kMaskSlots;
                 ++with_bits;
                 if (u > 0 && !mbar_wait(bar(c, kBarBitsEmpty + slot), (u - 1) & 1, err))
                     return;
-                if (lane < 4)
+                if (lane < kWords)
                     reinterpret_cast<uint32_t *>(c.sbase + L::kOffWords)[4 * slot + lane] = mine;
                 __syncwarp();
                 if (lane == 0)
@@ -526,7 +537,7 @@ __device__ void mask_stager(const Ctx &c, int lane)
                 return;
             __syncwarp();
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kWords; ++i) {
                 const uint32_t word = __shfl_sync(0xffffffffu, mine, i);
                 if (word == 0xffffffffu)
                     continue;
@@ -536,7 +547,7 @@ __device__ void mask_stager(const Ctx &c, int lane)
                 for (int j = lane; j < 32 * 8 * L::kHalves; j += 32) {
                     const int row = j / 8 % 32, part = j % 8, half = j / 256;
                     if (!(word >> row & 1))
-                        *reinterpret_cast<uint4 *>(v + half * kTileBytes + row * 128 + part * 16) =
+                        *reinterpret_cast<uint4 *>(v + half * L::kBox + row * 128 + part * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                 }
             }
@@ -619,7 +630,7 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
         if (w == 1 && !second_tile(s)) {
             // nothing to do but hand the key bits on
             for (int k = s.kb; k < s.ke && needs_bits(s); ++k) {
-                if (!needs_mask(s, k))
+                if (!needs_mask<L::kTileKeys>(s, k))
                     continue;
                 const uint32_t slot = with_bits % kMaskSlots;
                 if (!mbar_wait(bar(c, kBarBitsFull + slot), (with_bits / kMaskSlots) & 1, err))
@@ -658,7 +669,7 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                 mbar_arrive(bar(c, kBarSEmpty + w));   // S may be overwritten now
 
             const int kt = s.kb + j / L::kSteps;
-            if (needs_mask(s, kt)) {
+            if (needs_mask<L::kTileKeys>(s, kt)) {
                 if (needs_bits(s)) {
                     if (sub == 0) {
                         const uint32_t slot = with_bits % kMaskSlots;
@@ -685,7 +696,7 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                                     sc[32 * q + i] = -INFINITY;
                     }
                 } else {
-                    const int kvalid = s.k_len - kt * kBlockN - sub * kKeys;
+                    const int kvalid = s.k_len - kt * L::kTileKeys - sub * kKeys;
                     if (kvalid < kKeys) {
 #pragma unroll
                         for (int i = 0; i < kKeys; ++i)
@@ -869,7 +880,8 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
     static_assert(sizeof(typename Split<D, G>::Deal) <= 4 * G * L::kOutRows * 128, "dealing");
     Split<D, G> split(a, a.heads >> a.fold_log2);
     // two tiles and a unit's fixed work per CTA at least
-    const bool work = split.find(*reinterpret_cast<typename Split<D, G>::Scratch *>(sbase + L::kOffScratch), gridDim.x, 22,
+    constexpr int kLeast = 2 * Split<D, G>::kFull + Split<D, G>::kAlpha;
+    const bool work = split.find(*reinterpret_cast<typename Split<D, G>::Scratch *>(sbase + L::kOffScratch), gridDim.x, kLeast,
                                  reinterpret_cast<typename Split<D, G>::Deal *>(sbase + L::kOffOut));
     if (work) {
         Ctx c{base, 0u, sbase, a, base + L::kOffBar};
@@ -964,6 +976,8 @@ cudaError_t launch_cross_blocks(const CrossArgs &a, int dim, bool half, int unit
         return half ? launch<64, 1, true>(a, ctas, stream) : launch<64, 1, false>(a, ctas, stream);
     if (dim == 64)
         return half ? launch<64, 2, true>(a, ctas, stream) : launch<64, 2, false>(a, ctas, stream);
+    if (unit_rows == kCrossSmallRows)
+        return half ? launch<128, 1, true>(a, ctas, stream) : launch<128, 1, false>(a, ctas, stream);
     return half ? launch<128, 2, true>(a, ctas, stream) : launch<128, 2, false>(a, ctas, stream);
 }
 

@@ -40,9 +40,10 @@ __device__ __forceinline__ long long div_cost(long long x, long long y)
 
 // kBlockQ: query rows of a unit (0: all of a sequence's), each the rows of
 // 2^fold_log2 heads, side by side; kTile: keys of a tile; kRounds 0: units are
-// never dealt out whole; kPerSm: CTAs of an SM.
+// never dealt out whole; kPerSm: CTAs of an SM;
+// kAlone: a CTA alone on its SM is faster by a part in kAlone.
 template <int kThreads, int kBlockQ_, int kTile_, int kFull_, int kHalf_, int kAlpha_, int kSnap_, int kRounds = 0,
-          int kJoin = 0, int kPerSm = 1>
+          int kJoin = 0, int kPerSm = 1, int kAlone = 1>
 struct CrossSplit {
     static constexpr int kBlockQ = kBlockQ_, kTile = kTile_, kSnap = kSnap_;
     static constexpr int kFull = kFull_, kHalf = kHalf_, kAlpha = kAlpha_;
@@ -225,7 +226,9 @@ struct CrossSplit {
             // 512 keys: 14.1 -> 10.8 us)
             if (kPerSm == 2 && all <= max_ctas / 2 && !a.records)
                 ctas = min(ctas, max_ctas / 2);
-            const long long limit = a.records ? div_cost(total, ctas) + kJoin : INT64_MAX;
+            const long long share = div_cost(total, ctas);
+            const long long limit = !a.records ? INT64_MAX :
+                                    share + (kPerSm == 2 && all <= max_ctas / 2 ? share / kAlone : 0) + kJoin;
             if (a.n_seqs <= kDealSeqs && all <= kRounds * max_ctas &&
                 static_cast<long long>(longest) * kFull + kAlpha <= limit && deal(sm, *work, max_ctas, all, limit)) {
                 dealt = &sm;

@@ -304,7 +304,8 @@ int cross_plan(const mbert_attn *h, const mbert_attn_cross_args *c, CrossPlan *p
         ++p->fold_log2;
     if (most << p->fold_log2 > INT32_MAX)
         return MBERT_ERR_BAD_ARG;   // (more than any device holds)
-    const bool small = c->head_dim == 64 && most << p->fold_log2 <= kCrossSmallRows;
+    const bool small = most << p->fold_log2 <= kCrossSmallRows &&
+                       (c->head_dim == 64 || c->rows_k <= kCrossSmallKeys * static_cast<int64_t>(c->n_seqs));
     p->unit_rows = p->token ? kCrossTokenRows : small ? kCrossSmallRows : kCrossBlockRows;
     p->ctas = h->num_sms * (p->token ? cross_token_ctas(c->head_dim) : cross_block_ctas(p->unit_rows));
     const int64_t longest = c->cu_k || c->n_seqs == 0 ? c->rows_k : c->rows_k / c->n_seqs;
@@ -387,7 +388,7 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
     DeviceGuard g(h->device);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     CrossArgs a;
-    const int kbox = p.token ? 64 : kBlockN;
+    const int kbox = p.token ? 64 : cross_tile_keys(D, p.unit_rows);
     // A head's part of a row is what a CTA reads of it: 128 bytes for D = 64.
     // Fetching 256 brought the next head's in too, for nobody on a long cache
     // (672 MB from DRAM for 488 MB of keys and values).

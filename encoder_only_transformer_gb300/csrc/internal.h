@@ -309,10 +309,16 @@ struct CrossRecord {
     int parts;          // 0: CTA c holds no first part
 };
 
-// Rows of a unit of attn_cross.cu: two query tiles, or one for head size 64 in
-// calls whose sequences have no more (both measured there).
+// Rows of a unit of attn_cross.cu: two query tiles, or one in calls whose
+// sequences have no more (both measured there).
 constexpr int kCrossBlockRows = 256;
 constexpr int kCrossSmallRows = 128;
+// For head size 128 only up to this many keys a sequence, in the mean: its CTAs
+// have half the bytes in flight (19 sequences of 32 x 8000 keys, 32 heads over 8:
+// 107 us against 99; of 1000 keys 30 against 36).
+constexpr int kCrossSmallKeys = 1536;
+// Keys of a tile of its K and V: 64 where two CTAs of head size 128 share an SM.
+constexpr int cross_tile_keys(int dim, int unit_rows) { return dim == 128 && unit_rows == kCrossSmallRows ? 64 : 128; }
 constexpr int kCrossTokenRows = 16;     // rows of a unit of attn_cross_token.cu
 
 // Units of at most this many keys are not cut between CTAs (blocks of queries,

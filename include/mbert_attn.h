@@ -344,7 +344,7 @@ int mbert_attn_qk_norm_rotary(mbert_attn *h, const mbert_attn_heads *q, const mb
  *                as they were.  NULL: n_seqs sequences of rows / n_seqs each (a padded batch).
  *   max_seqlen_q the caller's bound on the longest query sequence, 0 for none.  Up to
  *                16 / g a kernel for single tokens runs, which reads k and v once, up to 128 / f
- *                (head_dim 64; f the largest power of two that divides g) one for short blocks; a longer
+ *                (f the largest power of two that divides g) one for short blocks; a longer
  *                sequence found on the device sets MBERT_ERR_SEQ_TOO_LONG.
  *   key_mask     device int32 [rows_k], non-zero = visible, or NULL for all.
  * Scores, weights' sums and products in fp32; weights are rounded to dtype for the second
