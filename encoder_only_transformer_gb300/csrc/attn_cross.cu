@@ -75,14 +75,14 @@ constexpr int kMaskSlots = 4;
 // tiles 2200 (D = 64) and 2900 (D = 128), for one 1750 and 1850 (G = 1: beside
 // another CTA's 2150, and 1450 for 64 keys of D = 128); a unit's fixed
 // work (the end of the softmax, the output, the refill) 3500 and 4700.  Units
-// stay whole, up to four to a CTA, where that puts no more than 34 (6 us; 72, 9
+// stay whole, up to four to a CTA, where that puts no more than 30 (6 us; 72, 9
 // us, for G = 1 of D = 128, where joining the parts of 304 CTAs takes longer: 24
 // sequences of 32 over 1000, 43 above the share, 30 us, 36 cut) on top of a CTA's
 // share.
 template <int D, int G>
 using Split = CrossSplit<G == 1 ? 256 : D == 64 ? 384 : 512, kBlockM * G, cross_tile_keys(D, kBlockM * G), 6,
                          G == 1 ? 6 : D == 64 ? 5 : 4, D == 128 && G == 1 ? 20 : 10,
-                         kCrossBlockWholeKeys / cross_tile_keys(D, kBlockM * G), 4, D == 128 && G == 1 ? 72 : 34,
+                         kCrossBlockWholeKeys / cross_tile_keys(D, kBlockM * G), 4, D == 128 && G == 1 ? 72 : 30,
                          cross_block_ctas(kBlockM * G), D == 64 ? 5 : 2>;
 
 // G: query tiles of a unit, a softmax group for each.
@@ -869,11 +869,15 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
     uint32_t *slot = reinterpret_cast<uint32_t *>(sbase + L::kOffBar + kSlotInBars);
     const int cta = blockIdx.x;
 
-    // TMEM first: the next CTA of this SM only starts once this one has given
-    // up its right to allocate
-    if (threadIdx.x < 32) {
-        tmem_alloc(smem_u32(slot), L::kTmemCols);
-        tmem_relinquish();
+    // TMEM first, as the next CTA of this SM only starts once this one has given
+    // up its right to allocate.  (The 12 warps of D = 64, alone on their SM, take
+    // it after the search: 193 us against 197 for 8192 x 8192; the 16 of D = 128
+    // lose 1 % so.)
+    if constexpr (!L::kPair) {
+        if (threadIdx.x < 32) {
+            tmem_alloc(smem_u32(slot), L::kTmemCols);
+            tmem_relinquish();
+        }
     }
     if (threadIdx.x == 0 && a.records)
         a.records[cta].parts = 0;
@@ -921,6 +925,12 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
             }
             fence_mbar_init();
         }
+        if constexpr (L::kPair) {
+            if (warp == 0) {
+                tmem_alloc(smem_u32(slot), L::kTmemCols);
+                tmem_relinquish();
+            }
+        }
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
@@ -948,12 +958,22 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
             softmax_group<D, G, kHalf>(c, warp >> 2, warp & 3, lane, cta);
             __syncwarp();
         }
+        if constexpr (L::kPair) {
+            tc_fence_before();
+            __syncthreads();
+            if (warp == 0) {
+                tc_fence_after();
+                tmem_dealloc(c.tmem, L::kTmemCols);
+            }
+        }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        tc_fence_after();
-        tmem_dealloc(*slot, L::kTmemCols);
+    if constexpr (!L::kPair) {
+        tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            tc_fence_after();
+            tmem_dealloc(*slot, L::kTmemCols);
+        }
     }
     pdl_trigger();
 }

@@ -21,22 +21,15 @@
 // cutting and joining costs, they stay so.  12 sequences of 250 queries over
 // 1000 keys, 12 heads of 64: 20.3 us, 24.6 cut; 24 over 600 to 1000: 31.9,
 // 35.7 cut; 32 heads over 8 of 128, 9 sequences: 41, 50 cut.  With the longest
-// unit 34 above the share (16 sequences of 118 to 1946 keys) both took 32.5.
+// unit 34 above the share (16 sequences of 118 to 1946 keys) both took 32.5 to
+// 33.  Divisions stay the compiler's 64-bit ones: 32-bit ones where the costs
+// allow, a branch at each, made 8192 x 8192 1 % slower.
 #pragma once
 
 #include "common.cuh"
 #include "internal.h"
 
 namespace mbert {
-
-// Quotient of numbers >= 0: most calls' costs fit 32 bits, whose division takes
-// a fifth of the instructions.
-__device__ __forceinline__ long long div_cost(long long x, long long y)
-{
-    if ((x | y) >> 32)
-        return x / y;
-    return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-}
 
 // kBlockQ: query rows of a unit (0: all of a sequence's), each the rows of
 // 2^fold_log2 heads, side by side; kTile: keys of a tile; kRounds 0: units are
@@ -55,7 +48,7 @@ struct CrossSplit {
         long long warp[kWarps];
         long long base[2];
         int seq[2];
-        int units[kWarps], most[kWarps];
+        int units[kWarps], most[kWarps], least[kWarps];
         int deal_seq[kRounds + 1], deal_unit[kRounds + 1];      // this CTA's whole units
     };
     // What dealing takes besides, while find() runs.
@@ -90,9 +83,9 @@ struct CrossSplit {
     {
         const long long ch = q.head(), cb = q.block();
         Place p;
-        p.head = static_cast<int>(div_cost(x - base, ch));
+        p.head = static_cast<int>((x - base) / ch);
         const long long h0 = base + p.head * ch;
-        const long long b = div_cost(x - h0, cb);
+        const long long b = (x - h0) / cb;
         p.b = b < q.whole ? static_cast<int>(b) : q.whole;
         p.per = p.b < q.whole ? kFull : kHalf;
         p.xa = h0 + p.b * cb;
@@ -152,13 +145,13 @@ struct CrossSplit {
 
     __device__ __forceinline__ long long border(int c) const
     {
-        return div_cost(c * total, ctas);
+        return c * total / ctas;
     }
 
     // The CTA whose range holds x (borders inside long units do not move).
     __device__ __forceinline__ int cta_of(long long x) const
     {
-        return static_cast<int>(div_cost((x + 1) * ctas - 1, total));
+        return static_cast<int>(((x + 1) * ctas - 1) / total);
     }
 
     // Every thread of the block.  min_cost: of a CTA, at least kFull, so that
@@ -169,7 +162,7 @@ struct CrossSplit {
     {
         const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
         long long sum = 0;
-        int bad = 0, units = 0, most = 0;       // most: tiles of a unit
+        int bad = 0, units = 0, most = 0, least = INT32_MAX;    // most, least: cost of a unit
         for (int s = tid; s < a.n_seqs; s += kThreads) {
             const Seq q = load(s);
             if (q.q_len < 0 || q.k_all < 0 || q.q_row < 0 || q.k_row < 0 ||
@@ -182,7 +175,11 @@ struct CrossSplit {
                 sum += cost(q);
                 // (only compared with few)
                 units = static_cast<int>(min(1ll << 20, units + static_cast<long long>(unit_heads) * (q.whole + q.half)));
-                most = max(most, q.whole ? q.tiles : 0);
+                if (q.whole + q.half > 0) {
+                    const int unit = q.tiles * (q.whole ? kFull : kHalf) + kAlpha;
+                    most = max(most, unit);
+                    least = min(least, unit);
+                }
             }
         }
         if (tid == 0 && ((a.cu_q && a.cu_q[0] != 0) || (a.cu_k && a.cu_k[0] != 0)))
@@ -193,11 +190,13 @@ struct CrossSplit {
         if constexpr (kRounds > 0) {
             units = __reduce_add_sync(0xffffffffu, units);
             most = __reduce_max_sync(0xffffffffu, most);
+            least = __reduce_min_sync(0xffffffffu, least);
         }
         if (lane == 0) {
             sm.warp[warp] = sum;
             sm.units[warp] = units;
             sm.most[warp] = most;
+            sm.least[warp] = least;
         }
         if (tid < 2)
             sm.seq[tid] = -1;
@@ -213,24 +212,28 @@ struct CrossSplit {
             total += sm.warp[w];
         if (total == 0)
             return false;
-        const long long want = div_cost(total, min_cost);
+        const long long want = total / min_cost;
         ctas = want < 1 ? 1 : want < max_ctas ? static_cast<int>(want) : max_ctas;
         if constexpr (kRounds > 0) {
-            int all = 0, longest = 0;
+            int all = 0, longest = 0, shortest = INT32_MAX;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 all += sm.units[w];
                 longest = max(longest, sm.most[w]);
+                shortest = min(shortest, sm.least[w]);
             }
             // an SM gets its second unit when every one has a first (152 units over
             // 512 keys: 14.1 -> 10.8 us)
             if (kPerSm == 2 && all <= max_ctas / 2 && !a.records)
                 ctas = min(ctas, max_ctas / 2);
-            const long long share = div_cost(total, ctas);
+            const long long share = total / ctas;
             const long long limit = !a.records ? INT64_MAX :
                                     share + (kPerSm == 2 && all <= max_ctas / 2 ? share / kAlone : 0) + kJoin;
-            if (a.n_seqs <= kDealSeqs && all <= kRounds * max_ctas &&
-                static_cast<long long>(longest) * kFull + kAlpha <= limit && deal(sm, *work, max_ctas, all, limit)) {
+            // (not worth dealing where one unit, or the shortest in every round, is
+            // above the limit)
+            const int rounds = (all + max_ctas - 1) / max_ctas;
+            if (a.n_seqs <= kDealSeqs && rounds <= kRounds && longest <= limit &&
+                static_cast<long long>(rounds) * shortest <= limit && deal(sm, *work, max_ctas, all, limit)) {
                 dealt = &sm;
                 return sm.deal_seq[0] >= 0;
             }
@@ -422,8 +425,8 @@ struct CrossSplit {
                 continue;
             }
             const Place p = place(it.s, it.base, it.x);
-            const int kb = static_cast<int>(div_cost(it.x - p.xa + p.per - 1, p.per));
-            const long long cut = div_cost(hi - p.xa + p.per - 1, p.per);
+            const int kb = static_cast<int>((it.x - p.xa + p.per - 1) / p.per);
+            const long long cut = (hi - p.xa + p.per - 1) / p.per;
             g.ke = cut < it.s.tiles ? static_cast<int>(cut) : it.s.tiles;
             it.x = p.end;
             if (kb >= g.ke)
