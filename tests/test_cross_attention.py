@@ -591,3 +591,49 @@ def test_limits(built):
     with pytest.raises(binding.MbertAttnError):
         binding.cross_attention(q, k, v, max_seqlen_q=bound, **cu)
     assert binding._default(q.device).get_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "f16")])
+@pytest.mark.parametrize("Sq", [60, 250])
+def test_captured_from_whole_to_cut_units(built, Sq, D, dtype):
+    """A captured padded call replayed with masks that leave its units whole,
+    cut, or without keys; two graphs at once on two streams, beside a global
+    layer of the encoder."""
+    from encoder_only_transformer_gb300 import workloads as W
+    B, Sk, H = 6, 1500, 3
+    g = torch.Generator().manual_seed(Sq + D)
+    q = torch.randn(B, Sq, H, D, generator=g).to(TYPES[dtype])
+    kv = torch.randn(B, Sk, 2 * H, D, generator=g).to(TYPES[dtype])
+    lens = ([700] * B, [1500, 3, 0, 90, 640, 1], [0] * B, [1100] * B)
+    dq, dkv = q.cuda(), kv.cuda()
+    masks = [torch.zeros(B, Sk, dtype=torch.int32, device="cuda") for _ in range(2)]
+    outs, graphs = [], []
+    binding.cross_attention_padded(dq, dkv[:, :, :H], dkv[:, :, H:], key_mask=masks[0])
+    for m in masks:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(binding.cross_attention_padded(dq, dkv[:, :, :H], dkv[:, :, H:], key_mask=m))
+        graphs.append(graph)
+    wl = W.custom([400, 9, 700], seed=3)
+    qkv, cu = wl.qkv.cuda(), wl.cu_seqlens.cuda()
+    layer = binding.attention(qkv, cu, "global")
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for i in range(len(lens)):
+        pair = (lens[i], lens[i - 1])
+        for m, kl in zip(masks, pair):
+            m.copy_((torch.arange(Sk)[None, :] < torch.tensor(kl)[:, None]).int())
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for s, graph in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    graph.replay()
+            with torch.cuda.stream(streams[2]):
+                beside = binding.attention(qkv, cu, "global")
+        torch.cuda.synchronize()
+        assert torch.equal(beside, layer)
+        for out, kl in zip(outs, pair):
+            for b in range(B):
+                n = kl[b]
+                check(out[b], *reference(q[b], kv[b, :n, :H], kv[b, :n, H:], [Sq], [n]))
+    assert binding._default(qkv.device).get_error() == 0
