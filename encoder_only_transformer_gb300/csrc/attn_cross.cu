@@ -148,9 +148,11 @@ constexpr int kBarRecFull = 38;   // + record slot (4)
 constexpr int kBarRecEmpty = 42;  // + record slot
 constexpr int kBarPOdd = 46;      // + group: kBarPFull of the odd steps (D = 128)
 constexpr int kBarOOdd = 48;      // + group: kBarODone of the odd steps (D = 128)
-constexpr int kNumBars = 50;
+constexpr int kBarDrain = 50;     // + issuer (4): all of its products are done
+constexpr int kNumBars = 54;
 constexpr uint32_t kSlotInBars = 8 * kNumBars;                 // TMEM address
-static_assert(kSlotInBars + 4 <= 512, "barriers");
+constexpr uint32_t kGaveUpInBars = kSlotInBars + 4;            // a wait has given up
+static_assert(kGaveUpInBars + 4 <= 512, "barriers");
 
 constexpr float kRescaleThreshold = 8.0f;
 
@@ -184,12 +186,21 @@ struct Ctx {
 
 __device__ __forceinline__ uint32_t bar(const Ctx &c, int i) { return c.bars + 8u * i; }
 
+// Waits for a phase of barrier i.  A role of whole warps goes on where it gives
+// up, and asks (stop) where that matters.
+__device__ __forceinline__ bool wait(const Ctx &c, int i, uint32_t parity)
+{
+    return mbar_wait_mark(bar(c, i), parity, c.a.err, c.bars + kGaveUpInBars);
+}
+__device__ __forceinline__ bool stop(const Ctx &c) { return any_gave_up(c.bars + kGaveUpInBars); }
+
 // The CTA's segment sg (all lanes of a reading warp).  False: there is none.
 template <int D, int G>
 __device__ __forceinline__ bool read_rec(const Ctx &c, uint32_t sg, int lane, Rec &r)
 {
     const int slot = sg % kRecs;
-    if (!mbar_wait(bar(c, kBarRecFull + slot), (sg / kRecs) & 1, c.a.err))
+    wait(c, kBarRecFull + slot, (sg / kRecs) & 1);
+    if (stop(c))
         return false;
     r = reinterpret_cast<const Rec *>(c.sbase + Layout<D, G>::kOffRecs)[slot];
     __syncwarp();
@@ -216,14 +227,17 @@ __device__ __forceinline__ int seg_steps(const Rec &s)
 }
 
 // ---------------------------------------------------------------- producer
+// What the producer has issued so far.
+struct Issued {
+    uint32_t q = 0, k = 0, v = 0;   // segments' queries, key tiles of K and of V
+};
+
 template <int D, int G>
-__device__ void producer(const Ctx &c, const Split<D, G> &split)
+__device__ void produce(const Ctx &c, const Split<D, G> &split, Issued &n)
 {
     using L = Layout<D, G>;
-    int *err = c.a.err;
     auto it = split.begin();
     typename Split<D, G>::Seg seg;
-    uint32_t g = 0;          // key tiles issued by this CTA so far
     for (uint32_t sg = 0;; ++sg) {
         Rec s{};
         if (split.next(it, seg)) {
@@ -241,7 +255,7 @@ __device__ void producer(const Ctx &c, const Split<D, G> &split)
             s.parts = seg.kb == 0 && seg.ke < seg.s.tiles ? split.parts(seg) : 0;
         }
         const int slot = sg % kRecs;
-        if (sg >= kRecs && !mbar_wait(bar(c, kBarRecEmpty + slot), (sg / kRecs - 1) & 1, err))
+        if (sg >= kRecs && !wait(c, kBarRecEmpty + slot, (sg / kRecs - 1) & 1))
             return;
         reinterpret_cast<Rec *>(c.sbase + L::kOffRecs)[slot] = s;
         mbar_arrive(bar(c, kBarRecFull + slot));
@@ -249,34 +263,49 @@ __device__ void producer(const Ctx &c, const Split<D, G> &split)
             return;
         const int qs = sg % L::kQSets;
         const bool two = G == 2 && second_tile(s);
-        if (sg >= L::kQSets && !mbar_wait(bar(c, kBarQEmpty + qs), (sg / L::kQSets - 1) & 1, err))
+        if (sg >= L::kQSets && !wait(c, kBarQEmpty + qs, (sg / L::kQSets - 1) & 1))
             return;
         const int col_k = s.head / c.a.group * D;
         const int fold = c.a.fold_log2, qrow = s.q_row + (s.q0 >> fold);
         const uint32_t qdst = c.base + qs * G * L::kQTile;
         mbar_arrive_expect_tx(bar(c, kBarQFull + qs), (two ? 2 : 1) * L::kQTile);
+        ++n.q;
         for (int w = 0; w < (two ? 2 : 1); ++w)
             for (int h = 0; h < L::kHalves; ++h)
                 tma_load_3d(qdst + w * L::kQTile + h * kTileBytes, &c.a.tm_q, 64 * h, s.head,
                             qrow + w * (kBlockM >> fold), bar(c, kBarQFull + qs));
-        for (int k = s.kb; k < s.ke; ++k, ++g) {
-            const int st = g % L::kStages;
-            const uint32_t u = g / L::kStages;
+        for (int k = s.kb; k < s.ke; ++k) {
+            const int st = n.k % L::kStages;
+            const uint32_t u = n.k / L::kStages;
             const int krow = s.k_row + k * L::kTileKeys;
-            if (u > 0 && !mbar_wait(bar(c, kBarKEmpty + st), (u - 1) & 1, err))
+            if (u > 0 && !wait(c, kBarKEmpty + st, (u - 1) & 1))
                 return;
             mbar_arrive_expect_tx(bar(c, kBarKFull + st), L::kTile);
             for (int h = 0; h < L::kHalves; ++h)
                 tma_load_2d(c.base + L::kOffK + st * L::kTile + h * L::kBox, &c.a.tm_k, col_k + 64 * h, krow,
                             bar(c, kBarKFull + st));
-            if (u > 0 && !mbar_wait(bar(c, kBarVEmpty + st), (u - 1) & 1, err))
+            ++n.k;
+            if (u > 0 && !wait(c, kBarVEmpty + st, (u - 1) & 1))
                 return;
             mbar_arrive_expect_tx(bar(c, kBarVFull + st), L::kTile);
             for (int h = 0; h < L::kHalves; ++h)
                 tma_load_2d(c.base + L::kOffV + st * L::kTile + h * L::kBox, &c.a.tm_v, col_k + 64 * h, krow,
                             bar(c, kBarVFull + st));
+            ++n.v;
         }
     }
+}
+
+// Every copy has landed before the CTA can exit, wherever the producer stopped.
+template <int D, int G>
+__device__ void producer(const Ctx &c, const Split<D, G> &split)
+{
+    using L = Layout<D, G>;
+    Issued n;
+    produce<D, G>(c, split, n);
+    ring_drain(bar(c, kBarQFull), n.q, L::kQSets);
+    ring_drain(bar(c, kBarKFull), n.k, L::kStages);
+    ring_drain(bar(c, kBarVFull), n.v, L::kStages);
 }
 
 // ---------------------------------------------------------------- MMA issuers
@@ -323,24 +352,21 @@ __device__ void so_issuer(const Ctx &c, int w, int lane)
 {
     constexpr int D = 64;
     using L = Layout<D, G>;
-    int *err = c.a.err;
     Rec s;
     uint32_t g0 = 0, gw0 = 0, sw = 0, masked = 0;
     for (uint32_t sg = 0; read_rec<D, G>(c, sg, lane, s); ++sg) {
         const int qs = sg % L::kQSets;
         const int n = s.ke - s.kb;
         const bool mine = w == 0 || second_tile(s);
-        if (!mbar_wait(bar(c, kBarQFull + qs), (sg / L::kQSets) & 1, err))
-            return;
+        wait(c, kBarQFull + qs, (sg / L::kQSets) & 1);
         for (int t = 0; t <= n; ++t) {
             if (t < n) {
                 const uint32_t g = g0 + t, gw = gw0 + t;
                 const int st = g % L::kStages;
-                if (!mbar_wait(bar(c, kBarKFull + st), (g / L::kStages) & 1, err))
-                    return;
+                wait(c, kBarKFull + st, (g / L::kStages) & 1);
                 if (mine) {
-                    if (gw > 0 && !mbar_wait(bar(c, kBarSEmpty + w), (gw - 1) & 1, err))
-                        return;
+                    if (gw > 0)
+                        wait(c, kBarSEmpty + w, (gw - 1) & 1);
                     __syncwarp();
                     tc_fence_after();
                     issue_s<D, G, kHalf>(c, w, qs, st, 0, gw);
@@ -358,19 +384,16 @@ __device__ void so_issuer(const Ctx &c, int w, int lane)
             if (t > 0) {
                 const uint32_t g = g0 + t - 1, gw = gw0 + t - 1;
                 const int st = g % L::kStages;
-                if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
-                    return;
+                wait(c, kBarVFull + st, (g / L::kStages) & 1);
                 if (needs_mask<L::kTileKeys>(s, s.kb + t - 1)) {
-                    if (mine &&
-                        !mbar_wait(bar(c, kBarVClean + masked % kMaskSlots), (masked / kMaskSlots) & 1, err))
-                        return;
+                    if (mine)
+                        wait(c, kBarVClean + masked % kMaskSlots, (masked / kMaskSlots) & 1);
                     ++masked;
                 }
                 if (mine) {
-                    if (!mbar_wait(bar(c, kBarPFull + w), gw & 1, err))
-                        return;
-                    if (t == 1 && sw > 0 && !mbar_wait(bar(c, kBarOFree + w), (sw - 1) & 1, err))
-                        return;
+                    wait(c, kBarPFull + w, gw & 1);
+                    if (t == 1 && sw > 0)
+                        wait(c, kBarOFree + w, (sw - 1) & 1);
                     __syncwarp();
                     tc_fence_after();
                     issue_o<D, G, kHalf>(c, w, st, 0, gw, t > 1);
@@ -395,20 +418,18 @@ template <int D, int G, bool kHalf>
 __device__ void s_issuer(const Ctx &c, int w, int lane)
 {
     using L = Layout<D, G>;
-    int *err = c.a.err;
     Rec s;
     uint32_t g = 0, gw = 0;
     for (uint32_t sg = 0; read_rec<D, G>(c, sg, lane, s); ++sg) {
         const int qs = sg % L::kQSets;
         const int n = seg_steps<D, G>(s);
         const bool mine = w == 0 || second_tile(s);
-        if (!mbar_wait(bar(c, kBarQFull + qs), (sg / L::kQSets) & 1, err))
-            return;
+        wait(c, kBarQFull + qs, (sg / L::kQSets) & 1);
         for (int j = 0; j < n; ++j) {
             const int st = g % L::kStages, sub = j % L::kSteps;
             const bool last_sub = sub == L::kSteps - 1 || j == n - 1;
-            if (sub == 0 && !mbar_wait(bar(c, kBarKFull + st), (g / L::kStages) & 1, err))
-                return;
+            if (sub == 0)
+                wait(c, kBarKFull + st, (g / L::kStages) & 1);
             g += last_sub;
             if (!mine) {
                 if (lane == 0 && last_sub)
@@ -417,8 +438,8 @@ __device__ void s_issuer(const Ctx &c, int w, int lane)
                 continue;
             }
             // this buffer's last P has been multiplied
-            if (gw > 1 && !mbar_wait(bar(c, (gw & 1 ? kBarOOdd : kBarODone) + w), ((gw >> 1) - 1) & 1, err))
-                return;
+            if (gw > 1)
+                wait(c, (gw & 1 ? kBarOOdd : kBarODone) + w, ((gw >> 1) - 1) & 1);
             __syncwarp();
             tc_fence_after();
             issue_s<D, G, kHalf>(c, w, qs, st, sub * L::kKeys, gw);
@@ -442,7 +463,6 @@ template <int D, int G, bool kHalf>
 __device__ void o_issuer(const Ctx &c, int w, int lane)
 {
     using L = Layout<D, G>;
-    int *err = c.a.err;
     Rec s;
     uint32_t g = 0, gw = 0, sw = 0, masked = 0;
     for (uint32_t sg = 0; read_rec<D, G>(c, sg, lane, s); ++sg) {
@@ -452,12 +472,10 @@ __device__ void o_issuer(const Ctx &c, int w, int lane)
             const int st = g % L::kStages, sub = j % L::kSteps;
             const bool last_sub = sub == L::kSteps - 1 || j == n - 1;
             if (sub == 0) {
-                if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
-                    return;
+                wait(c, kBarVFull + st, (g / L::kStages) & 1);
                 if (needs_mask<L::kTileKeys>(s, s.kb + j / L::kSteps)) {
-                    if (mine &&
-                        !mbar_wait(bar(c, kBarVClean + masked % kMaskSlots), (masked / kMaskSlots) & 1, err))
-                        return;
+                    if (mine)
+                        wait(c, kBarVClean + masked % kMaskSlots, (masked / kMaskSlots) & 1);
                     ++masked;
                 }
             }
@@ -470,10 +488,9 @@ __device__ void o_issuer(const Ctx &c, int w, int lane)
             }
             // one barrier per P buffer: the softmax may finish two steps, whose S
             // are both there, before this wait
-            if (!mbar_wait(bar(c, (gw & 1 ? kBarPOdd : kBarPFull) + w), gw >> 1 & 1, err))
-                return;
-            if (j == 0 && sw > 0 && !mbar_wait(bar(c, kBarOFree + w), (sw - 1) & 1, err))
-                return;
+            wait(c, (gw & 1 ? kBarPOdd : kBarPFull) + w, gw >> 1 & 1);
+            if (j == 0 && sw > 0)
+                wait(c, kBarOFree + w, (sw - 1) & 1);
             __syncwarp();
             tc_fence_after();
             issue_o<D, G, kHalf>(c, w, st, sub * L::kKeys, gw, j > 0);
@@ -503,7 +520,6 @@ __device__ void mask_stager(const Ctx &c, int lane)
 {
     using L = Layout<D, G>;
     constexpr int kWords = L::kTileKeys / 32;
-    int *err = c.a.err;
     Rec s;
     uint32_t g = 0, masked = 0, with_bits = 0;
     for (uint32_t sg = 0; read_rec<D, G>(c, sg, lane, s); ++sg) {
@@ -512,8 +528,7 @@ __device__ void mask_stager(const Ctx &c, int lane)
             // every tile is waited for and handed back, seen or not, so that
             // this warp neither runs ahead of the ring nor falls behind it
             if (!needs_mask<L::kTileKeys>(s, k)) {
-                if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
-                    return;
+                wait(c, kBarVFull + st, (g / L::kStages) & 1);
                 if (lane == 0)
                     mbar_arrive(bar(c, kBarVEmpty + st));
                 __syncwarp();
@@ -525,16 +540,15 @@ __device__ void mask_stager(const Ctx &c, int lane)
             if (needs_bits(s)) {
                 const uint32_t slot = with_bits % kMaskSlots, u = with_bits / kMaskSlots;
                 ++with_bits;
-                if (u > 0 && !mbar_wait(bar(c, kBarBitsEmpty + slot), (u - 1) & 1, err))
-                    return;
+                if (u > 0)
+                    wait(c, kBarBitsEmpty + slot, (u - 1) & 1);
                 if (lane < kWords)
                     reinterpret_cast<uint32_t *>(c.sbase + L::kOffWords)[4 * slot + lane] = mine;
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(c, kBarBitsFull + slot));
             }
-            if (!mbar_wait(bar(c, kBarVFull + st), (g / L::kStages) & 1, err))
-                return;
+            wait(c, kBarVFull + st, (g / L::kStages) & 1);
             __syncwarp();
 #pragma unroll 1
             for (int i = 0; i < kWords; ++i) {
@@ -612,16 +626,18 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
     using L = Layout<D, G>;
     constexpr int kKeys = L::kKeys;
     constexpr float kLift = kHalf ? 7.f : 0.f;        // weights times 2^7 in fp16
-    int *err = c.a.err;
     const uint32_t lane_off = static_cast<uint32_t>(32 * warp_in_group) << 16;
     const uint32_t tO = c.tmem + L::col_o(w) + lane_off;
     const int rr = kBlockM * w + 32 * warp_in_group + lane;      // row within the unit
     const float scale = c.a.scale_log2;
     // step's P V has completed.  (D = 128: S of a step stands for the P V two
     // steps before, that is for the last phase of the same barrier.)
-    auto wait_o = [&](uint32_t step) -> bool {
-        return D == 64 ? mbar_wait(bar(c, kBarODone + w), step & 1, err)
-                       : mbar_wait(bar(c, step & 1 ? kBarOOdd + w : kBarODone + w), step >> 1 & 1, err);
+    auto wait_o = [&](uint32_t step) {
+        if constexpr (D == 64)
+            wait(c, kBarODone + w, step & 1);
+        else
+            wait(c, step & 1 ? kBarOOdd + w : kBarODone + w, step >> 1 & 1);
+        __syncwarp();
     };
     Rec s;
     uint32_t gw = 0, with_bits = 0;
@@ -633,8 +649,7 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                 if (!needs_mask<L::kTileKeys>(s, k))
                     continue;
                 const uint32_t slot = with_bits % kMaskSlots;
-                if (!mbar_wait(bar(c, kBarBitsFull + slot), (with_bits / kMaskSlots) & 1, err))
-                    return;
+                wait(c, kBarBitsFull + slot, (with_bits / kMaskSlots) & 1);
                 mbar_arrive(bar(c, kBarBitsEmpty + slot));
                 ++with_bits;
             }
@@ -645,9 +660,10 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
         uint32_t bits[4] = {0u, 0u, 0u, 0u};   // the tile's key bits
         for (int j = 0; j < n; ++j, ++gw) {
             const int sub = j % L::kSteps;
-            if (!(D == 64 ? mbar_wait(bar(c, kBarSFull + w), gw & 1, err)
-                          : mbar_wait(bar(c, gw & 1 ? kBarSOdd + w : kBarSFull + w), gw >> 1 & 1, err)))
-                return;
+            if constexpr (D == 64)
+                wait(c, kBarSFull + w, gw & 1);
+            else
+                wait(c, gw & 1 ? kBarSOdd + w : kBarSFull + w, gw >> 1 & 1);
             __syncwarp();
             tc_fence_after();
             float sc[kKeys];
@@ -673,8 +689,7 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                 if (needs_bits(s)) {
                     if (sub == 0) {
                         const uint32_t slot = with_bits % kMaskSlots;
-                        if (!mbar_wait(bar(c, kBarBitsFull + slot), (with_bits / kMaskSlots) & 1, err))
-                            return;
+                        wait(c, kBarBitsFull + slot, (with_bits / kMaskSlots) & 1);
                         ++with_bits;
                         const uint4 b = reinterpret_cast<const uint4 *>(c.sbase + L::kOffWords)[slot];
                         bits[0] = b.x, bits[1] = b.y, bits[2] = b.z, bits[3] = b.w;
@@ -743,9 +758,7 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
                 // (D = 64: which also frees P)
                 const bool any = __any_sync(0xffffffffu, need);
                 if (D == 64 || any) {
-                    if (!wait_o(gw - 1))
-                        return;
-                    __syncwarp();
+                    wait_o(gw - 1);
                     tc_fence_after();
                 }
                 if (any) {
@@ -775,9 +788,9 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
 
         // ---- end of the segment: O / l to the output, or the state to this
         // CTA's part slot
-        if (!wait_o(gw - 1))
+        wait_o(gw - 1);
+        if (stop(c))
             return;
-        __syncwarp();
         tc_fence_after();
         const bool whole = s.ke - s.kb == s.tiles;
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -856,6 +869,14 @@ __device__ void softmax_group(const Ctx &c, int w, int warp_in_group, int lane, 
     }
 }
 
+// The products that an issuer has issued are done before the CTA can exit and
+// give its TMEM back.
+__device__ __forceinline__ void drain_products(const Ctx &c, int issuer)
+{
+    mma_commit_warp(bar(c, kBarDrain + issuer));
+    drain_wait(bar(c, kBarDrain + issuer), 0);
+}
+
 template <int D, int G, bool kHalf>
 __global__ void __launch_bounds__(Layout<D, G>::kThreads, Layout<D, G>::kCtas)
 attn_cross_kernel(const __grid_constant__ CrossArgs a)
@@ -923,6 +944,9 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
                 mbar_init(bar(c, kBarBitsEmpty + i), L::kUnitRows);
                 mbar_init(bar(c, kBarVClean + i), 1);
             }
+            for (int i = 0; i < 4; ++i)
+                mbar_init(bar(c, kBarDrain + i), 1);
+            sts32(c.bars + kGaveUpInBars, 0u);
             fence_mbar_init();
         }
         if constexpr (L::kPair) {
@@ -948,9 +972,12 @@ attn_cross_kernel(const __grid_constant__ CrossArgs a)
                     s_issuer<D, G, kHalf>(c, warp - L::kControl - 2, lane);
                 else
                     so_issuer<G, kHalf>(c, warp - L::kControl - 2, lane);
+                drain_products(c, warp - L::kControl - 2);
             } else if (warp < L::kControl + 2 + 2 * G) {
-                if constexpr (L::kSplitIssuers)
+                if constexpr (L::kSplitIssuers) {
                     o_issuer<D, G, kHalf>(c, warp - L::kControl - 2 - G, lane);
+                    drain_products(c, warp - L::kControl - 2);
+                }
             }
             __syncwarp();
         } else {

@@ -71,6 +71,8 @@ constexpr int kBarStates = 6;     // the four states are in shared memory
 constexpr int kBarJoined = 7;     // they have been read
 constexpr int kBarRecFull = 8;    // + record slot: a segment and its query rows
 constexpr int kBarRecEmpty = 10;  // + record slot: read by the four warps
+constexpr int kNumBars = 12;
+constexpr uint32_t kGaveUpInBars = 8 * kNumBars;    // a wait has given up
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4])
 {
@@ -128,6 +130,14 @@ struct Ctx {
 
 __device__ __forceinline__ uint32_t bar(const Ctx &c, int i) { return c.bars + 8u * i; }
 
+// Waits for a phase of barrier i.  The warps that compute go on where it gives
+// up, and ask (stop) where that matters.
+__device__ __forceinline__ bool wait(const Ctx &c, int i, uint32_t parity)
+{
+    return mbar_wait_mark(bar(c, i), parity, c.a.err, c.bars + kGaveUpInBars);
+}
+__device__ __forceinline__ bool stop(const Ctx &c) { return any_gave_up(c.bars + kGaveUpInBars); }
+
 // 16-byte aligned bulk copy of `bytes` (a multiple of 16) into shared memory.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar)
 {
@@ -135,14 +145,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(mbar) : "memory");
 }
 
+// What the producer has issued so far.
+struct Issued {
+    uint32_t recs = 0, kv = 0;  // records (with their queries, but for the last), key tiles
+};
+
 template <int D>
-__device__ void producer(const Ctx &c, const Split &split)
+__device__ void produce(const Ctx &c, const Split &split, Issued &n)
 {
     using L = Layout<D>;
     const CrossArgs &a = c.a;
     auto it = split.begin();
     Split::Seg seg;
-    uint32_t g = 0;
     for (uint32_t sg = 0;; ++sg) {
         Rec r{};
         const bool more = split.next(it, seg);
@@ -160,9 +174,10 @@ __device__ void producer(const Ctx &c, const Split &split)
             r.parts = seg.kb == 0 && seg.ke < seg.s.tiles ? split.parts(seg) : 0;
         }
         const int slot = sg % kRecs;
-        if (sg >= kRecs && !mbar_wait(bar(c, kBarRecEmpty + slot), (sg / kRecs - 1) & 1, a.err))
+        if (sg >= kRecs && !wait(c, kBarRecEmpty + slot, (sg / kRecs - 1) & 1))
             return;
         reinterpret_cast<Rec *>(c.sbase + L::kOffRecs)[slot] = r;
+        ++n.recs;
         if (!more) {
             mbar_arrive(bar(c, kBarRecFull + slot));
             return;
@@ -177,10 +192,10 @@ __device__ void producer(const Ctx &c, const Split &split)
                           static_cast<long long>(r.head) * a.group * D,
                       row, bar(c, kBarRecFull + slot));
         const int col = r.head * D;
-        for (int k = r.kb; k < r.ke; ++k, ++g) {
-            const int st = g % L::kStages;
-            const uint32_t u = g / L::kStages;
-            if (u > 0 && !mbar_wait(bar(c, kBarEmpty + st), (u - 1) & 1, a.err))
+        for (int k = r.kb; k < r.ke; ++k, ++n.kv) {
+            const int st = n.kv % L::kStages;
+            const uint32_t u = n.kv / L::kStages;
+            if (u > 0 && !wait(c, kBarEmpty + st, (u - 1) & 1))
                 return;
             const uint32_t dst = c.base + st * 2 * L::kTile;
             mbar_arrive_expect_tx(bar(c, kBarFull + st), 2 * L::kTile);
@@ -192,6 +207,16 @@ __device__ void producer(const Ctx &c, const Split &split)
             }
         }
     }
+}
+
+// Every copy has landed before the CTA can exit, wherever the producer stopped.
+template <int D>
+__device__ void producer(const Ctx &c, const Split &split)
+{
+    Issued n;
+    produce<D>(c, split, n);
+    ring_drain(bar(c, kBarRecFull), n.recs, kRecs);
+    ring_drain(bar(c, kBarFull), n.kv, Layout<D>::kStages);
 }
 
 // The 16 keys of this warp in tile k that are visible, as bits.
@@ -219,7 +244,8 @@ __device__ void compute(const Ctx &c, int warp, int lane, int cta)
     uint32_t g = 0;
     for (uint32_t sg = 0;; ++sg) {
         const int slot = sg % kRecs;
-        if (!mbar_wait(bar(c, kBarRecFull + slot), (sg / kRecs) & 1, a.err))
+        wait(c, kBarRecFull + slot, (sg / kRecs) & 1);
+        if (stop(c))
             return;
         const Rec s = reinterpret_cast<const Rec *>(c.sbase + L::kOffRecs)[slot];
         if (s.ke == 0)
@@ -250,8 +276,7 @@ __device__ void compute(const Ctx &c, int warp, int lane, int cta)
             if (k + 1 < s.ke)
                 keys = warp_keys(c, s, k + 1, warp);      // a tile ahead
             const int st = g % L::kStages;
-            if (!mbar_wait(bar(c, kBarFull + st), (g / L::kStages) & 1, a.err))
-                return;
+            wait(c, kBarFull + st, (g / L::kStages) & 1);
             __syncwarp();
             const uint32_t kt = c.base + st * 2 * L::kTile, vt = kt + L::kTile;
             if (now) {
@@ -345,8 +370,8 @@ __device__ void compute(const Ctx &c, int warp, int lane, int cta)
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-        if (sg > 0 && !mbar_wait(bar(c, kBarJoined), (sg - 1) & 1, a.err))
-            return;
+        if (sg > 0)
+            wait(c, kBarJoined, (sg - 1) & 1);
         __syncwarp();
         float *mine = states + warp * kRows * L::kStateRow;
 #pragma unroll
@@ -364,9 +389,9 @@ __device__ void compute(const Ctx &c, int warp, int lane, int cta)
         __syncwarp();
         if (lane == 0)
             mbar_arrive(bar(c, kBarStates));
-        if (!mbar_wait(bar(c, kBarStates), sg & 1, a.err))
+        wait(c, kBarStates, sg & 1);
+        if (stop(c))
             return;
-        __syncwarp();
         const bool whole = s.ke - s.kb == s.tiles;
         float *part = a.parts + (2ll * cta + (s.kb == 0)) * cross_slot_floats(kRows, D);
         // eight numbers of a row per thread
@@ -448,6 +473,7 @@ attn_cross_token_kernel(const __grid_constant__ CrossArgs a)
             }
             mbar_init(bar(c, kBarStates), kWarps);
             mbar_init(bar(c, kBarJoined), kWarps);
+            sts32(c.bars + kGaveUpInBars, 0u);
             fence_mbar_init();
         }
         __syncthreads();
