@@ -65,6 +65,7 @@
 #include "common.cuh"
 #include "cross_sched.cuh"
 #include "internal.h"
+#include "roles.cuh"
 
 namespace mbert {
 namespace {

@@ -24,6 +24,7 @@
 #include "common.cuh"
 #include "cross_sched.cuh"
 #include "internal.h"
+#include "roles.cuh"
 
 namespace mbert {
 namespace {

@@ -77,6 +77,7 @@ constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, false);
 constexpr uint32_t kIdescO = make_idesc_bf16(128, 64, true);
 constexpr float kScaleLog2 = 0.125f * 1.4426950408889634f;
 constexpr float kSlack = 64.0f;     // reference maximum may sit this far (base 2) below the row maximum
+constexpr unsigned long long kDrainLimitNs = 100000000ull;
 
 __device__ __forceinline__ uint32_t barp(uint32_t base, int i) { return base + kOffBar + 8u * i; }
 __device__ __forceinline__ uint32_t ring_parity(int t) { return static_cast<uint32_t>(t / kRing) & 1u; }

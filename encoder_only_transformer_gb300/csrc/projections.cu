@@ -78,6 +78,7 @@ enum : int {
 };
 
 constexpr uint32_t kIdesc = make_idesc_bf16(kUnitM, kBN, false);
+constexpr unsigned long long kDrainLimitNs = 100000000ull;
 
 __device__ __forceinline__ uint32_t barp(uint32_t base, int i) { return base + kOffBar + 8u * i; }
 
