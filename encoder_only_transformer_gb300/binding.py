@@ -694,7 +694,8 @@ class Attention:
                 int(tot.value))
 
     def get_error(self) -> int:
-        """Synchronise and return (and clear) the device-side status."""
+        """Wait for the device (every stream, replayed graphs too), then return
+        and clear the device-side status."""
         return int(load_library().mbert_attn_get_error(self._h))
 
 

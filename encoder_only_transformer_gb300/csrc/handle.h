@@ -22,7 +22,7 @@ struct mbert_attn {
     int num_sms = 0;
     mbert_attn_config cfg{};
     float2 *rope[2] = {nullptr, nullptr};   // [MBERT_GLOBAL], [MBERT_LOCAL]: [max_seqlen][32]
-    int32_t *err = nullptr;                 // sticky device error word
+    int32_t *err = nullptr;                 // sticky device error word, and what get_error took of it
     int32_t *work_count = nullptr;
     int2 *work = nullptr;
     int64_t work_cap = 0;                   // entries
@@ -48,7 +48,6 @@ struct mbert_attn {
     // lets the softmax skip its row maximum: Q fp32 [12][rot_cap], then K
     // fp16 [12][rot_cap] (rot_cap a multiple of 8)
     float *norms = nullptr;
-    cudaStream_t last_stream = nullptr;
     EncodeTiledFn encode = nullptr;
     // measurement: event pairs around the attention kernel, per layer kind
     bool profiling = false;

@@ -377,10 +377,10 @@ MBERT_API int mbert_attn_create(mbert_attn **out, const mbert_attn_config *cfg, 
         }
     }
     if (rc == MBERT_OK) {
-        if (cudaMalloc(&h->err, sizeof(int32_t)) != cudaSuccess ||
+        if (cudaMalloc(&h->err, 2 * sizeof(int32_t)) != cudaSuccess ||
             cudaMalloc(&h->work_count, sizeof(int32_t)) != cudaSuccess)
             rc = MBERT_ERR_OOM;
-        else if (cudaMemset(h->err, 0, sizeof(int32_t)) != cudaSuccess ||
+        else if (cudaMemset(h->err, 0, 2 * sizeof(int32_t)) != cudaSuccess ||
                  cudaMemset(h->work_count, 0, sizeof(int32_t)) != cudaSuccess)
             rc = MBERT_ERR_CUDA;
     }
@@ -495,7 +495,6 @@ int forward_impl(mbert_attn *h, const void *qkv, const int32_t *cu_seqlens, int 
         if (e == cudaSuccess && ev1)
             e = cudaEventRecord(ev1, st);
         h->launches += 1;
-        h->last_stream = st;
         return e == cudaSuccess ? MBERT_OK : fail_cuda(e);
     }
     float *norms = nullptr;
@@ -517,7 +516,6 @@ int forward_impl(mbert_attn *h, const void *qkv, const int32_t *cu_seqlens, int 
     if (e == cudaSuccess && ev1)
         e = cudaEventRecord(ev1, st);
     h->launches += 2;
-    h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : fail_cuda(e);
 }
 
@@ -601,7 +599,6 @@ MBERT_API int mbert_attn_forward_padded(mbert_attn *h, const void *qkv, const in
     e = launch_scatter_rows(h->pad_out, h->pad_idx, h->pad_cu, batch, seq_len, kHidden,
                             static_cast<__nv_bfloat16 *>(out), h->num_sms, st);
     h->launches += 1;
-    h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : fail_cuda(e);
 }
 
@@ -626,7 +623,6 @@ MBERT_API int mbert_attn_key_counts(mbert_attn *h, const int32_t *cu_seqlens, in
     cudaError_t e = launch_plan(p, st);
     if (e == cudaSuccess)
         e = launch_key_count(p, layer_kind == MBERT_GLOBAL ? -1 : h->cfg.half_window, counts, st);
-    h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : fail_cuda(e);
 }
 
@@ -669,7 +665,6 @@ MBERT_API int mbert_attn_out_proj(mbert_attn *h, const void *a, const void *wo, 
     if (e == cudaSuccess && ev1)
         e = cudaEventRecord(ev1, st);
     h->launches += 1;
-    h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : fail_cuda(e);
 }
 
@@ -734,7 +729,6 @@ MBERT_API int mbert_attn_ln_qkv(mbert_attn *h, const void *x, const void *norm_w
     if (e == cudaSuccess && ev1)
         e = cudaEventRecord(ev1, st);
     h->launches += 1;
-    h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : fail_cuda(e);
 }
 
@@ -803,7 +797,6 @@ MBERT_API int mbert_attn_mlp(mbert_attn *h, const void *x, const void *norm_w, c
     });
     timed(MBERT_PROFILE_MLP_UP, [&] { return launch_mlp_up(up, st); });
     timed(MBERT_PROFILE_MLP_DOWN, [&] { return launch_mlp_down(down, st); });
-    h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : fail_cuda(e);
 }
 
@@ -812,11 +805,14 @@ MBERT_API int mbert_attn_get_error(mbert_attn *h)
     if (!h)
         return MBERT_ERR_BAD_ARG;
     DeviceGuard g(h->device);
-    if (cudaStreamSynchronize(h->last_stream) != cudaSuccess)
+    // The calls so far, on whichever streams, replayed graphs among them.  Then
+    // the word is read and cleared in one step: another thread may be replaying a
+    // graph, and a bit that it sets must not get lost in between.
+    if (cudaDeviceSynchronize() != cudaSuccess)
         return MBERT_ERR_CUDA;
     int32_t word = 0;
-    if (cudaMemcpy(&word, h->err, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess ||
-        cudaMemset(h->err, 0, sizeof(int32_t)) != cudaSuccess)
+    if (launch_take_error(h->err, h->err + 1, nullptr) != cudaSuccess ||
+        cudaMemcpy(&word, h->err + 1, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess)
         return MBERT_ERR_CUDA;
     if (word & kErrTimeout)
         return MBERT_ERR_TIMEOUT;
@@ -837,7 +833,6 @@ MBERT_API int mbert_attn_selftest_timeout(mbert_attn *h, int64_t limit_us, void 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_wait_timeout_selftest(
         h->err, static_cast<unsigned long long>(limit_us) * 1000ull, st);
-    h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : fail_cuda(e);
 }
 

@@ -181,7 +181,6 @@ int rotary_impl(mbert_attn *h, const mbert_attn_heads *const (&xs)[2], int64_t t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = launch_rotary(a, h->num_sms, st);
     h->launches += 1;
-    h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : MBERT_ERR_CUDA;
 }
 
@@ -441,6 +440,5 @@ MBERT_API int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args,
         e = launch_cross_join(a, D, half, p.token ? p.max_q * p.group : p.unit_rows, p.ctas, st);
         h->launches += 1;
     }
-    h->last_stream = st;
     return e == cudaSuccess ? MBERT_OK : MBERT_ERR_CUDA;
 }

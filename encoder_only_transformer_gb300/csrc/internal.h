@@ -357,6 +357,9 @@ cudaError_t launch_cross_join(const CrossArgs &a, int dim, bool half, int rows, 
 // (above it the plan kernel writes a work list first).
 constexpr int kLocalSelfScheduleMaxSeqs = 256;
 
+// Moves the error word to *taken (device) and clears it, in one step.
+cudaError_t launch_take_error(int32_t *err, int32_t *taken, cudaStream_t stream);
+
 // One bounded mbarrier wait that nothing completes (exercises kErrTimeout).
 cudaError_t launch_wait_timeout_selftest(int32_t *err, unsigned long long limit_ns,
                                          cudaStream_t stream);

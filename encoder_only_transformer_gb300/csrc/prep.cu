@@ -325,7 +325,16 @@ __global__ void wait_timeout_selftest_kernel(int32_t *err, unsigned long long li
     mbar_wait(b, 0, err, limit_ns);
 }
 
+// One thread: the error word's bits to *taken, and the word cleared.
+__global__ void take_error_kernel(int32_t *err, int32_t *taken) { *taken = atomicExch(err, 0); }
+
 }  // namespace
+
+cudaError_t launch_take_error(int32_t *err, int32_t *taken, cudaStream_t stream)
+{
+    take_error_kernel<<<1, 1, 0, stream>>>(err, taken);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_wait_timeout_selftest(int32_t *err, unsigned long long limit_ns,
                                          cudaStream_t stream)

@@ -222,7 +222,7 @@ int mbert_attn_out_proj(mbert_attn *h, const void *a, const void *wo, const void
  * heads are turned or normed in another way than ModernBERT-base's, and for
  * decoders and pooling heads that read the encoder's states.  These calls
  * keep nothing in the handle but the error word, so calls on different
- * streams may overlap on the GPU.
+ * streams may overlap on the GPU; mbert_attn_get_error() waits for all of them.
  * ------------------------------------------------------------------------ */
 
 /* Element types of the calls below. */
@@ -375,10 +375,12 @@ int mbert_attn_cross_workspace(mbert_attn *h, const mbert_attn_cross_args *args,
 int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args, void *workspace,
                      int64_t workspace_bytes, void *stream);
 
-/* Wait for the handle's most recent stream, then return (and clear) the
- * device error word as a status: MBERT_OK, MBERT_ERR_BAD_CU_SEQLENS,
- * MBERT_ERR_SEQ_TOO_LONG or MBERT_ERR_TIMEOUT; MBERT_ERR_CUDA if the wait
- * itself fails. */
+/* Wait for the device's work so far (every stream the handle was used on, and
+ * replayed graphs), then return and clear, in one step, the device error word
+ * as a status: MBERT_OK, MBERT_ERR_BAD_CU_SEQLENS, MBERT_ERR_SEQ_TOO_LONG or
+ * MBERT_ERR_TIMEOUT; MBERT_ERR_CUDA if the wait itself fails.  The word holds
+ * what calls on all streams have set since it was last asked for; it does not
+ * say which call. */
 int mbert_attn_get_error(mbert_attn *h);
 
 /* Diagnostic: enqueue one kernel whose bounded wait on a barrier that
