@@ -1,6 +1,7 @@
 // Host side of the calls beside the attention block: argument checks of the
 // rotary, norm and cross-attention calls, the rotation's frequencies, the
 // choice of the cross-attention kernel.
+#include <algorithm>
 #include <cmath>
 
 #include "mbert_attn.h"
@@ -173,6 +174,14 @@ int rotary_impl(mbert_attn *h, const mbert_attn_heads *const (&xs)[2], int64_t t
     a.interleaved = a.rot > 0 && rope->layout == MBERT_ROTARY_INTERLEAVED;
     a.norm = norm;
     a.eps = eps;
+    // Squares that fp32 rounds to nothing (below 2^-149, so a sum of 2^-90 of 256
+    // numbers is off by 2^-51 of itself at most) only matter beside an eps below
+    // 2^-40.  A scale of 2^k keeps eps 2^2k at 2^100 or less; where that holds k
+    // down, eps is all that counts of the sum.
+    constexpr uint32_t kBits2M90 = (127 - 90) << 23, kBits2P126 = (127 + 126) << 23;
+    a.least_squares = eps >= 0x1p-40f ? 0 : kBits2M90;
+    a.squares = kBits2P126 - a.least_squares;
+    a.most_scale = eps > 0.f ? std::ldexp(1.f, std::min(126, (100 - std::ilogb(eps)) / 2)) : 0x1p126f;
     a.amplitude = a.rot > 0 ? static_cast<float>(rope->amplitude) : 1.f;
     a.sin_amplitude = inverse ? -a.amplitude : a.amplitude;
     a.tokens = tokens;

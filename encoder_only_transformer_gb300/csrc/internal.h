@@ -257,6 +257,10 @@ struct RotaryArgs {
     int interleaved = 0;
     int norm = 0;                    // MBERT_NORM_*
     float eps = 0.f;
+    // a head's squares add up to one of the `squares` floats from the one with these
+    // bits on, or it is scaled first, by most_scale at most
+    uint32_t least_squares = 0, squares = 0;
+    float most_scale = 1.f;
     float amplitude = 1.f, sin_amplitude = 1.f;   // sin_amplitude < 0: the inverse rotation
     long long tokens = 0;
     // positions: 32 or 64 bits per row, or from cu_seqlens; none for rot = 0

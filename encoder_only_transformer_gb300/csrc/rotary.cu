@@ -25,6 +25,9 @@
 // side by side, so a norm needs k shuffles and no shared memory.  All heads of
 // a row share its cosines and sines: the block computes its rows' once into
 // shared memory, laid out so that the lanes' 16-byte reads have no conflicts.
+// Heads whose squares fp32 does not hold are left out by the loop and done after
+// it, scaled; that they are looked for costs nothing that shows on 24 heads a row,
+// on one head (262144 rows of 64, bf16) 27.6 -> 30.4 us.
 //
 // Measured: 65536 rows x 12 heads of 64 bf16 32.3 us, 6.2 TB/s (0.92 of the
 // copy bandwidth); queries and keys with RMS norm 63.2 us, 6.4 TB/s; LayerNorm,
@@ -33,6 +36,9 @@
 // rotation pair by pair: 280 instructions a step, 55 % of the issue slots, and
 // 64 registers leave 25 warps an SM to hide it).
 #include <cuda_fp16.h>
+
+#include <cmath>
+#include <type_traits>
 
 #include "mbert_attn.h"
 #include "common.cuh"
@@ -227,6 +233,15 @@ __device__ __forceinline__ float head_sum(float s, int lanes)
     return s;
 }
 
+__device__ __forceinline__ float head_max(float m, int lanes)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        if (lanes > d)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return m;
+}
+
 // Position of a row: given (32 or 64 bits), or its place in its sequence.
 // False for a row behind the last sequence.
 __device__ __forceinline__ bool row_position(const RotaryArgs &a, long long row, long long &pos)
@@ -296,6 +311,38 @@ __device__ __forceinline__ Nums<VW> table_read(const float *t, int slot, int rot
         c.v = t[slot];
     }
     return c;
+}
+
+// A row's numbers from memory, scaled by the power of two that brings its head's
+// largest near 1, at most most_scale; by 1 where that is zero or infinite.  Gives
+// the scale.
+template <typename T, int VW, int SPL>
+__device__ float load_scaled(const T *row, const int (&off0)[SPL], const int (&off1)[SPL], int slots, int slot0,
+                             bool mine, float most_scale, int lanes, Nums<VW> (&f0)[SPL], Nums<VW> (&f1)[SPL])
+{
+    using V = Vec<T, VW>;
+    float big = 0.f;
+#pragma unroll
+    for (int j = 0; j < SPL; ++j) {
+        V v{}, w{};
+        if (mine && slot0 + 32 * j < slots) {
+            v = *reinterpret_cast<const V *>(row + off0[j]);
+            w = *reinterpret_cast<const V *>(row + off1[j]);
+        }
+        f0[j] = unpack(v);
+        f1[j] = unpack(w);
+#pragma unroll
+        for (int i = 0; i < VW; ++i)
+            big = fmaxf(big, fmaxf(fabsf(f0[j].get(i)), fabsf(f1[j].get(i))));
+    }
+    big = head_max(big, lanes);
+    const float s = big > 0.f && big < INFINITY ? fminf(scalbnf(1.f, -ilogbf(big)), most_scale) : 1.f;
+#pragma unroll
+    for (int j = 0; j < SPL; ++j) {
+        f0[j] = f0[j] * Nums<VW>::splat(s);
+        f1[j] = f1[j] * Nums<VW>::splat(s);
+    }
+    return s;
 }
 
 // VW numbers per vector; SPL slots per lane (more than one only where a head
@@ -409,60 +456,60 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
             w1[j] = unpack(z);
         }
     }
+    const uint32_t least_squares = placed ? a.least_squares : 0u;
     const float inv_dim = 1.f / a.dim;
     const int lanes = 1 << a.lanes_log2;
-    const float *trow = s_table + 2 * half * team;          // of the step's row
-    const int tstep = 2 * half * a.teams;
-    auto step = [&](int r0, int u) {
-        const int r = r0 + team;
-        Nums<VW> f0[SPL], f1[SPL];
-        fetch_wait<kAhead - 1>();
+    // The statistics of a head, in fp32 over its lanes: LayerNorm in two passes
+    // (mean, then squared deviations).  Gives the sum of squares, and the factor.
+    auto norm = [&](Nums<VW> (&f0)[SPL], Nums<VW> (&f1)[SPL], float eps, float &rs) -> float {
+        if (a.norm == MBERT_NORM_LAYER) {
+            Nums<VW> t = f0[0] + f1[0];
 #pragma unroll
-        for (int j = 0; j < SPL; ++j) {
-            f0[j] = unpack(s_rows[((u * SPL + j) * 2) * threads + tid]);
-            f1[j] = unpack(s_rows[((u * SPL + j) * 2 + 1) * threads + tid]);
+            for (int j = 1; j < SPL; ++j)
+                t = t + (f0[j] + f1[j]);
+            const Nums<VW> mean = Nums<VW>::splat(head_sum(t.sum(), lanes) * inv_dim);
+#pragma unroll
+            for (int j = 0; j < SPL; ++j)
+                if (slot0 + 32 * j < slots) {
+                    f0[j] = f0[j] - mean;
+                    f1[j] = f1[j] - mean;
+                }
         }
-        // the place is free for a later row
-        load(r + kAhead * a.teams, u);
+        Nums<VW> q = f0[0] * f0[0];
+        q = fma(f1[0], f1[0], q);
+#pragma unroll
+        for (int j = 1; j < SPL; ++j) {
+            q = fma(f0[j], f0[j], q);
+            q = fma(f1[j], f1[j], q);
+        }
+        const float total = head_sum(q.sum(), lanes);
+        rs = rsqrtf(fmaf(total, inv_dim, eps));
+        return total;
+    };
+    // Where a head's squares (or their sum, or LayerNorm's first one) are beyond
+    // fp32, or below it and not hidden by eps.  (In one comparison, as floats from 0
+    // up order like their bits.)  fp16's numbers have no such squares.
+    constexpr bool kOdd = kNorm && !std::is_same_v<T, __half>;
+    auto is_odd = [&](float total) { return kOdd && __float_as_uint(total) - least_squares >= a.squares; };
+    // norm's factor and weight, the rotation and the result
+    auto finish = [&](Nums<VW> (&f0)[SPL], Nums<VW> (&f1)[SPL], float rs, const float *table, T *to, bool store) {
         if constexpr (kNorm) {
-            // statistics in fp32 over the head's lanes; LayerNorm in two passes
-            // (mean, then squared deviations)
-            if (a.norm == MBERT_NORM_LAYER) {
-                Nums<VW> t = f0[0] + f1[0];
-#pragma unroll
-                for (int j = 1; j < SPL; ++j)
-                    t = t + (f0[j] + f1[j]);
-                const Nums<VW> mean = Nums<VW>::splat(head_sum(t.sum(), lanes) * inv_dim);
-#pragma unroll
-                for (int j = 0; j < SPL; ++j)
-                    if (slot0 + 32 * j < slots) {
-                        f0[j] = f0[j] - mean;
-                        f1[j] = f1[j] - mean;
-                    }
-            }
-            Nums<VW> q = f0[0] * f0[0];
-            q = fma(f1[0], f1[0], q);
-#pragma unroll
-            for (int j = 1; j < SPL; ++j) {
-                q = fma(f0[j], f0[j], q);
-                q = fma(f1[j], f1[j], q);
-            }
-            const Nums<VW> inv = Nums<VW>::splat(rsqrtf(fmaf(head_sum(q.sum(), lanes), inv_dim, a.eps)));
+            const Nums<VW> inv = Nums<VW>::splat(rs);
 #pragma unroll
             for (int j = 0; j < SPL; ++j) {
                 f0[j] = f0[j] * inv * w0[j];
                 f1[j] = f1[j] * inv * w1[j];
             }
         }
-        if (placed && r < rows && s_live[r]) {
+        if (store) {
 #pragma unroll
             for (int j = 0; j < SPL; ++j) {
                 const int s = slot0 + 32 * j;
                 if (s >= slots)
                     continue;
                 if (s < rot_slots) {
-                    const Nums<VW> c = table_read<VW>(trow, s, rot_slots);
-                    const Nums<VW> sn = table_read<VW>(trow + half, s, rot_slots);
+                    const Nums<VW> c = table_read<VW>(table, s, rot_slots);
+                    const Nums<VW> sn = table_read<VW>(table + half, s, rot_slots);
                     if constexpr (!kInterleaved) {
                         const Nums<VW> y = f0[j] * c - f1[j] * sn;
                         f1[j] = fma(f0[j], sn, f1[j] * c);
@@ -482,16 +529,63 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
                         }
                     }
                 }
-                *reinterpret_cast<V *>(dst + off0[j]) = pack<T, VW>(f0[j]);
-                *reinterpret_cast<V *>(dst + off1[j]) = pack<T, VW>(f1[j]);
+                *reinterpret_cast<V *>(to + off0[j]) = pack<T, VW>(f0[j]);
+                *reinterpret_cast<V *>(to + off1[j]) = pack<T, VW>(f1[j]);
             }
         }
+    };
+    const float *trow = s_table + 2 * half * team;          // of the step's row
+    const int tstep = 2 * half * a.teams;
+    static_assert(kMaxRows <= 64, "a bit per step");
+    uint64_t odd_steps = 0, bit = 1;
+    auto step = [&](int r0, int u) {
+        const int r = r0 + team;
+        Nums<VW> f0[SPL], f1[SPL];
+        fetch_wait<kAhead - 1>();
+#pragma unroll
+        for (int j = 0; j < SPL; ++j) {
+            f0[j] = unpack(s_rows[((u * SPL + j) * 2) * threads + tid]);
+            f1[j] = unpack(s_rows[((u * SPL + j) * 2 + 1) * threads + tid]);
+        }
+        // the place is free for a later row
+        load(r + kAhead * a.teams, u);
+        float rs = 1.f;
+        bool odd = false;
+        if constexpr (kNorm)
+            odd = is_odd(norm(f0, f1, a.eps, rs));
+        if constexpr (kOdd) {
+            odd_steps |= odd ? bit : 0;
+            bit <<= 1;
+        }
+        finish(f0, f1, rs, trow, dst, placed && r < rows && s_live[r] && !odd);
         dst += dst_step;
         trow += tstep;
     };
 #pragma unroll 1
     for (int r0 = 0, u = 0; r0 < rows; r0 += a.teams, u = (u + 1) % kAhead)
         step(r0, u);
+    if constexpr (kOdd) {
+        // The odd heads, which are as they were: scaled by a power of two, which
+        // with eps times its square leaves the norm as it is.  (Behind the loop, as
+        // a branch within it cost up to 9 %; and by the bits, as the other heads may
+        // have been written over their numbers.)
+#pragma unroll 1
+        for (int r0 = 0; __any_sync(0xffffffffu, odd_steps != 0); r0 += a.teams, odd_steps >>= 1) {
+            const bool odd = odd_steps & 1;
+            if (!__any_sync(0xffffffffu, odd))
+                continue;
+            const int r = r0 + team;
+            const bool mine = odd && r < rows;
+            Nums<VW> f0[SPL], f1[SPL];
+            float rs;
+            const float s = load_scaled<T, VW, SPL>(
+                static_cast<const T *>(x.src) + head * x.src_head + (row0 + r) * x.src_row, off0, off1, slots, slot0,
+                mine, a.most_scale, lanes, f0, f1);
+            norm(f0, f1, a.eps * s * s, rs);
+            finish(f0, f1, rs, s_table + 2 * half * r,
+                   static_cast<T *>(x.dst) + head * x.dst_head + (row0 + r) * x.dst_row, mine && s_live[r]);
+        }
+    }
     pdl_trigger();
 }
 

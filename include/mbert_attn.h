@@ -315,8 +315,10 @@ enum {
 /* Norm of every query and key head, then the rotation, in one pass and one
  * kernel.  q and k share the rows; either may be NULL (the other is then done
  * alone).  rope == NULL (or rope->dim == 0): the norm alone, without
- * positions.  0 <= eps <= 1; statistics in fp32 (numbers beyond 2^63, whose
- * squares fp32 does not hold, give 0).  Else as mbert_attn_rotary. */
+ * positions.  0 <= eps <= 1; statistics in fp32, where heads whose squares it
+ * does not hold are scaled by a power of two first, so any finite numbers do; a
+ * head without spread (all zeros, for LayerNorm all equal) is 0/0 with eps = 0.
+ * Else as mbert_attn_rotary. */
 int mbert_attn_qk_norm_rotary(mbert_attn *h, const mbert_attn_heads *q, const mbert_attn_heads *k,
                               int64_t tokens, int head_dim, int dtype, int norm, float eps,
                               const mbert_attn_rotary_spec *rope, const void *positions,
