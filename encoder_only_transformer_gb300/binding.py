@@ -160,6 +160,9 @@ def _layout(*tensors):
     return tuple([(t.shape, t.stride(), t.dtype, t.device) for t in tensors])
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
 class Rotary:
     """How a head is rotated: its first `dim` numbers (even, up to 256) in
     pairs, `layout` "half" (x[m], x[m + dim/2]) or "interleaved" (x[2m],
@@ -178,6 +181,11 @@ class Rotary:
     Host data only: made once, usable on every device."""
 
     def __init__(self, dim: int, base: float = 10000.0, layout: str = "half", scaling: dict = None):
+        if dim != int(dim):
+            raise ValueError(f"dim must be a whole number, not {dim!r}")
+        # (ctypes would cut a larger number to its lower 32 bits)
+        if abs(int(dim)) > _INT_MAX:
+            raise MbertAttnError(-1, "rotary_init")
         if layout not in _LAYOUTS:
             raise ValueError(f"layout must be 'half' or 'interleaved', not {layout!r}")
         sc = None
@@ -588,7 +596,9 @@ class Attention:
         16 / (Hq / Hk) rows a sequence), which then read k and v once, and for
         short ones (128 / (Hq / Hk)).  scale
         None: 1 / sqrt(D).  Rows may be strided (views of fused rows)."""
-        max_seqlen_q, scale = int(max_seqlen_q), None if scale is None else float(scale)
+        # (a bound beyond 32 bits is none; ctypes would cut it to its lower bits)
+        max_seqlen_q = max(-1, min(int(max_seqlen_q), _INT_MAX))
+        scale = None if scale is None else float(scale)
         key = ("cross", _layout(q, k, v, cu_seqlens_q, cu_seqlens_k), None if out is None else _layout(out),
                None if key_mask is None else _layout(key_mask), max_seqlen_q, scale)
         known = self._known.get(key)

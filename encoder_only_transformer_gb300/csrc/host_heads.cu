@@ -102,7 +102,7 @@ int rotary_impl(mbert_attn *h, const mbert_attn_heads *const (&xs)[2], int64_t t
         return MBERT_ERR_BAD_ARG;
     if (a.rot > 0) {
         if ((rope->layout != MBERT_ROTARY_HALF && rope->layout != MBERT_ROTARY_INTERLEAVED) ||
-            !std::isfinite(rope->amplitude))
+            !std::isfinite(static_cast<float>(rope->amplitude)))    // (fp32 in the kernel)
             return MBERT_ERR_BAD_ARG;
         for (int m = 0; m < a.rot / 2; ++m) {
             if (!(rope->freq[m] >= 0.0) || !std::isfinite(rope->freq[m]))

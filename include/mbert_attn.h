@@ -266,7 +266,7 @@ typedef struct {
 typedef struct {
     int dim;            /* even, 0 .. 256 (0: no rotation) */
     int layout;         /* MBERT_ROTARY_* */
-    double amplitude;
+    double amplitude;   /* within fp32's range */
     double freq[128];   /* dim / 2 of them, radians per position, finite, >= 0 */
 } mbert_attn_rotary_spec;
 
