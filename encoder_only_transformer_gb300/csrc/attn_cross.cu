@@ -143,7 +143,7 @@ constexpr int kBarPFull = 20;
 constexpr int kBarODone = 22;
 constexpr int kBarOFree = 24;
 constexpr int kBarBitsFull = 26;  // + mask slot (4): a tile's key bits are in shared memory
-constexpr int kBarBitsEmpty = 30; // + mask slot: read by all 256 softmax threads
+constexpr int kBarBitsEmpty = 30; // + mask slot: read by every softmax thread
 constexpr int kBarVClean = 34;    // + mask slot: a tile's unseen V rows are zeros
 constexpr int kBarRecFull = 38;   // + record slot (4)
 constexpr int kBarRecEmpty = 42;  // + record slot
@@ -578,17 +578,6 @@ __device__ void mask_stager(const Ctx &c, int lane)
 }
 
 // ---------------------------------------------------------------- softmax
-template <bool kHalf>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    uint32_t r;
-    if constexpr (kHalf)
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Two weights 2^(x scale - m): added to a packed row sum, packed to 16 bits.
 template <bool kHalf>
 __device__ __forceinline__ uint32_t weights(float x0, float x1, uint64_t sc2, uint64_t nm2, uint64_t &acc)

@@ -1,9 +1,8 @@
 // What cross attention does before and after its attention kernels: the key
 // mask as bits, and the joining of units that were cut between CTAs.
-#include <cuda_fp16.h>
-
 #include "common.cuh"
 #include "internal.h"
+#include "roles.cuh"
 
 namespace mbert {
 namespace {
@@ -53,17 +52,6 @@ key_bits_kernel(const int32_t *__restrict__ cu_k, int len_k, long long rows_k,
             len[s] = make_int2(v, f);
     }
     pdl_trigger();
-}
-
-template <bool kHalf>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    uint32_t r;
-    if constexpr (kHalf)
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 // The parts of a unit are states over disjoint keys, (O_p, m_p, l_p) with

@@ -118,8 +118,10 @@ int rotary_impl(mbert_attn *h, const mbert_attn_heads *const (&xs)[2], int64_t t
             if ((position_bits != 32 && position_bits != 64) || cu ||
                 reinterpret_cast<uintptr_t>(positions) % (position_bits / 8))
                 return MBERT_ERR_BAD_ARG;
-            (position_bits == 32 ? reinterpret_cast<const void *&>(a.pos32)
-                                 : reinterpret_cast<const void *&>(a.pos64)) = positions;
+            if (position_bits == 32)
+                a.pos32 = static_cast<const int32_t *>(positions);
+            else
+                a.pos64 = static_cast<const int64_t *>(positions);
         } else if (tokens > 0) {
             if (!cu || n_seqs < 1 || (reinterpret_cast<uintptr_t>(cu) & 3))
                 return MBERT_ERR_BAD_ARG;

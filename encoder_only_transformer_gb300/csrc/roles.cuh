@@ -1,6 +1,6 @@
-// Beside common.cuh, for kernels whose warps have roles of their own (cross
-// attention): waits that keep a warp together, the end of a CTA with work in
-// flight, 3-D TMA.
+// Beside common.cuh, for the kernels of cross attention, whose warps have roles of
+// their own: waits that keep a warp together, the end of a CTA with work in
+// flight, 3-D TMA, either 16-bit type.
 #pragma once
 
 #include "common.cuh"
@@ -84,6 +84,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm,
         " [%0], [%1, {%2, %3, %4}], [%5];"
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+
+// Two numbers as a pair of fp16 or bf16.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (kHalf)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 }  // namespace mbert
