@@ -84,7 +84,7 @@ template <int D, int G>
 using Split = CrossSplit<G == 1 ? 256 : D == 64 ? 384 : 512, kBlockM * G, cross_tile_keys(D, kBlockM * G), 6,
                          G == 1 ? 6 : D == 64 ? 5 : 4, D == 128 && G == 1 ? 20 : 10,
                          kCrossBlockWholeKeys / cross_tile_keys(D, kBlockM * G), 4, D == 128 && G == 1 ? 72 : 30,
-                         cross_block_ctas(kBlockM * G), D == 64 ? 5 : 2>;
+                         cross_block_ctas(kBlockM * G)>;
 
 // G: query tiles of a unit, a softmax group for each.
 template <int D, int G>

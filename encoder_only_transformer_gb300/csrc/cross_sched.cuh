@@ -33,10 +33,9 @@ namespace mbert {
 
 // kBlockQ: query rows of a unit (0: all of a sequence's), each the rows of
 // 2^fold_log2 heads, side by side; kTile: keys of a tile; kRounds 0: units are
-// never dealt out whole; kPerSm: CTAs of an SM;
-// kAlone: a CTA alone on its SM is faster by a part in kAlone.
+// never dealt out whole; kPerSm: CTAs of an SM.
 template <int kThreads, int kBlockQ_, int kTile_, int kFull_, int kHalf_, int kAlpha_, int kSnap_, int kRounds = 0,
-          int kJoin = 0, int kPerSm = 1, int kAlone = 1>
+          int kJoin = 0, int kPerSm = 1>
 struct CrossSplit {
     static constexpr int kBlockQ = kBlockQ_, kTile = kTile_, kSnap = kSnap_;
     static constexpr int kFull = kFull_, kHalf = kHalf_, kAlpha = kAlpha_;
@@ -227,8 +226,7 @@ struct CrossSplit {
             if (kPerSm == 2 && all <= max_ctas / 2 && !a.records)
                 ctas = min(ctas, max_ctas / 2);
             const long long share = total / ctas;
-            const long long limit = !a.records ? INT64_MAX :
-                                    share + (kPerSm == 2 && all <= max_ctas / 2 ? share / kAlone : 0) + kJoin;
+            const long long limit = a.records ? share + kJoin : INT64_MAX;
             // (not worth dealing where one unit, or the shortest in every round, is
             // above the limit)
             const int rounds = (all + max_ctas - 1) / max_ctas;
