@@ -593,9 +593,11 @@ class Attention:
         hides keys; a row without a visible key is 0; rows of out behind the
         last sequence are left as they were.  max_seqlen_q is the caller's bound
         on the longest query sequence: give it for single tokens (at most
-        16 / (Hq / Hk) rows a sequence), which then read k and v once, and for
-        short ones (128 / (Hq / Hk)).  scale
-        None: 1 / sqrt(D).  Rows may be strided (views of fused rows)."""
+        16 / (Hq / Hk) rows a sequence), which then have a kernel of their own, and
+        for short ones (128 / (Hq / Hk)): without it the call counts on one sequence
+        of Tq rows (a token of 200 sequences over 500 keys, 12 heads of 64: 125 us
+        instead of 61; of 64 over 2000: 81 instead of 76).  scale None: 1 / sqrt(D).
+        Rows may be strided (views of fused rows)."""
         # (a bound beyond 32 bits is none; ctypes would cut it to its lower bits)
         max_seqlen_q = max(-1, min(int(max_seqlen_q), _INT_MAX))
         scale = None if scale is None else float(scale)

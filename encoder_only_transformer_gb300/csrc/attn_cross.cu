@@ -7,10 +7,11 @@
 // Work: a unit is 256 query rows of one sequence and head (two tiles of 128;
 // G = 2 below) or, in calls whose sequences have no more than 128 rows, one such
 // tile (G = 1, with two CTAs an SM: a unit's start and end then lie beside the
-// other one's tiles, and no softmax warps stand idle; D = 64, 64 sequences of 30
-// queries over 600 keys 45 -> 32 us, 100 of 20 over 250 39 -> 30; D = 128, 24 of
-// 32 over 1000, 32 heads over 8, 36 -> 30; but for 256 rows and more, D = 64, 200
-// us against 195 and 35 against 33, as K and V are fetched twice as often); units
+// other one's tiles, and no softmax warps stand idle; packed calls with their
+// bound given: 64 sequences of 30 queries over 600 keys each, 12 heads of 64, 45.7 ->
+// 36.1 us, 100 of 20 over 250 44.4 -> 33.5; 24 of 32 over 1000, 32 heads over 8 of 128,
+// 33.8 -> 30.7; but for 256 rows and more, D = 64, 200 us against 195 and 35 against
+// 33, as K and V are fetched twice as often); units
 // and their tiles of 128 keys (D = 128, G = 1: 64) are split among the CTAs by cost
 // (cross_sched.cuh), and units cut between CTAs are joined by a second kernel
 // (cross_join.cu) in a fixed order.  Query heads that share a key head share
@@ -49,11 +50,16 @@
 // What bounds it.  D = 64: the softmax; a query tile alone takes 1750 clocks a
 // key tile (TMEM load 290, maximum 280, exponentials 710, the rest hand-offs),
 // two together 2100 to 2200, the tensor cores' products 1024.  8192 x 8192, 12
-// heads bf16: 185 us and 6 us of joining, 1080 TFLOP/s, 0.56 of the measured
-// peak.  Steps of 64 keys with three S buffers, which overlap more, took 231
+// heads bf16: 191 us and 5 us of joining, 1049 TFLOP/s, 0.54 of the measured
+// peak.  (The compiler's layout of the loop counts: the same loop beside more or
+// less code that runs once took 193 to 203 us.)  Steps of 64 keys with three S buffers, which overlap more, took 231
 // us: their loads, stores and waits come twice as often.  D = 128: the tensor
 // cores and the hand-offs; ragged prompts of 16 heads over 4 (fp16): 160 us and
-// 10 us of joining for 214 GFLOP, 1260 TFLOP/s, 0.65 of the peak.
+// 10 us of joining (178 in all on another board) for 214 GFLOP, 1260 TFLOP/s, 0.65 of
+// the peak.
+//
+// Spills: D = 64, G = 2 reloads 16 bytes, D = 128, G = 2 148 (16 warps leave 128
+// registers a thread before the split), G = 1 8 bytes.
 //
 // Softmax: online, in base 2, held in fp32.  The reference m moves (and O is
 // rescaled) only when a tile's maximum passes it by more than 8, so weights

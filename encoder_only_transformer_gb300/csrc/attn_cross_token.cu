@@ -10,8 +10,8 @@
 // three (D = 64) or two (D = 128) CTAs an SM (130 KB in flight), and the units
 // (sequence, key head) are split by cost over all CTAs (cross_sched.cuh), long
 // ones into many parts, which a second kernel joins.  32 sequences of 128 to
-// 8192 keys, 12 heads of 64 in rows of 24: 85 us and 4.5 us of joining for
-// 488 MB, 5.4 TB/s; the same keys with each head's rows together, 6.2 TB/s, so
+// 8192 keys, 12 heads of 64 in rows of 24: 88 us and 3 us of joining for
+// 488 MB, 5.4 TB/s (82 in all on another board); the same keys with each head's rows together, 6.2 TB/s, so
 // what is left is DRAM's price for 128 bytes out of each row of 24 heads.  (Four heads to a
 // CTA, 512 bytes in one place, gave 3 to 8 % there and lost up to 45 % on few
 // sequences, whose units then are cut into four times as many parts.)

@@ -19,8 +19,10 @@
 // whole, the longest first, in rounds that run forth and back over the CTAs;
 // if the CTA with the most gets no more than the line's share and kJoin, what
 // cutting and joining costs, they stay so.  12 sequences of 250 queries over
-// 1000 keys, 12 heads of 64: 20.3 us, 24.6 cut; 24 over 600 to 1000: 31.9,
-// 35.7 cut; 32 heads over 8 of 128, 9 sequences: 41, 50 cut.  With the longest
+// 1000 keys, 12 heads of 64: 21.0 us, 25.5 cut; 24 of 256 over 600 to 1000 evenly: 29.9,
+// 33.6 cut; 9 of 250 over 1000, 32 heads over 8 of 128: 41.6, 50.4 cut; 64 of 30 over
+// 600, 12 heads of 64: 36.1, 42.4 cut.  What it loses is its search, where no unit is
+// long enough to be cut: 100 of 20 over 250: 33.5, 30.9 without.  With the longest
 // unit 34 above the share (16 sequences of 118 to 1946 keys) both took 32.5 to
 // 33.  Divisions stay the compiler's 64-bit ones: 32-bit ones where the costs
 // allow, a branch at each, made 8192 x 8192 1 % slower.
@@ -40,7 +42,10 @@ struct CrossSplit {
     static constexpr int kBlockQ = kBlockQ_, kTile = kTile_, kSnap = kSnap_;
     static constexpr int kFull = kFull_, kHalf = kHalf_, kAlpha = kAlpha_;
     static constexpr int kWarps = kThreads / 32;
-    static constexpr int kDealSeqs = 128;       // sequences whose units are dealt out, at most
+    // Sequences whose units are dealt out, at most: two threads rank each, and the
+    // lists must fit the output's staging place.  One more costs what dealing gains
+    // (20 queries over 550 keys, 6 heads of 64: 128 sequences 36.3 us, 129 42.5).
+    static constexpr int kDealSeqs = 128;
     static_assert(kRounds == 0 || 2 * kDealSeqs <= kThreads, "two threads per sequence");
 
     struct Scratch {

@@ -318,8 +318,10 @@ struct CrossRecord {
 constexpr int kCrossBlockRows = 256;
 constexpr int kCrossSmallRows = 128;
 // For head size 128 only up to this many keys a sequence, in the mean: its CTAs
-// have half the bytes in flight (19 sequences of 32 x 8000 keys, 32 heads over 8:
-// 107 us against 99; of 1000 keys 30 against 36).
+// have half the bytes in flight.  One query tile against two, us: 24 sequences of 32,
+// 32 heads over 8: 800 keys 26.6 / 33.1, 1500 38.9 / 42.2, 2000 52.9 / 49.9, 3000 72.6 /
+// 69.1; 100 of 100, 8 heads: 1200 94 / 106, 1600 116 / 128, 2000 156 / 153; 40 of 16, 16
+// over 2: 1600 25.9 / 27.0, 2000 29.4 / 29.4.
 constexpr int kCrossSmallKeys = 1536;
 // Keys of a tile of its K and V: 64 where two CTAs of head size 128 share an SM.
 constexpr int cross_tile_keys(int dim, int unit_rows) { return dim == 128 && unit_rows == kCrossSmallRows ? 64 : 128; }
