@@ -57,10 +57,27 @@ class CrossArgs(ctypes.Structure):
                 ("cu_q", _vp), ("cu_k", _vp), ("max_seqlen_q", ctypes.c_int), ("key_mask", _vp)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("weight", _vp), ("bias", _vp), ("residual", _vp), ("out", _vp),
+                ("x_row", _c_i64), ("weight_row", _c_i64), ("weight_expert", _c_i64), ("residual_row", _c_i64),
+                ("out_row", _c_i64), ("rows", _c_i64), ("inner", _c_int), ("outer", _c_int), ("dtype", _c_int),
+                ("activation", _c_int), ("gated", _c_int), ("experts", _c_int), ("cu_experts", _vp),
+                ("row_scale", _vp)]
+
+
+class ResidualNormArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("branch", _vp), ("gate", _vp), ("weight", _vp), ("bias", _vp),
+                ("branch_weight", _vp), ("branch_bias", _vp), ("h", _vp), ("y", _vp),
+                ("x_row", _c_i64), ("branch_row", _c_i64), ("gate_row", _c_i64), ("h_row", _c_i64), ("y_row", _c_i64),
+                ("rows", _c_i64), ("width", _c_int), ("dtype", _c_int), ("norm", _c_int), ("gate_kind", _c_int),
+                ("cu_seqlens", _vp), ("n_seqs", _c_int), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "yarn": 4}
 _NORMS = {"rms": 1, "layer": 2}
+_ACTIVATIONS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3, "relu": 4}
 
 SIGNATURES = {
     "mbert_attn_default_config": (_c_int, [ctypes.POINTER(Config)]),
@@ -81,6 +98,8 @@ SIGNATURES = {
                                            ctypes.POINTER(RotarySpec), _vp, _c_int, _vp, _c_int, _vp]),
     "mbert_attn_cross_workspace": (_c_int, [_vp, ctypes.POINTER(CrossArgs), ctypes.POINTER(_c_i64)]),
     "mbert_attn_cross": (_c_int, [_vp, ctypes.POINTER(CrossArgs), _vp, _c_i64, _vp]),
+    "mbert_attn_linear": (_c_int, [_vp, ctypes.POINTER(LinearArgs), _vp]),
+    "mbert_attn_residual_norm": (_c_int, [_vp, ctypes.POINTER(ResidualNormArgs), _vp]),
     "mbert_attn_get_error": (_c_int, [_vp]),
     "mbert_attn_selftest_timeout": (_c_int, [_vp, _c_i64, _vp]),
     "mbert_attn_forward_noalloc": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_int, _c_int, _vp, _vp,
@@ -670,6 +689,202 @@ class Attention:
             out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
         return self._cross(known, q, k, v, out, None, None, key_mask)
 
+    def _check_rows(self, t, name, dtype, shape):
+        """A tensor of that type and shape on this device whose last dimension is contiguous."""
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != self.device:
+            raise TypeError(f"{name} must be a {dtype} {list(shape)} tensor on {self.device}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+
+    @staticmethod
+    def _pitch(t):
+        """Elements from row to row of a [T, D] tensor (one row has no pitch that matters)."""
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+    def _linear_known(self, key, x, weight, experts, bias, activation, gated, residual, row_scale, out):
+        """Check a call's layouts and remember its arguments without pointers."""
+        if activation not in _ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, not {activation!r}")
+        if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16) or x.device != self.device:
+            raise TypeError(f"x must be a bf16 or fp16 [T, K] tensor on {self.device}")
+        T, K = x.shape
+        lead = () if experts is None else (experts,)
+        if weight.dim() != 2 + len(lead):
+            raise TypeError(f"weight must have the shape {'[N, K]' if experts is None else '[experts, N, K]'}")
+        W = weight.shape[-2]
+        if gated and W % 2:
+            raise ValueError("a gated product's weight has an even number of rows")
+        N = W // 2 if gated else W
+        if K < 1 or N < 1:
+            raise ValueError("weight must have rows and columns")
+        self._check_rows(x, "x", x.dtype, (T, K))
+        self._check_rows(weight, "weight", x.dtype, lead + (W, K))
+        if bias is not None:
+            self._check_rows(bias, "bias", x.dtype, lead + (W,))
+            if not bias.is_contiguous():
+                raise ValueError("bias must be contiguous")
+        if residual is not None:
+            self._check_rows(residual, "residual", x.dtype, (T, N))
+        if row_scale is not None and (row_scale.dtype != torch.float32 or tuple(row_scale.shape) != (T,)
+                                      or row_scale.device != self.device or not row_scale.is_contiguous()):
+            raise TypeError(f"row_scale must be a contiguous fp32 [{T}] tensor on {self.device}")
+        if out is not None:
+            self._check_rows(out, "out", x.dtype, (T, N))
+        for t, name in ((x, "x"), (weight, "weight")):
+            if any(n > 1 and st % 8 for n, st in zip(t.shape[:-1], t.stride()[:-1])):
+                raise ValueError(f"the rows of {name} must lie a multiple of 8 elements apart")
+        args = LinearArgs(None, None, None, None, None, self._pitch(x), weight.stride(-2) if W > 1 else K,
+                          weight.stride(0) if experts is not None and experts > 1 else 0,
+                          self._pitch(residual) if residual is not None else 0,
+                          self._pitch(out) if out is not None else N, T, K, N, _DTYPES[x.dtype],
+                          _ACTIVATIONS[activation], 1 if gated else 0, experts or 0, None, None)
+        return self._remember(key, (bytes(args), (T, N)))
+
+    def _linear(self, known, what, x, weight, bias, residual, out, cu=None, row_scale=None):
+        template, shape = known
+        if out is None:
+            out = torch.empty(shape, dtype=x.dtype, device=self.device)
+        args = LinearArgs.from_buffer_copy(template)
+        args.x, args.weight, args.out = x.data_ptr(), weight.data_ptr(), out.data_ptr()
+        if bias is not None:
+            args.bias = bias.data_ptr()
+        if residual is not None:
+            args.residual = residual.data_ptr()
+        if cu is not None:
+            args.cu_experts = cu.data_ptr()
+        if row_scale is not None:
+            args.row_scale = row_scale.data_ptr()
+        st = _lib.mbert_attn_linear(self._h, ctypes.byref(args), _stream_of(self.device))
+        if st != 0:
+            _check(st, what)
+        return out
+
+    def linear(self, x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor = None, activation: str = "none",
+               gated: bool = False, residual: torch.Tensor = None, out: torch.Tensor = None) -> torch.Tensor:
+        """out[T, N] = residual + act(x weight^T + bias), for x [T, K] and weight
+        [N, K] (bf16 or fp16) of any width; fp32 sums and epilogue, one rounding.
+        activation: "none", "gelu" (the erf form), "gelu_tanh", "silu" or "relu".
+        gated: weight [2N, K] and bias [2N] hold the activated half first, and
+        out = residual + act(x Wg^T + bg) * (x Wu^T + bu).  `out` may be
+        `residual` itself.  Rows may be strided; those of x and weight start at
+        16-byte boundaries (K a multiple of 8 where they are contiguous)."""
+        gated = bool(gated)
+        key = ("linear", _layout(x, weight), None if bias is None else _layout(bias), activation, gated,
+               None if residual is None else _layout(residual), None if out is None else _layout(out))
+        known = self._known.get(key)
+        if known is None:
+            known = self._linear_known(key, x, weight, None, bias, activation, gated, residual, None, out)
+        return self._linear(known, "linear", x, weight, bias, residual, out)
+
+    def expert_linear(self, x: torch.Tensor, weight: torch.Tensor, cu_experts: torch.Tensor,
+                      bias: torch.Tensor = None, activation: str = "none", gated: bool = False,
+                      row_scale: torch.Tensor = None, out: torch.Tensor = None) -> torch.Tensor:
+        """linear with a weight for each group of rows: rows cu_experts[e] ..
+        cu_experts[e+1] (int32 [E+1]) of x take weight[e] and bias[e] of weight
+        [E, N, K] and bias [E, N] ([E, 2N, K] and [E, 2N] gated), and row t's
+        result is multiplied by row_scale[t] (fp32, a router's weight).  Empty
+        groups are allowed; rows of out behind the last group are left as they
+        were."""
+        gated = bool(gated)
+        key = ("expert_linear", _layout(x, weight, cu_experts), None if bias is None else _layout(bias), activation,
+               gated, None if row_scale is None else _layout(row_scale), None if out is None else _layout(out))
+        known = self._known.get(key)
+        if known is None:
+            self._check_cu(cu_experts)
+            experts = cu_experts.numel() - 1
+            if experts < 1:
+                raise ValueError("cu_experts must name at least one expert")
+            known = self._linear_known(key, x, weight, experts, bias, activation, gated, None, row_scale, out)
+        return self._linear(known, "expert_linear", x, weight, bias, None, out, cu_experts, row_scale)
+
+    def residual_norm(self, x: torch.Tensor, branch: torch.Tensor = None, weight: torch.Tensor = None,
+                      bias: torch.Tensor = None, branch_weight: torch.Tensor = None, branch_bias: torch.Tensor = None,
+                      gate: torch.Tensor = None, cu_seqlens: torch.Tensor = None, norm: str = "layer",
+                      residual_scale: float = 1.0, eps: float = NORM_EPS, h_out: torch.Tensor = None,
+                      y_out: torch.Tensor = None):
+        """(h, y) = the residual stream behind a block and its norm for the next:
+        h = residual_scale x + gate P(branch), y = N(h), over rows of x [T, D]
+        (bf16, fp16 or fp32; D up to 16384) in one kernel.  P is the norm with
+        branch_weight [D] (None: none) and branch_bias, N that with weight (None:
+        no y, None is returned for it) and bias, both "layer" or "rms".  gate:
+        [D], [T, D], or with cu_seqlens (int32 [n+1]) [n, D], of the row's
+        sequence; rows behind the last sequence are left as they were.  branch
+        None: (x, N(x)).  h_out and y_out may each be x or branch.  y is of the
+        h that has not been rounded.  Rows may be strided."""
+        if norm not in _NORMS:
+            raise ValueError(f"norm must be 'rms' or 'layer', not {norm!r}")
+        residual_scale, eps = float(residual_scale), float(eps)
+        given = (x, branch, weight, bias, branch_weight, branch_bias, gate, cu_seqlens, h_out, y_out)
+        key = ("residual_norm", tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in given]),
+               norm, residual_scale, eps)
+        known = self._known.get(key)
+        if known is None:
+            known = self._residual_norm_known(key, *given, norm, residual_scale, eps)
+        args = ResidualNormArgs.from_buffer_copy(known)
+        args.x = x.data_ptr()
+        h, y = x, None
+        if branch is not None:
+            h = torch.empty(x.shape, dtype=x.dtype, device=self.device) if h_out is None else h_out
+            args.branch, args.h = branch.data_ptr(), h.data_ptr()
+        if weight is not None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=self.device) if y_out is None else y_out
+            args.weight, args.y = weight.data_ptr(), y.data_ptr()
+        if bias is not None:
+            args.bias = bias.data_ptr()
+        if branch_weight is not None:
+            args.branch_weight = branch_weight.data_ptr()
+        if branch_bias is not None:
+            args.branch_bias = branch_bias.data_ptr()
+        if gate is not None:
+            args.gate = gate.data_ptr()
+        if cu_seqlens is not None:
+            args.cu_seqlens = cu_seqlens.data_ptr()
+        st = _lib.mbert_attn_residual_norm(self._h, ctypes.byref(args), _stream_of(self.device))
+        if st != 0:
+            _check(st, "residual_norm")
+        return h, y
+
+    def _residual_norm_known(self, key, x, branch, weight, bias, branch_weight, branch_bias, gate, cu_seqlens, h_out,
+                             y_out, norm, residual_scale, eps):
+        if x.dim() != 2 or x.dtype not in _DTYPES or x.device != self.device:
+            raise TypeError(f"x must be a bf16, fp16 or fp32 [T, D] tensor on {self.device}")
+        T, D = x.shape
+        if branch is None and weight is None:
+            raise ValueError("give branch, weight or both")
+        if branch is None and (branch_weight is not None or gate is not None or h_out is not None
+                               or residual_scale != 1.0):
+            raise ValueError("branch_weight, gate, residual_scale and h_out go with a branch")
+        for w, b, name in ((weight, bias, "bias"), (branch_weight, branch_bias, "branch_bias")):
+            if b is not None and w is None:
+                raise ValueError(f"{name} goes with its norm's weight")
+        if y_out is not None and weight is None:
+            raise ValueError("y_out goes with weight")
+        if cu_seqlens is not None and gate is None:
+            raise ValueError("cu_seqlens goes with a gate for each sequence")
+        for t, name in ((x, "x"), (branch, "branch"), (h_out, "h_out"), (y_out, "y_out")):
+            if t is not None:
+                self._check_rows(t, name, x.dtype, (T, D))
+        for t, name in ((weight, "weight"), (bias, "bias"), (branch_weight, "branch_weight"),
+                        (branch_bias, "branch_bias")):
+            if t is not None:
+                self._check_rows(t, name, x.dtype, (D,))
+        kind, n, gate_row = 0, 0, 0
+        if gate is not None:
+            if cu_seqlens is not None:
+                self._check_cu(cu_seqlens)
+                n = cu_seqlens.numel() - 1
+                if n < 1:
+                    raise ValueError("cu_seqlens must name at least one sequence")
+                kind, shape = 3, (n, D)
+            else:
+                kind, shape = (1, (D,)) if gate.dim() == 1 else (2, (T, D))
+            self._check_rows(gate, "gate", x.dtype, shape)
+            gate_row = self._pitch(gate) if gate.dim() == 2 else D
+        args = ResidualNormArgs(*[None] * 9, self._pitch(x), 0 if branch is None else self._pitch(branch), gate_row,
+                                D if h_out is None else self._pitch(h_out), D if y_out is None else self._pitch(y_out),
+                                T, D, _DTYPES[x.dtype], _NORMS[norm], kind, None, n, residual_scale, eps)
+        return self._remember(key, bytes(args))
+
     def key_counts(self, cu_seqlens: torch.Tensor, total_tokens: int, layer_kind,
                    max_seqlen: int = 0) -> torch.Tensor:
         """int32 [T]: keys the kernels' schedule and mask admit per query row."""
@@ -813,3 +1028,35 @@ def cross_attention_padded(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ke
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
     return _default(q.device).cross_attention_padded(q, k, v, key_mask, scale, out)
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor = None, activation: str = "none",
+           gated: bool = False, residual: torch.Tensor = None, out: torch.Tensor = None) -> torch.Tensor:
+    """out = residual + act(x weight^T + bias), or gated, of any width (CUDA, bf16
+    or fp16): Attention.linear on the device's handle."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    return _default(x.device).linear(x, weight, bias, activation, gated, residual, out)
+
+
+def expert_linear(x: torch.Tensor, weight: torch.Tensor, cu_experts: torch.Tensor, bias: torch.Tensor = None,
+                  activation: str = "none", gated: bool = False, row_scale: torch.Tensor = None,
+                  out: torch.Tensor = None) -> torch.Tensor:
+    """linear with a weight for each group of rows: Attention.expert_linear on the
+    device's handle."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    return _default(x.device).expert_linear(x, weight, cu_experts, bias, activation, gated, row_scale, out)
+
+
+def residual_norm(x: torch.Tensor, branch: torch.Tensor = None, weight: torch.Tensor = None,
+                  bias: torch.Tensor = None, branch_weight: torch.Tensor = None, branch_bias: torch.Tensor = None,
+                  gate: torch.Tensor = None, cu_seqlens: torch.Tensor = None, norm: str = "layer",
+                  residual_scale: float = 1.0, eps: float = NORM_EPS, h_out: torch.Tensor = None,
+                  y_out: torch.Tensor = None):
+    """(h, y): the residual stream behind a block and its norm for the next one:
+    Attention.residual_norm on the device's handle."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    return _default(x.device).residual_norm(x, branch, weight, bias, branch_weight, branch_bias, gate, cu_seqlens,
+                                            norm, residual_scale, eps, h_out, y_out)

@@ -377,6 +377,100 @@ int mbert_attn_cross_workspace(mbert_attn *h, const mbert_attn_cross_args *args,
 int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args, void *workspace,
                      int64_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Layers of any width: matrix products with their epilogue, plain and grouped by
+ * expert, and the norms around a block.  For encoders of other sizes, a model's
+ * heads, decoders beside the cross attention, and mixtures of experts.  These too
+ * keep nothing in the handle but the error word, so calls on different streams may
+ * overlap on the GPU.
+ * ------------------------------------------------------------------------ */
+
+/* Activations, of z in fp32. */
+enum {
+    MBERT_ACT_NONE = 0,
+    MBERT_ACT_GELU = 1,         /* z Phi(z), Phi the normal distribution (the erf form) */
+    MBERT_ACT_GELU_TANH = 2,    /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    MBERT_ACT_SILU = 3,         /* z / (1 + e^-z) */
+    MBERT_ACT_RELU = 4          /* max(z, 0) */
+};
+
+/* A matrix product with bias, activation and residual:
+ *   z = x weight^T + bias,  out = residual + act(z);
+ * gated, with weight and bias of 2 outer rows, z_g the first and z_u the other half of z:
+ *   out = residual + act(z_g) z_u.
+ * With experts > 0 the rows are grouped: rows cu_experts[e] .. cu_experts[e+1] take
+ * weight and bias e, and row t's result is multiplied by row_scale[t] (a router's weight).
+ *   x, out, residual  device [rows][inner] / [rows][outer], rows x_row / out_row /
+ *                residual_row elements apart (at least the width).  residual NULL: 0, and
+ *                always with experts.  out may be residual itself with the same pitch; else it
+ *                overlaps nothing.  x 16-byte aligned with x_row a multiple of 8; out, residual
+ *                and bias of any alignment (16-byte aligned rows are faster).
+ *   weight       device [max(experts, 1)][outer or 2 outer][inner], rows weight_row and experts
+ *                weight_expert elements apart, multiples of 8, 16-byte aligned.  ([out][in].)
+ *   bias         device [max(experts, 1)][outer or 2 outer], contiguous, or NULL.
+ *   rows         0 <= rows < 2^31 - 1024 (0 enqueues nothing); inner, outer 1 .. 2^24.
+ *   dtype        MBERT_BF16 or MBERT_F16, of all of these, else MBERT_ERR_UNSUPPORTED.
+ *   cu_experts   device int32 [experts + 1] (experts at most 65536): cu[0] = 0, non-decreasing,
+ *                cu[experts] <= rows; empty experts are allowed; rows of out from cu[experts] on
+ *                are left as they were.  A bad list sets MBERT_ERR_BAD_CU_SEQLENS for
+ *                mbert_attn_get_error(), and nothing is written.
+ *   row_scale    device fp32 [rows], with experts only, or NULL for 1.
+ * Products, sums and the epilogue in fp32, out rounded once.  One kernel, no workspace; results
+ * do not depend on timing. */
+typedef struct {
+    const void *x, *weight, *bias, *residual;
+    void *out;
+    int64_t x_row, weight_row, weight_expert, residual_row, out_row;
+    int64_t rows;
+    int inner, outer, dtype, activation, gated;
+    int experts;
+    const int32_t *cu_experts;
+    const float *row_scale;
+} mbert_attn_linear_args;
+
+int mbert_attn_linear(mbert_attn *h, const mbert_attn_linear_args *args, void *stream);
+
+/* Whose gate a row takes. */
+enum {
+    MBERT_GATE_NONE = 0,
+    MBERT_GATE_CHANNELS = 1,    /* gate [width], of every row */
+    MBERT_GATE_ROWS = 2,        /* gate [rows][width] */
+    MBERT_GATE_SEQUENCES = 3    /* gate [n_seqs][width], of the row's sequence */
+};
+
+/* The norms after one block and before the next, with the gate and the residual between:
+ *   h = residual_scale x + gate P(branch),  y = N(h),
+ * P the norm with branch_weight and branch_bias (branch_weight NULL: none), N the one with
+ * weight and bias (weight NULL: no y), both of kind `norm` (MBERT_NORM_*; a bias is added last
+ * and may be NULL) over rows of `width`.  branch NULL: y = N(x) alone (no gate, no h,
+ * residual_scale 1).
+ *   x, branch, h, y   device [rows][width], rows x_row, ... elements apart (at least the width).
+ *                h and y may each be x or branch itself with the same pitch; else they overlap
+ *                nothing.
+ *   width        1 .. 16384; rows as in mbert_attn_linear; dtype MBERT_BF16, _F16 or _F32, of all.
+ *   gate         rows of width, gate_row elements apart, as gate_kind says.
+ *   cu_seqlens   with MBERT_GATE_SEQUENCES: device int32 [n_seqs + 1], cu[0] = 0, non-decreasing,
+ *                cu[n] <= rows; rows of h and y from cu[n] on are left as they were.  A bad list
+ *                sets MBERT_ERR_BAD_CU_SEQLENS, and nothing is written.
+ *   eps          0 <= eps <= 1.
+ * All in fp32, h and y rounded once; y is of the h that has not been rounded.  Rows whose squares
+ * fp32 does not hold are scaled by a power of two first, so any finite rows do; a row without
+ * spread (all zeros, for LayerNorm all equal) is 0/0 with eps = 0.  Any alignment of the element
+ * size; rows of whole, 16-byte aligned vectors are read in these.  One kernel. */
+typedef struct {
+    const void *x, *branch, *gate;
+    const void *weight, *bias, *branch_weight, *branch_bias;
+    void *h, *y;
+    int64_t x_row, branch_row, gate_row, h_row, y_row;
+    int64_t rows;
+    int width, dtype, norm, gate_kind;
+    const int32_t *cu_seqlens;
+    int n_seqs;
+    float residual_scale, eps;
+} mbert_attn_residual_norm_args;
+
+int mbert_attn_residual_norm(mbert_attn *h, const mbert_attn_residual_norm_args *args, void *stream);
+
 /* Wait for the device's work so far (every stream the handle was used on, and
  * replayed graphs), then return and clear, in one step, the device error word
  * as a status: MBERT_OK, MBERT_ERR_BAD_CU_SEQLENS, MBERT_ERR_SEQ_TOO_LONG or
