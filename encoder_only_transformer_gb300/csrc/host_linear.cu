@@ -262,7 +262,8 @@ MBERT_API int mbert_attn_residual_norm(mbert_attn *h, const mbert_attn_residual_
     a.y = c.y;
     a.x_row = c.x_row;
     a.branch_row = c.branch_row;
-    a.gate_row = c.gate_kind == MBERT_GATE_CHANNELS ? 0 : c.gate_row;
+    a.gate_row = c.gate_row;
+    a.gate_channels = c.gate_kind == MBERT_GATE_CHANNELS;
     a.h_row = c.h_row;
     a.y_row = c.y_row;
     a.cu = c.cu_seqlens;

@@ -7,15 +7,23 @@
 // bf16, fp16 or fp32; everything between loading and storing is fp32, y is of the
 // h that has not been rounded.
 //
-// Bound by HBM: x and branch in, h and y out.  A row stays in registers from its
-// load to its store: 16-byte vectors, up to four (eight in fp32) a lane, by 1 to 32
-// lanes a row up to 1024 numbers and 2 to 16 warps beyond, which add their sums up in
-// shared memory; the weights come from L1 or L2 each time, which costs no DRAM traffic
-// and leaves the registers to the rows.  A norm's statistics are sums over the
-// registers, the LayerNorm's in two passes (mean, then squares about it).
+// Bound by HBM: x and branch in, h and y out.  A crew takes a row (or, of short rows,
+// as many as a warp has lanes for): a warp up to 2048 numbers (1024 in fp32), 32 to 64
+// a lane in registers, and up to 16 warps beyond, which add their sums up in shared
+// memory.  Rows come by cp.async into a ring of shared-memory slots of the crew's own,
+// and a slot is filled again as soon as h is in registers: the loads of the next rows run
+// while a row goes through its sums, which are chains of shuffles.  Every thread copies
+// the vectors that it will read, so it waits for its own copies only; the same ring with
+// bulk copies and barriers took 73 us where this takes 69 (65536 x 768 bf16, 403 MB, 5.8
+// TB/s), rows loaded into registers 84.  A norm's statistics are sums over the registers
+// in pairs, the LayerNorm's in two passes (mean, then squares about it).  Weights come
+// from L1 or L2 for each row.  Rows off 16 bytes come as the 16-byte pieces they lie in
+// and are taken number by number.
 //
 // Where the squares add up to what fp32 does not hold (or, beside a small eps, to
-// what it holds badly), the row is scaled by a power of two first: see Norm.
+// what it holds badly), the row is scaled by a power of two first: see norm_row.
+#include <algorithm>
+
 #include "internal.h"
 #include "residual_norm.h"
 #include "linear.cuh"
@@ -23,54 +31,115 @@
 namespace mbert {
 namespace {
 
-constexpr int kLaneNumbers = 32;    // numbers of a row that a lane holds, at most
-constexpr int kMostThreads = kResidualNormMaxWidth / kLaneNumbers;
+constexpr int kMostWarps = 16;      // of a crew
+constexpr int kCrewNumbers = 16;    // numbers of a row a lane holds in a crew of several warps, or, with
+                                    // all 16, up to twice as many
+static_assert(kResidualNormMaxWidth == 32 * kMostWarps * 2 * kCrewNumbers, "widest rows");
+constexpr int kWarpCrews = 4;       // crews of one warp in a block
+constexpr int kMostSlots = 8;
+// Few numbers a lane leave registers for a norm's bias and a gate of channels to be on
+// their way during the sums too, as the weights are (4099 x 8192 fp32 with all of them, a
+// crew of 16 warps alone on its SM: 110 us against 142).
+constexpr bool early(bool vectors, int numbers) { return vectors && numbers <= kCrewNumbers; }
 
-// The numbers of a row that lane `lane` of `step` holds: vectors of 16 bytes, the
-// lanes' side by side, or (rows that such vectors do not fit) single numbers, again
-// side by side.  load() fills with 0 behind the row's end.
-template <int kType, bool kVectors>
+// Registers of a kernel: the numbers that a lane holds, what is on its way to them as it
+// is in memory, and the rest.  With what the compiler takes by itself (126 for 24
+// numbers) too few warps share an SM.
+constexpr int most_registers(bool vectors, int numbers, int bytes)
+{
+    return (numbers + (early(vectors, numbers) ? 3 : 1) * numbers * bytes / 4 + 51) / 8 * 8;
+}
+static_assert(most_registers(true, kCrewNumbers, 4) * 32 * kMostWarps <= 65536 &&
+              most_registers(true, 2 * kCrewNumbers, 4) * 32 * kMostWarps <= 65536, "a crew on an SM");
+
+// The numbers of a row that a lane holds: kVecs vectors of 16 bytes, the lanes' side
+// by side and a warp's in one piece, or (of rows off 16 bytes) as many single numbers,
+// again side by side.  Numbers behind the row's end are 0.
+template <int kType, bool kVectors, int kVecs>
 struct Row {
-    static constexpr int kN = kType == MBERT_F32 ? 4 : 8;
-    int lane, step, width;
+    static constexpr int kBytes = kType == MBERT_F32 ? 4 : 2;
+    static constexpr int kN = 16 / kBytes;
+    int first, width;           // the first of them, the row's end
 
-    // number e of vector j is number at(j, e) of the row
-    __device__ int at(int j, int e) const
+    __device__ Row(int warp, int lane, int w)
+        : first(kVectors ? (warp * 32 * kVecs + lane) * kN : warp * 32 * kVecs * kN + lane), width(w)
     {
-        return kVectors ? (lane + j * step) * kN + e : lane + (j * kN + e) * step;
     }
-    __device__ bool in(int j, int e) const { return at(j, kVectors ? 0 : e) < width; }
+    // number e of vector j is number first + at(j, e) of the row
+    static constexpr __device__ int at(int j, int e) { return kVectors ? 32 * kN * j + e : 32 * (kN * j + e); }
+    __device__ bool in(int j, int e) const { return first + at(j, kVectors ? 0 : e) < width; }
 
-    __device__ void load(const void *p, long long row, int j, float (&v)[kN]) const
+    static constexpr int kPairs = kN / 2;
+
+    __device__ static void unpack(const uint4 &x, uint64_t (&v)[kPairs])
     {
-        if constexpr (kVectors) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (in(j, 0))
-                x = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + (row + at(j, 0)) * (16 / kN));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (kType == MBERT_F32)
-                    v[e] = __uint_as_float(w[e]);
-                else
-                    f2_split(unpack2<kType == MBERT_F16>(w[e]), v[2 * e], v[2 * e + 1]);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-                v[e] = 0.f;
-                if (in(j, e)) {
-                    if constexpr (kType == MBERT_F32)
-                        v[e] = static_cast<const float *>(p)[row + at(j, e)];
-                    else
-                        v[e] = load16<kType == MBERT_F16>(p, row + at(j, e));
-                }
-            }
+        for (int e = 0; e < kPairs; ++e) {
+            if constexpr (kType == MBERT_F32)
+                v[e] = f2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+            else
+                v[e] = unpack2<kType == MBERT_F16>(w[e]);
         }
     }
 
-    __device__ void store(void *p, long long row, int j, const float (&v)[kN]) const
+    // vector j from global memory, as it is
+    __device__ uint4 load_raw(const void *p, int j) const
     {
+        const char *q = static_cast<const char *>(p) + first * kBytes;
+        return in(j, 0) ? *reinterpret_cast<const uint4 *>(q + at(j, 0) * kBytes) : make_uint4(0, 0, 0, 0);
+    }
+
+    // vector j, from global memory
+    __device__ void load(const void *p, int j, uint64_t (&v)[kPairs]) const
+    {
+        const char *q = static_cast<const char *>(p) + first * kBytes;
+        if constexpr (kVectors) {
+            unpack(load_raw(p, j), v);
+        } else {
+            single(j, v, [&](int offset) {
+                if constexpr (kType == MBERT_F32)
+                    return *reinterpret_cast<const float *>(q + offset);
+                else
+                    return load16<kType == MBERT_F16>(q + offset, 0);
+            });
+        }
+    }
+
+    // from a row in shared memory
+    __device__ void load_shared(uint32_t row, int j, uint64_t (&v)[kPairs]) const
+    {
+        const uint32_t q = row + first * kBytes;
+        if constexpr (kVectors) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (in(j, 0))
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(q + at(j, 0) * kBytes) : "memory");
+            unpack(x, v);
+        } else {
+            single(j, v, [&](int offset) {
+                if constexpr (kType == MBERT_F32) {
+                    uint32_t x;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(q + offset) : "memory");
+                    return __uint_as_float(x);
+                } else {
+                    uint16_t x;
+                    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(q + offset) : "memory");
+                    float lo, hi;
+                    f2_split(unpack2<kType == MBERT_F16>(x), lo, hi);
+                    return lo;
+                }
+            });
+        }
+    }
+
+    __device__ void store(char *p, int j, const uint64_t (&v)[kPairs]) const
+    {
+        char *q = p + first * kBytes;
+        float f[kN];
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e)
+            f2_split(v[e], f[2 * e], f[2 * e + 1]);
         if constexpr (kVectors) {
             if (!in(j, 0))
                 return;
@@ -78,22 +147,58 @@ struct Row {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (kType == MBERT_F32)
-                    w[e] = __float_as_uint(v[e]);
+                    w[e] = __float_as_uint(f[e]);
                 else
-                    w[e] = pack2<kType == MBERT_F16>(v[2 * e], v[2 * e + 1]);
+                    w[e] = pack2<kType == MBERT_F16>(f[2 * e], f[2 * e + 1]);
             }
-            *reinterpret_cast<uint4 *>(static_cast<char *>(p) + (row + at(j, 0)) * (16 / kN)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(q + at(j, 0) * kBytes) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
                 if (!in(j, e))
                     continue;
                 if constexpr (kType == MBERT_F32)
-                    static_cast<float *>(p)[row + at(j, e)] = v[e];
+                    *reinterpret_cast<float *>(q + at(j, e) * kBytes) = f[e];
                 else
-                    static_cast<uint16_t *>(p)[row + at(j, e)] = static_cast<uint16_t>(pack2<kType == MBERT_F16>(v[e], 0.f));
+                    *reinterpret_cast<uint16_t *>(q + at(j, e) * kBytes) =
+                        static_cast<uint16_t>(pack2<kType == MBERT_F16>(f[e], 0.f));
             }
+        }
+    }
+
+    // does every lane hold numbers of the row only?
+    __device__ bool full(int warps) const { return width == warps * 32 * kVecs * kN; }
+
+    // 0 behind the row's end
+    __device__ void clear_behind(int j, uint64_t (&v)[kPairs]) const
+    {
+        if constexpr (kVectors) {
+            if (!in(j, 0))
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e)
+                    v[e] = 0;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                float lo, hi;
+                f2_split(v[e], lo, hi);
+                v[e] = f2(in(j, 2 * e) ? lo : 0.f, in(j, 2 * e + 1) ? hi : 0.f);
+            }
+        }
+    }
+
+private:
+    template <typename F>
+    __device__ void single(int j, uint64_t (&v)[kPairs], F &&number) const
+    {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+            float lo = 0.f, hi = 0.f;
+            if (in(j, 2 * e))
+                lo = number(at(j, 2 * e) * kBytes);
+            if (in(j, 2 * e + 1))
+                hi = number(at(j, 2 * e + 1) * kBytes);
+            v[e] = f2(lo, hi);
         }
     }
 };
@@ -101,28 +206,41 @@ struct Row {
 // The lanes of a row: `lanes` of a warp, or `warps` whole warps of a block.
 struct Team {
     int lanes, warps;
-    float *scratch;     // [2][warps]
+    float *scratch;     // [2][32]
     int turn;
 
     template <typename Op>
-    __device__ float all(float v, Op op)
+    __device__ float all(float v, float none, Op op)
     {
-        for (int o = lanes >> 1; o > 0; o >>= 1)
-            v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if (lanes == 32) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+        } else {
+            for (int o = lanes >> 1; o > 0; o >>= 1)
+                v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+        }
         if (warps > 1) {
             // two places in turn, so that one barrier a sum will do
             float *s = scratch + (turn ^= 1) * 32;
-            if ((threadIdx.x & 31) == 0)
+            const int lane = threadIdx.x & 31;
+            if (lane == 0)
                 s[threadIdx.x >> 5] = v;
             __syncthreads();
-            v = s[0];
-            for (int w = 1; w < warps; ++w)
-                v = op(v, s[w]);
+            v = lane < warps ? s[lane] : none;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
         }
         return v;
     }
-    __device__ float sum(float v) { return all(v, [](float x, float y) { return x + y; }); }
-    __device__ float most(float v) { return all(v, [](float x, float y) { return fmaxf(x, y); }); }
+    __device__ float sum(uint64_t v)
+    {
+        float lo, hi;
+        f2_split(v, lo, hi);
+        return all(lo + hi, 0.f, [](float x, float y) { return x + y; });
+    }
+    __device__ float most(float v) { return all(v, 0.f, [](float x, float y) { return fmaxf(x, y); }); }
 };
 
 // v[] of a row -> its norm times w plus b.  Called by all lanes of a warp.
@@ -134,94 +252,160 @@ struct Team {
 // sum at most), are taken again of the row times a power of two that brings its
 // largest number to 1 .. 2, or as near as keeps eps times its square at 2^100.
 template <int kType, bool kVectors, int kVecs, bool kLayer>
-__device__ __forceinline__ void norm_row(const ResidualNormArgs &a, const Row<kType, kVectors> &at,
-                                         float (&v)[kVecs][Row<kType, kVectors>::kN], const void *w, const void *b,
-                                         Team &team)
+__device__ __forceinline__ void norm_row(const ResidualNormArgs &a, const Row<kType, kVectors, kVecs> &at,
+                                         uint64_t (&v)[kVecs][Row<kType, kVectors, kVecs>::kPairs], const void *w,
+                                         const void *b, Team &team)
 {
-    constexpr int kN = Row<kType, kVectors>::kN;
-    auto centre = [&](bool keep) {
-        float s = 0.f;
+    constexpr int kPairs = Row<kType, kVectors, kVecs>::kPairs;
+    auto each = [&](auto &&f) {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j)
 #pragma unroll
-            for (int e = 0; e < kN; ++e)
-                s = fmaf(v[j][e], a.sum_scale, s);
-        const float half_mean = team.sum(s) * a.half_mean_scale;
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-            for (int e = 0; e < kN; ++e)
-                if (!keep)
-                    v[j][e] = at.in(j, e) ? fmaf(v[j][e], 0.5f, -half_mean) : 0.f;
+            for (int e = 0; e < kPairs; ++e)
+                f(v[j][e]);
     };
-    auto squares = [&] {
-        float s = 0.f;
+    // two chains of sums
+    auto total = [&](auto &&f) {
+        uint64_t s[2] = {};
 #pragma unroll
         for (int j = 0; j < kVecs; ++j)
 #pragma unroll
-            for (int e = 0; e < kN; ++e)
-                s = fmaf(v[j][e], v[j][e], s);
-        return team.sum(s);
+            for (int e = 0; e < kPairs; ++e)
+                s[e & 1] = f(v[j][e], s[e & 1]);
+        return team.sum(fadd2p(s[0], s[1]));
     };
+    auto half_mean = [&] {
+        const uint64_t scale = bc2(a.sum_scale);
+        return total([&](uint64_t x, uint64_t s) { return ffma2(x, scale, s); }) * a.half_mean_scale;
+    };
+    auto centre = [&](float half, float mean) {
+        each([&](uint64_t &x) { x = ffma2(x, bc2(half), bc2(-mean)); });
+        if (!at.full(team.warps))
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                at.clear_behind(j, v[j]);
+    };
+    auto squares = [&] { return total([](uint64_t x, uint64_t s) { return ffma2(x, x, s); }); };
+    // the weights are on their way during the sums
+    constexpr bool kEarly = early(kVectors, kVecs * 2 * kPairs);
+    uint4 wr[kVectors ? kVecs : 1], br[kEarly ? kVecs : 1];
+    if constexpr (kVectors) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            wr[j] = at.load_raw(w, j);
+            if constexpr (kEarly)
+                br[j] = b ? at.load_raw(b, j) : make_uint4(0, 0, 0, 0);
+        }
+    }
     float eps = a.eps;
     if constexpr (kLayer) {
-        centre(false);
+        centre(0.5f, half_mean());
         eps *= 0.25f;
     }
     float q = squares();
     bool again = !(q >= a.least_squares && q <= 0x1p126f);      // (NaN too, which stay)
     if (__any_sync(0xffffffffu, again)) {
         float m = 0.f;
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-            for (int e = 0; e < kN; ++e)
-                m = fmaxf(m, fabsf(v[j][e]));
+        each([&](uint64_t &x) {
+            float lo, hi;
+            f2_split(x, lo, hi);
+            m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
+        });
         m = team.most(m);
         again = again && m > 0.f && m < INFINITY;
         const int k = min(127 - (__float_as_int(m) >> 23), a.most_scale);
         const float up = again ? __int_as_float((max(k, -126) + 127) << 23) : 1.f;
         eps = eps * up * up;
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-            for (int e = 0; e < kN; ++e)
-                v[j][e] *= up;
+        each([&](uint64_t &x) { x = fmul2(x, bc2(up)); });
         if constexpr (kLayer) {
-            centre(!again);
+            const float mean = half_mean();
+            centre(again ? 0.5f : 1.f, again ? mean : 0.f);
             eps *= again ? 0.25f : 1.f;
         }
         const float sum = squares();
         q = again ? sum : q;
     }
-    const float r = rsqrtf(fmaf(q, a.inv_width, eps));
+    const uint64_t r = bc2(rsqrtf(fmaf(q, a.inv_width, eps)));
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        float wv[kN];
-        at.load(w, 0, j, wv);
-#pragma unroll
-        for (int e = 0; e < kN; ++e)
-            v[j][e] = v[j][e] * r * wv[e];
+        uint64_t wv[kPairs], bv[kPairs];
+        if constexpr (kVectors)
+            at.unpack(wr[j], wv);
+        else
+            at.load(w, j, wv);
         if (b) {
-            at.load(b, 0, j, wv);
+            if constexpr (kEarly)
+                at.unpack(br[j], bv);
+            else
+                at.load(b, j, bv);
 #pragma unroll
-            for (int e = 0; e < kN; ++e)
-                v[j][e] += wv[e];
+            for (int e = 0; e < kPairs; ++e)
+                v[j][e] = ffma2(fmul2(v[j][e], r), wv[e], bv[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e)
+                v[j][e] = fmul2(fmul2(v[j][e], r), wv[e]);
         }
     }
 }
 
+// 16 bytes to shared memory, in the calling thread's current group of copies
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// all but the `n` newest groups have landed
+__device__ __forceinline__ void copy_wait(int n)
+{
+    switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+    }
+}
+
+// The sequence of row t: the last that begins there or before.  `seq` is the one of
+// an earlier row.
+__device__ __forceinline__ int sequence_of(const int32_t *cu, int n, long long t, int seq)
+{
+    if (seq + 1 >= n || cu[seq + 1] > t)
+        return seq;
+    int hi = n;
+    while (hi - seq > 1) {
+        const int mid = (seq + hi) >> 1;
+        (cu[mid] <= t ? seq : hi) = mid;
+    }
+    return seq;
+}
+
 // kVecs 16-byte vectors a lane.
 template <int kType, bool kVectors, int kVecs, bool kLayer>
-__global__ void __launch_bounds__(kMostThreads) residual_norm_kernel(const ResidualNormArgs a)
+__global__ void __maxnreg__(most_registers(kVectors, kVecs * (kType == MBERT_F32 ? 4 : 8), kType == MBERT_F32 ? 4 : 2))
+residual_norm_kernel(const ResidualNormArgs a)
 {
-    constexpr int kN = Row<kType, kVectors>::kN;
+    using At = Row<kType, kVectors, kVecs>;
+    constexpr int kPairs = At::kPairs, kBytes = At::kBytes;
+    constexpr bool kEarly = early(kVectors, kVecs * 2 * kPairs);
+    extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ float scratch[64];
     pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool one_warp = a.warps == 1;
     Team team{a.lanes, a.warps, scratch, 0};
-    // rows side by side in a block, this thread's place among them and in its row
-    const int step = a.lanes * a.warps, beside = blockDim.x / step;
-    const Row<kType, kVectors> at{static_cast<int>(threadIdx.x) % step, step, a.width};
+    // the crew: its rows side by side, this thread's row among them and place in the row
+    const int beside = 32 / a.lanes;
+    const At at(one_warp ? 0 : warp, lane & (a.lanes - 1), a.width);
+    const int mine = lane / a.lanes;
+
     bool bad = false;
     if (a.cu) {
         for (int g = threadIdx.x; g <= a.n_seqs; g += blockDim.x) {
@@ -233,95 +417,207 @@ __global__ void __launch_bounds__(kMostThreads) residual_norm_kernel(const Resid
         if (bad && blockIdx.x == 0 && threadIdx.x == 0)
             atomicOr(a.err, kErrBadCu);
     }
-    const long long rows = bad ? 0 : a.cu ? a.cu[a.n_seqs] : a.rows;
-    // (every thread makes the same rounds, so that its warp and block stay together)
-    for (long long t0 = static_cast<long long>(blockIdx.x) * beside; t0 < rows;
-         t0 += static_cast<long long>(gridDim.x) * beside) {
-        const long long row = t0 + threadIdx.x / step;
-        const bool on = row < rows;
-        const long long t = on ? row : rows - 1;
-        float h[kVecs][kN], v[kVecs][kN];
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-            at.load(a.x, t * a.x_row, j, h[j]);
-        if (a.branch) {
+    const unsigned rows = static_cast<unsigned>(bad ? 0 : a.cu ? a.cu[a.n_seqs] : a.rows);
+    // this thread's first row and the rows from round to round (a row and a stride stay
+    // below 2^32: there are at most 2^31 - 1024 rows, and a row for every lane)
+    const unsigned row0 = (one_warp ? blockIdx.x * kWarpCrews + warp : blockIdx.x) * beside;
+    const unsigned stride = (one_warp ? gridDim.x * kWarpCrews : gridDim.x) * beside;
+
+    // The ring: a slot holds the crew's rows of x, of the branch and of the gate.
+    const bool gate_rows = a.gate && !a.gate_channels;
+    const uint32_t tensor_bytes = beside * a.row_bytes, slot_bytes = a.tensors * tensor_bytes;
+    const uint32_t slot0 = smem_u32(smem_raw) + (one_warp ? warp * a.slots * slot_bytes : 0) + mine * a.row_bytes;
+    const uint32_t end = slot0 + a.slots * slot_bytes;
+    int seq = 0;
+    auto row_of = [&](const void *p, long long pitch, unsigned row) {
+        return static_cast<const char *>(p) + row * pitch * kBytes;
+    };
+    auto gate_of = [&](unsigned row, int &s) {
+        if (a.cu) {
+            s = sequence_of(a.cu, a.n_seqs, static_cast<int>(row), s);
+            row = s;
+        }
+        return row_of(a.gate, a.gate_row, row);
+    };
+    // Whole vectors: every thread copies the ones that it will read, so nothing but its
+    // own copies has to be waited for.  Single numbers: the crew copies the 16-byte pieces
+    // of memory that the row lies in (its neighbours' numbers at either end are not looked
+    // at), and waits for each other.
+    auto copy = [&](uint32_t dst, const char *p) {
+        if constexpr (kVectors) {
 #pragma unroll
             for (int j = 0; j < kVecs; ++j)
-                at.load(a.branch, t * a.branch_row, j, v[j]);
-            long long gate = t * a.gate_row;
-            if (a.cu) {
-                // the sequence of the row: the last that begins there or before
-                int lo = 0, hi = a.n_seqs;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    (a.cu[mid] <= t ? lo : hi) = mid;
-                }
-                gate = lo * a.gate_row;
-            }
-            if (a.after_weight)
-                norm_row<kType, kVectors, kVecs, kLayer>(a, at, v, a.after_weight, a.after_bias, team);
+                if (at.in(j, 0))
+                    copy_async(dst + (at.first + At::at(j, 0)) * kBytes, p + (at.first + At::at(j, 0)) * kBytes);
+        } else {
+            const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
+            const int pieces = (off + a.width * kBytes + 15) / 16;
+            for (int i = one_warp ? lane : threadIdx.x; i < pieces; i += 32 * a.warps)
+                copy_async(dst + 16 * i, p - off + 16 * i);
+        }
+    };
+    unsigned fill_row = row0 + mine;
+    uint32_t fill = slot0;
+    auto refill = [&] {
+        if (fill_row < rows) {
+            copy(fill, row_of(a.x, a.x_row, fill_row));
+            if (a.branch)
+                copy(fill + tensor_bytes, row_of(a.branch, a.branch_row, fill_row));
+            if (gate_rows)
+                copy(fill + 2 * tensor_bytes, gate_of(fill_row, seq));
+        }
+        copy_commit();      // one group a slot, if an empty one
+        fill_row += stride;
+        fill = fill + slot_bytes == end ? slot0 : fill + slot_bytes;
+    };
+    for (int s = 0; s < a.slots; ++s)
+        refill();
+
+    uint32_t from = slot0;
+    int read_seq = 0;
+    for (unsigned base = row0; base < rows; base += stride) {
+        const unsigned row = base + mine;
+        const bool on = row < rows;
+        copy_wait(a.slots - 1);
+        if constexpr (!kVectors)
+            one_warp ? __syncwarp() : __syncthreads();
+        uint64_t v[kVecs][kPairs];
+        // f(j, numbers) for the row at `p`, which is in the slot as tensor i
+        auto take = [&](int i, const char *p, auto &&f) {
+            uint64_t w[kPairs];
+            const uint32_t s = from + i * tensor_bytes + (kVectors ? 0 : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15));
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                if (a.gate) {
-                    float g[kN];
-                    at.load(a.gate, gate, j, g);
-#pragma unroll
-                    for (int e = 0; e < kN; ++e)
-                        v[j][e] *= g[e];
-                }
-#pragma unroll
-                for (int e = 0; e < kN; ++e)
-                    h[j][e] = fmaf(a.residual_scale, h[j][e], v[j][e]);
-                if (on)
-                    at.store(a.h, t * a.h_row, j, h[j]);
+                at.load_shared(s, j, w);
+                f(j, w);
             }
-        }
-        if (a.weight) {
-            norm_row<kType, kVectors, kVecs, kLayer>(a, at, h, a.weight, a.bias, team);
+        };
+        auto keep = [&](int j, const uint64_t (&w)[kPairs]) {
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e)
+                v[j][e] = w[e];
+        };
+        auto store = [&](void *p, long long pitch) {
+            if (!on)
+                return;
+            char *q = static_cast<char *>(p) + row * pitch * kBytes;
 #pragma unroll
             for (int j = 0; j < kVecs; ++j)
-                if (on)
-                    at.store(a.y, t * a.y_row, j, h[j]);
+                at.store(q, j, v[j]);
+        };
+        uint4 gr[kEarly ? kVecs : 1];
+        if constexpr (kEarly)
+            if (a.gate_channels)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+                    gr[j] = at.load_raw(a.gate, j);
+        if (a.branch) {
+            take(1, row_of(a.branch, a.branch_row, row), keep);
+            if (a.after_weight)
+                norm_row<kType, kVectors, kVecs, kLayer>(a, at, v, a.after_weight, a.after_bias, team);
+            auto times = [&](int j, const uint64_t (&w)[kPairs]) {
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e)
+                    v[j][e] = fmul2(v[j][e], w[e]);
+            };
+            if (gate_rows) {
+                take(2, kVectors ? nullptr : gate_of(on ? row : 0, read_seq), times);
+            } else if (a.gate) {
+                uint64_t w[kPairs];
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    if constexpr (kEarly)
+                        at.unpack(gr[j], w);
+                    else
+                        at.load(a.gate, j, w);
+                    times(j, w);
+                }
+            }
+            take(0, row_of(a.x, a.x_row, row), [&](int j, const uint64_t (&w)[kPairs]) {
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e)
+                    v[j][e] = ffma2(bc2(a.residual_scale), w[e], v[j][e]);
+            });
+        } else {
+            take(0, row_of(a.x, a.x_row, row), keep);
+        }
+        // the slot has been read: filled again
+        if constexpr (!kVectors)
+            one_warp ? __syncwarp() : __syncthreads();
+        refill();
+        from = from + slot_bytes == end ? slot0 : from + slot_bytes;
+        if (a.branch)
+            store(a.h, a.h_row);
+        if (a.weight) {
+            norm_row<kType, kVectors, kVecs, kLayer>(a, at, v, a.weight, a.bias, team);
+            store(a.y, a.y_row);
         }
     }
+    copy_wait(0);
     pdl_trigger();
 }
 
+// Shared memory of one SM for the rings: one slot of the widest rows at least.
+constexpr int kRingBytes = 200 * 1024;
+static_assert(3 * (kResidualNormMaxWidth * 4 + 30) <= kRingBytes, "a slot");
+
 template <int kType, bool kVectors, int kVecs, bool kLayer>
-cudaError_t launch(const ResidualNormArgs &a, int num_sms, cudaStream_t stream)
+cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
 {
     static PerDeviceOnce once;
-    const int step = a.lanes * a.warps;
-    const int threads = a.warps > 1 ? step : 256;
-    int fit = 0;
+    constexpr int kBytes = Row<kType, kVectors, kVecs>::kBytes;
     auto *kernel = residual_norm_kernel<kType, kVectors, kVecs, kLayer>;
+    int fit = 0;                                            // warps on one SM, by registers
     const cudaError_t e = per_device_once(once, &fit, [&](int *out) {
-        int regs = 0;
         cudaFuncAttributes f;
-        const cudaError_t r = cudaFuncGetAttributes(&f, kernel);
-        regs = f.numRegs > 0 ? f.numRegs : 64;
-        *out = 65536 / (32 * ((regs + 7) / 8 * 8));       // warps on one SM
+        cudaError_t r = cudaFuncGetAttributes(&f, kernel);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        *out = 65536 / (32 * ((f.numRegs > 0 ? f.numRegs + 7 : 64) / 8 * 8));
         return r;
     });
     if (e != cudaSuccess)
         return e;
-    const int beside = threads / step;
-    const long long need = (a.rows + beside - 1) / beside;
-    const int per_sm = fit * 32 / threads > 0 ? fit * 32 / threads : 1;
-    const long long most = static_cast<long long>(num_sms) * (per_sm < 2048 / threads ? per_sm : 2048 / threads);
-    return launch_chained(kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(threads), 0, stream, a);
+    const int crews = a.warps > 1 ? 1 : kWarpCrews, threads = 32 * (a.warps > 1 ? a.warps : kWarpCrews);
+    const int beside = 32 / a.lanes;
+    // a row, from and to 16 bytes
+    a.row_bytes = kVectors ? a.width * kBytes : (a.width * kBytes + 30) / 16 * 16;
+    a.tensors = a.gate && !a.gate_channels ? 3 : a.branch ? 2 : 1;
+    // two slots or more: the SM's blocks share the memory, fewer blocks where that does
+    // not do, and one slot where it does not do for a single block (rows of 48 KB or
+    // more from three tensors in fp32)
+    const int slot = crews * beside * a.row_bytes * a.tensors;
+    const int per_sm =
+        std::max(1, std::min(std::min(fit / (threads / 32), 2048 / threads), kRingBytes / (2 * slot)));
+    a.slots = std::min(kMostSlots, kRingBytes / (per_sm * slot));
+    const long long need = (a.rows + crews * beside - 1) / (crews * beside);
+    const long long most = static_cast<long long>(num_sms) * per_sm;
+    return launch_chained(kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(threads), a.slots * slot,
+                          stream, a);
 }
 
 template <int kType, bool kVectors, bool kLayer>
-cudaError_t launch(const ResidualNormArgs &a, int vecs, int num_sms, cudaStream_t stream)
+cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
 {
-    if constexpr (kType == MBERT_F32) {
-        if (vecs > 6)
+    constexpr int kN = Row<kType, kVectors, 1>::kN;
+    const int vecs = (a.width + kN - 1) / kN;           // of a row
+    // up to 32 lanes take a row (all 32 where they take single numbers), then more
+    // vectors each, then more warps
+    a.lanes = kVectors ? 1 : 32;
+    while (a.lanes < 32 && a.lanes < vecs)
+        a.lanes *= 2;
+    const int most = kVectors ? 8 : 32 / kN;            // vectors a lane in a crew of one warp
+    a.warps = vecs <= 32 * most ? 1 : std::min(kMostWarps, (a.width + 32 * kCrewNumbers - 1) / (32 * kCrewNumbers));
+    const int each = (vecs + a.lanes * a.warps - 1) / (a.lanes * a.warps);
+    if constexpr (kVectors || kN == 4) {
+        if (each > 6)
             return launch<kType, kVectors, 8, kLayer>(a, num_sms, stream);
-        if (vecs > 4)
+        if (each == 6)
             return launch<kType, kVectors, 6, kLayer>(a, num_sms, stream);
+        if (each == 5)
+            return launch<kType, kVectors, 5, kLayer>(a, num_sms, stream);
     }
-    switch (vecs) {
+    switch (each) {
     case 1: return launch<kType, kVectors, 1, kLayer>(a, num_sms, stream);
     case 2: return launch<kType, kVectors, 2, kLayer>(a, num_sms, stream);
     case 3: return launch<kType, kVectors, 3, kLayer>(a, num_sms, stream);
@@ -332,19 +628,9 @@ cudaError_t launch(const ResidualNormArgs &a, int vecs, int num_sms, cudaStream_
 template <int kType>
 cudaError_t launch(ResidualNormArgs &a, bool layer, int num_sms, cudaStream_t stream)
 {
-    constexpr int kN = Row<kType, true>::kN, kMost = kLaneNumbers / kN;
-    const int vecs = (a.width + kN - 1) / kN;           // of a row
-    // up to 32 lanes take a row, then more vectors each, then more warps
-    a.lanes = 1;
-    while (a.lanes < 32 && a.lanes < vecs)
-        a.lanes *= 2;
-    a.warps = (vecs + 32 * kMost - 1) / (32 * kMost);
-    const int step = a.lanes * a.warps, each = (vecs + step - 1) / step;
     if (a.vectors)
-        return layer ? launch<kType, true, true>(a, each, num_sms, stream)
-                     : launch<kType, true, false>(a, each, num_sms, stream);
-    return layer ? launch<kType, false, true>(a, each, num_sms, stream)
-                 : launch<kType, false, false>(a, each, num_sms, stream);
+        return layer ? launch<kType, true, true>(a, num_sms, stream) : launch<kType, true, false>(a, num_sms, stream);
+    return layer ? launch<kType, false, true>(a, num_sms, stream) : launch<kType, false, false>(a, num_sms, stream);
 }
 
 }  // namespace

@@ -28,8 +28,10 @@ struct ResidualNormArgs {
     float least_squares = 0.f;
     int most_scale = 0;
     int32_t *err = nullptr;
-    // set by the launcher: lanes of a row, or warps of 32
-    int lanes = 32, warps = 1;
+    int gate_channels = 0;              // one gate for all rows
+    // set by the launcher: lanes of a row, or warps of 32; the ring's slots, a row's bytes
+    // there, the tensors whose rows a slot holds
+    int lanes = 32, warps = 1, slots = 1, row_bytes = 0, tensors = 1;
 };
 
 cudaError_t launch_residual_norm(ResidualNormArgs &a, int dtype, bool layer, int num_sms, cudaStream_t stream);
