@@ -179,6 +179,12 @@ def _layout(*tensors):
     return tuple([(t.shape, t.stride(), t.dtype, t.device) for t in tensors])
 
 
+def _key(t):
+    """One tensor's part of such a look, with the device as a number (-1 for the
+    host): cheaper to make and to compare."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
 _INT_MAX = 2 ** 31 - 1
 
 
@@ -768,12 +774,10 @@ class Attention:
         out = residual + act(x Wg^T + bg) * (x Wu^T + bu).  `out` may be
         `residual` itself.  Rows may be strided; those of x and weight start at
         16-byte boundaries (K a multiple of 8 where they are contiguous)."""
-        gated = bool(gated)
-        key = ("linear", _layout(x, weight), None if bias is None else _layout(bias), activation, gated,
-               None if residual is None else _layout(residual), None if out is None else _layout(out))
+        key = ("linear", activation, bool(gated), _key(x), _key(weight), _key(bias), _key(residual), _key(out))
         known = self._known.get(key)
         if known is None:
-            known = self._linear_known(key, x, weight, None, bias, activation, gated, residual, None, out)
+            known = self._linear_known(key, x, weight, None, bias, activation, bool(gated), residual, None, out)
         return self._linear(known, "linear", x, weight, bias, residual, out)
 
     def expert_linear(self, x: torch.Tensor, weight: torch.Tensor, cu_experts: torch.Tensor,
@@ -785,16 +789,15 @@ class Attention:
         result is multiplied by row_scale[t] (fp32, a router's weight).  Empty
         groups are allowed; rows of out behind the last group are left as they
         were."""
-        gated = bool(gated)
-        key = ("expert_linear", _layout(x, weight, cu_experts), None if bias is None else _layout(bias), activation,
-               gated, None if row_scale is None else _layout(row_scale), None if out is None else _layout(out))
+        key = ("expert_linear", activation, bool(gated), _key(x), _key(weight), _key(cu_experts), _key(bias),
+               _key(row_scale), _key(out))
         known = self._known.get(key)
         if known is None:
             self._check_cu(cu_experts)
             experts = cu_experts.numel() - 1
             if experts < 1:
                 raise ValueError("cu_experts must name at least one expert")
-            known = self._linear_known(key, x, weight, experts, bias, activation, gated, None, row_scale, out)
+            known = self._linear_known(key, x, weight, experts, bias, activation, bool(gated), None, row_scale, out)
         return self._linear(known, "expert_linear", x, weight, bias, None, out, cu_experts, row_scale)
 
     def residual_norm(self, x: torch.Tensor, branch: torch.Tensor = None, weight: torch.Tensor = None,
@@ -814,12 +817,12 @@ class Attention:
         if norm not in _NORMS:
             raise ValueError(f"norm must be 'rms' or 'layer', not {norm!r}")
         residual_scale, eps = float(residual_scale), float(eps)
-        given = (x, branch, weight, bias, branch_weight, branch_bias, gate, cu_seqlens, h_out, y_out)
-        key = ("residual_norm", tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in given]),
-               norm, residual_scale, eps)
+        key = ("residual_norm", norm, residual_scale, eps, _key(x), _key(branch), _key(weight), _key(bias),
+               _key(branch_weight), _key(branch_bias), _key(gate), _key(cu_seqlens), _key(h_out), _key(y_out))
         known = self._known.get(key)
         if known is None:
-            known = self._residual_norm_known(key, *given, norm, residual_scale, eps)
+            known = self._residual_norm_known(key, x, branch, weight, bias, branch_weight, branch_bias, gate, cu_seqlens,
+                                              h_out, y_out, norm, residual_scale, eps)
         args = ResidualNormArgs.from_buffer_copy(known)
         args.x = x.data_ptr()
         h, y = x, None
@@ -937,6 +940,17 @@ def _default(device) -> Attention:
     return h
 
 
+def _of(x) -> Attention:
+    """The handle of a tensor's device."""
+    idx = x.get_device()
+    h = _handles.get(idx)
+    if h is None:
+        if not x.is_cuda:
+            raise ValueError("x must be a CUDA tensor")
+        h = _default(x.device)
+    return h
+
+
 def attention(qkv: torch.Tensor, cu_seqlens: torch.Tensor, layer_kind, max_seqlen: int = 0,
               out: torch.Tensor = None) -> torch.Tensor:
     """ModernBERT-base attention for one layer: qkv[T,2304] bf16 (CUDA),
@@ -1034,9 +1048,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor = None, act
            gated: bool = False, residual: torch.Tensor = None, out: torch.Tensor = None) -> torch.Tensor:
     """out = residual + act(x weight^T + bias), or gated, of any width (CUDA, bf16
     or fp16): Attention.linear on the device's handle."""
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    return _default(x.device).linear(x, weight, bias, activation, gated, residual, out)
+    return _of(x).linear(x, weight, bias, activation, gated, residual, out)
 
 
 def expert_linear(x: torch.Tensor, weight: torch.Tensor, cu_experts: torch.Tensor, bias: torch.Tensor = None,
@@ -1044,9 +1056,7 @@ def expert_linear(x: torch.Tensor, weight: torch.Tensor, cu_experts: torch.Tenso
                   out: torch.Tensor = None) -> torch.Tensor:
     """linear with a weight for each group of rows: Attention.expert_linear on the
     device's handle."""
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    return _default(x.device).expert_linear(x, weight, cu_experts, bias, activation, gated, row_scale, out)
+    return _of(x).expert_linear(x, weight, cu_experts, bias, activation, gated, row_scale, out)
 
 
 def residual_norm(x: torch.Tensor, branch: torch.Tensor = None, weight: torch.Tensor = None,
@@ -1056,7 +1066,5 @@ def residual_norm(x: torch.Tensor, branch: torch.Tensor = None, weight: torch.Te
                   y_out: torch.Tensor = None):
     """(h, y): the residual stream behind a block and its norm for the next one:
     Attention.residual_norm on the device's handle."""
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    return _default(x.device).residual_norm(x, branch, weight, bias, branch_weight, branch_bias, gate, cu_seqlens,
+    return _of(x).residual_norm(x, branch, weight, bias, branch_weight, branch_bias, gate, cu_seqlens,
                                             norm, residual_scale, eps, h_out, y_out)

@@ -10,6 +10,7 @@
 
 #include "mbert_attn.h"
 #include "internal.h"
+#include "linear.h"
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -66,6 +67,7 @@ struct mbert_attn {
     };
     MapEntry maps[32];
     uint64_t map_clock = 0;
+    mbert::PlanEntry plans[64];             // of products of any width, by their sizes
 };
 
 namespace mbert {

@@ -2,6 +2,7 @@
 // checks, tensor maps, the choice of the kernel.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "mbert_attn.h"
 #include "common.cuh"
@@ -76,13 +77,21 @@ int encode_groups(const mbert_attn *h, CUtensorMap *tm, const void *p, int64_t i
     return r == CUDA_SUCCESS ? MBERT_OK : MBERT_ERR_CUDA;
 }
 
-// How a product runs: the kernel, its tiles, an upper bound on its units.
-struct LinearPlan {
-    bool rows;          // the kernel for few rows
-    int tile;           // rows of its tile; else accumulator columns of the pair kernel
-    int split;          // CTAs that share the inner dimension
-    int64_t units;
-};
+// 2-D map of 16-bit elements over [rows][width] for the staging buffers of linear.cu:
+// box 64 x 32 with the 128-byte swizzle or 32 x 32 with the 64-byte one.
+int encode_chunks(const mbert_attn *h, CUtensorMap *tm, const void *p, int64_t width, int64_t rows, int64_t pitch,
+                  int chunk)
+{
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+    const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(chunk), 32};
+    const cuuint32_t ones[2] = {1, 1};
+    const CUresult r = h->encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, boxes,
+                                 ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                 chunk == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MBERT_OK : MBERT_ERR_CUDA;
+}
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -94,32 +103,134 @@ int64_t block_bound(const mbert_attn_linear_args &c, int rows)
     return std::min<int64_t>(c.rows, c.rows / rows + c.experts);
 }
 
-LinearPlan linear_plan(const mbert_attn *h, const mbert_attn_linear_args &c)
+// What a product takes, in clocks of an SM: estimates from measured calls (a few rows to
+// 2048 by 768 to 8192, 8 to 64 experts), good for the choice between kernels and
+// tiles and no more: over 102 sizes the chosen one took 4 % longer than the best of
+// all.  (Kernel for few rows against that for many, us: 128 x 4096 -> 512 9.2 / 19.0, 300 x
+// 768 -> 2304 8.9 / 9.7, 1024 x 1024 -> 8192 26.8 / 20.5; 500 rows of 16 experts, 768 -> 2304,
+// 15.8 / 26.3, 2000 rows of 2, 1024 -> 8192, 70 / 70; tiles of 64 against 128 rows, 500 rows of
+// 16 experts, 4096 -> 2 x 512, 48 / 32.)
+struct Cost {
+    double clocks;
+    LinearPlan plan;
+};
+
+// Does the activation go without exponentials?
+bool plain(const mbert_attn_linear_args &c)
 {
-    LinearPlan p;
-    const int64_t groups = std::max(c.experts, 1);
-    const int64_t mean = ceil_div(c.rows, groups);      // rows of a group
-    p.split = 1;
-    p.rows = mean <= 128;
-    if (p.rows) {
-        const int64_t want = c.experts == 0 ? mean : 2 * mean;
-        p.tile = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
-        p.units = block_bound(c, p.tile) * ceil_div(c.outer, kLinearRowsColumns);
-        const int64_t places = static_cast<int64_t>(h->num_sms) * linear_rows_ctas(p.tile, c.gated);
-        const int64_t steps = ceil_div(c.inner, 64);
-        while (p.split < linear_rows_most_split(p.tile, c.gated) && 2 * p.split <= steps &&
-               p.units * p.split * 2 <= places)
-            p.split *= 2;
-        return p;
-    }
-    const int64_t pairs = h->num_sms / 2;
-    p.tile = 256;
-    p.units = block_bound(c, kLinearRows) * ceil_div(c.outer, c.gated ? 128 : 256);
-    if (p.units <= pairs / 2) {
-        p.tile = 128;
-        p.units = block_bound(c, kLinearRows) * ceil_div(c.outer, c.gated ? 64 : 128);
-    }
+    return c.activation == MBERT_ACT_NONE || c.activation == MBERT_ACT_RELU;
+}
+
+// The row tiles that groups of about the same size make.
+int64_t tile_estimate(const mbert_attn_linear_args &c, int rows)
+{
+    if (c.experts == 0)
+        return ceil_div(c.rows, rows);
+    const int64_t groups = std::min<int64_t>(c.experts, c.rows);
+    return std::max(groups, c.rows / rows + groups / 2);
+}
+
+// The kernel for few rows with tiles of `tile`, its best pieces and split: a step takes
+// what its bytes take at 60 a clock, its MMAs (which read 4 KB of weights and the rows
+// each), or what a warp needs from step to step, 330; 32 rows of an epilogue 1300, 2300 with
+// exponentials; a cluster's exchange of sums 2000 and its bytes at 8 a clock.
+Cost rows_cost(const mbert_attn *h, const mbert_attn_linear_args &c, int tile)
+{
+    Cost best{1e300, {}};
+    const bool gated = c.gated;
+    const int64_t bound = block_bound(c, tile), tiles = tile_estimate(c, tile);
+    const int64_t granules = ceil_div(c.outer, kLinearGranule), steps = ceil_div(c.inner, 64);
+    const int64_t places = static_cast<int64_t>(h->num_sms) * linear_rows_ctas(tile, gated);
+    const double sides = gated ? 2 : 1, mma = 4 * sides * (32 + tile / 4.0);
+    const double epilogue = (plain(c) ? 1300.0 : 2300.0) * (gated ? 1.3 : 1.0) * ceil_div(tile, 32);
+    // every row tile reads its group's weights, from memory or from L2, at 2850 a clock
+    const double traffic = static_cast<double>(tiles) * c.outer * sides * c.inner * 2 / 2850;
+    auto consider = [&](int m, int split, bool whole) {
+        const int64_t pieces = ceil_div(granules, m), ctas = split > 1 ? bound * pieces : std::min(places, bound * (whole ? pieces : granules));
+        // clusters fit where their SMs lie together, which leaves some idle
+        if (split > 1 && (10 * ctas * split > 8 * places || linear_rows_stages(tile, gated, m, split) < 3))
+            return;
+        // pieces of a CTA (a run of granules may begin and end within a row tile)
+        const int64_t runs = split > 1 ? 1 : whole ? ceil_div(tiles * pieces, ctas) : ceil_div(ceil_div(tiles * granules, ctas), m) + 1;
+        const int64_t share = std::max<int64_t>(1, ceil_div(std::min(ctas, tiles * pieces) * split, h->num_sms));
+        const double step = std::max(330.0, share * std::max(mma, (tile * 128 + sides * m * 4096) / 60.0));
+        const double work = runs * std::max(ceil_div(steps, split) * step, epilogue) + epilogue;
+        const double clocks = 9500 + std::max(traffic, work) + 0.3 * std::min(traffic, work) +
+                              (split > 1 ? 2000 + linear_rows_parts(tile, gated, m, split) / 8.0 : 0.0);
+        if (clocks < best.clocks) {
+            best.clocks = clocks;
+            best.plan.few = true;
+            best.plan.rows = {tile, m, split, whole, ctas};
+            best.plan.units = bound * granules;
+        }
+    };
+    for (int m = 1; m <= kLinearGranules; ++m)
+        for (int split = 1; split <= 8 && split <= steps; split *= 2)
+            consider(m, split, true);
+    if (bound * granules >= 2 * kLinearGranules * places)
+        consider(kLinearGranules, 1, false);
+    return best;
+}
+
+// The kernel for many rows: a step of 256 x 256 takes 600 clocks, one of 256 x 128 450; an
+// epilogue 5000 (gated 3700, for half the columns), an activation that computes
+// exponentials 3700 (2100) more, ragged groups 1000; 256 x 128 a little over half of it.
+Cost pair_cost(const mbert_attn *h, const mbert_attn_linear_args &c, int columns)
+{
+    Cost p{};
+    const int64_t across = ceil_div(c.outer, c.gated ? columns / 2 : columns);
+    const int64_t waves = ceil_div(tile_estimate(c, kLinearRows) * across, h->num_sms / 2);
+    const double epilogue = (columns == 256 ? 1.0 : 0.56) *
+        ((c.gated ? 3700 : 5000) + (plain(c) ? 0 : c.gated ? 2100 : 3700) + (c.experts > 0 ? 1000 : 0));
+    // weights that few rows meet come at 1750 a clock
+    const double fetch = static_cast<double>(std::max<int64_t>(1, std::min<int64_t>(c.experts, c.rows))) * c.outer *
+                         (c.gated ? 2 : 1) * c.inner * 2 / 1750;
+    p.clocks = 9900 + std::max(fetch, waves * std::max<double>(ceil_div(c.inner, 64) * (columns == 256 ? 600 : 450), epilogue)) +
+               epilogue;
+    p.plan.columns = columns;
+    p.plan.units = block_bound(c, kLinearRows) * across;
     return p;
+}
+
+LinearPlan make_plan(const mbert_attn *h, const mbert_attn_linear_args &c)
+{
+    Cost best = pair_cost(h, c, 256);
+    auto consider = [&](const Cost &o) {
+        if (o.clocks < best.clocks)
+            best = o;
+    };
+    consider(pair_cost(h, c, 128));
+    const int64_t mean = ceil_div(c.rows, std::max(c.experts, 1));
+    if (mean <= 2048) {
+        // tiles that a group of the mean size fills, smaller and larger ones
+        int tile = 16;
+        while (tile < 128 && tile < mean)
+            tile *= 2;
+        consider(rows_cost(h, c, tile));
+        if (tile < 128)
+            consider(rows_cost(h, c, 2 * tile));
+        if (tile > 16)
+            consider(rows_cost(h, c, tile / 2));
+    }
+    return best.plan;
+}
+
+// The plan of a call; that of one like an earlier one is found again (weighing takes
+// microseconds, as long as a short kernel).
+LinearPlan linear_plan(mbert_attn *h, const mbert_attn_linear_args &c)
+{
+    const int64_t key[4] = {c.rows, static_cast<int64_t>(c.inner) << 32 | c.outer, c.experts,
+                            c.activation * 2 + c.gated};
+    uint64_t x = 0;
+    for (const int64_t k : key)
+        x = (x ^ static_cast<uint64_t>(k)) * 0x9E3779B97F4A7C15ull;
+    mbert::PlanEntry &e = h->plans[x >> 58];
+    if (!e.known || std::memcmp(e.key, key, sizeof key) != 0) {
+        e.plan = make_plan(h, c);
+        std::memcpy(e.key, key, sizeof key);
+        e.known = true;
+    }
+    return e.plan;
 }
 
 }  // namespace
@@ -168,17 +279,23 @@ MBERT_API int mbert_attn_linear(mbert_attn *h, const mbert_attn_linear_args *arg
     // a dimension of one element has no stride that matters; a map wants one all the same
     auto pitch = [](int64_t rows, int64_t given, int64_t w) { return rows > 1 ? given : (w + 7) / 8 * 8; };
     const int64_t wrow = pitch(width, c.weight_row, c.inner);
-    const int xbox = p.rows ? p.tile : kLinearRows / 2, wbox = p.rows ? kLinearRowsColumns : p.tile / 2;
+    const int xbox = p.few ? p.rows.tile : kLinearRows / 2, wbox = p.few ? kLinearGranule * p.rows.granules : p.columns / 2;
     if (encode_rows(h, &a.tm_x, c.x, c.inner, c.rows, pitch(c.rows, c.x_row, c.inner), xbox, 256) != MBERT_OK ||
         encode_groups(h, &a.tm_w, c.weight, c.inner, width, groups, wrow, groups > 1 ? c.weight_expert : width * wrow,
-                      wbox) != MBERT_OK)
+                      wbox) != MBERT_OK ||
+        (p.few && p.rows.granules > 1 &&
+         encode_groups(h, &a.tm_granule, c.weight, c.inner, width, groups, wrow,
+                       groups > 1 ? c.weight_expert : width * wrow, kLinearGranule) != MBERT_OK))
         return MBERT_ERR_CUDA;
-    a.out_tma = !p.rows && out.aligned(16);
-    a.residual_tma = !p.rows && c.residual && residual.aligned(16);
-    if ((a.out_tma && encode_rows(h, &a.tm_out, c.out, c.outer, c.rows, pitch(c.rows, c.out_row, c.outer), 32, 256) !=
+    a.out_vectors = out.aligned(16);
+    a.out_bytes = out.aligned(8) ? 8 : out.aligned(4) ? 4 : 2;
+    a.residual_bytes = residual.aligned(8) ? 8 : residual.aligned(4) ? 4 : 2;
+    a.residual_vectors = c.residual && residual.aligned(16);
+    const int chunk = linear_chunk(c.gated);
+    if ((a.out_vectors && !p.few && encode_chunks(h, &a.tm_out, c.out, c.outer, c.rows, pitch(c.rows, c.out_row, c.outer), chunk) !=
                           MBERT_OK) ||
-        (a.residual_tma && encode_rows(h, &a.tm_residual, c.residual, c.outer, c.rows,
-                                       pitch(c.rows, c.residual_row, c.outer), 32, 256) != MBERT_OK))
+        (a.residual_vectors && !p.few && encode_chunks(h, &a.tm_residual, c.residual, c.outer, c.rows,
+                                         pitch(c.rows, c.residual_row, c.outer), chunk) != MBERT_OK))
         return MBERT_ERR_CUDA;
     a.bias = c.bias;
     a.residual = c.residual;
@@ -196,8 +313,8 @@ MBERT_API int mbert_attn_linear(mbert_attn *h, const mbert_attn_linear_args *arg
     a.err = h->err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool half = c.dtype == MBERT_F16;
-    const cudaError_t e = p.rows ? launch_linear_rows(a, p.tile, p.split, c.gated, half, p.units, h->num_sms, st)
-                                 : launch_linear(a, p.tile, c.gated, half, p.units, h->num_sms, st);
+    const cudaError_t e = p.few ? launch_linear_rows(a, p.rows, c.gated, half, st)
+                                : launch_linear(a, p.columns, c.gated, half, p.units, h->num_sms, st);
     h->launches += 1;
     return e == cudaSuccess ? MBERT_OK : MBERT_ERR_CUDA;
 }

@@ -17,13 +17,14 @@ namespace mbert {
 struct Unit {
     int group, column;          // group, block of columns
     long long row, end;         // first row, the group's end
+    bool first;                 // the group's first rows
 };
 
 // The units of a call in order.  Within a group they go by bands of `band` row
 // blocks, column after column of a band, so that the units that run at the same
 // time share rows and weights in L2.  Offsets are read as the walk comes to
-// them, 32 groups at a time, one a lane, so any number of groups will do and no
-// kernel has to write a list first.
+// them, 128 groups at a time, four a lane, so any number of groups will do and no kernel
+// has to write a list first.
 class UnitWalk {
 public:
     __device__ UnitWalk(const LinearArgs &a, int block, int columns, int band)
@@ -49,15 +50,28 @@ public:
             const int last = __shfl_sync(0xffffffffu, upto_, 31);
             if (u < last)
                 break;
-            if (first_ + 32 >= groups_)
+            if (first_ + kWindow >= groups_)
                 return false;
-            window(first_ + 32, last);
+            window(first_ + kWindow, last);
         }
+        // the lane whose groups hold the unit, and the group
         const int l = __ffs(__ballot_sync(0xffffffffu, u < upto_)) - 1;
-        const int row = __shfl_sync(0xffffffffu, row_, l), n = __shfl_sync(0xffffffffu, n_, l);
-        const int blocks = (n + block_ - 1) / block_;
-        out.group = first_ + l;
-        place(u - (__shfl_sync(0xffffffffu, upto_, l) - blocks * columns_), blocks, row, row + static_cast<long long>(n), out);
+        int at = __shfl_sync(0xffffffffu, upto_ - units_, l), g = first_ + l * kPerLane, row = 0, end = 0;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            const int x = __shfl_sync(0xffffffffu, cut_[i], l), y = __shfl_sync(0xffffffffu, cut_[i + 1], l);
+            const int n = (y - x + block_ - 1) / block_ * columns_;
+            if (!found && u < at + n) {
+                found = true;
+                g += i;
+                row = x;
+                end = y;
+            }
+            at += found ? 0 : n;
+        }
+        out.group = g;
+        place(u - at, (end - row + block_ - 1) / block_, row, end, out);
         return true;
     }
 
@@ -74,19 +88,22 @@ private:
         r = b * band_ + i - out.column * h;
         out.row = row + static_cast<long long>(r) * block_;
         out.end = end;
+        out.first = r == 0;
     }
 
-    // groups first .. first + 31, whose units begin at `before`
+    // groups first .. first + 127, whose units begin at `before`
     __device__ void window(int first, int before)
     {
-        const int lane = threadIdx.x & 31, g = first + lane;
+        const int lane = threadIdx.x & 31, g = first + lane * kPerLane;
         first_ = first;
-        row_ = n_ = 0;
-        if (g < groups_) {
-            row_ = cu_[g];
-            n_ = cu_[g + 1] - row_;
-        }
-        upto_ = (n_ + block_ - 1) / block_ * columns_;
+#pragma unroll
+        for (int i = 0; i <= kPerLane; ++i)
+            cut_[i] = cu_[min(g + i, groups_)];
+        units_ = 0;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+            units_ += (cut_[i + 1] - cut_[i] + block_ - 1) / block_ * columns_;
+        upto_ = units_;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, upto_, o);
@@ -95,13 +112,37 @@ private:
         upto_ += before;
     }
 
+    static constexpr int kPerLane = 4, kWindow = 32 * kPerLane;
     const int32_t *cu_;
     int groups_;
     long long rows_;
     int block_, columns_, band_;
     int first_ = 0;
-    int row_ = 0, n_ = 0, upto_ = 0;    // this lane's group: first row, rows, units up to its end
+    // this lane's groups: where they begin and end, their units, the units up to their end
+    int cut_[kPerLane + 1] = {}, units_ = 0, upto_ = 0;
 };
+
+// The units of a call, of `columns` a block of rows; -1 if the groups' offsets are not in
+// order and within the rows (reported once).  Called by all lanes of a warp.
+__device__ __forceinline__ long long count_units(const LinearArgs &a, int block, int columns)
+{
+    if (!a.cu)
+        return (a.rows + block - 1) / block * columns;
+    long long n = 0;
+    bool bad = false;
+    for (int g = threadIdx.x & 31; g < a.groups; g += 32) {
+        const int x = a.cu[g], y = a.cu[g + 1];
+        bad |= y < x || (g == 0 && x != 0) || (g == a.groups - 1 && y > a.rows);
+        n += (static_cast<long long>(y) - x + block - 1) / block;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad && blockIdx.x == 0 && (threadIdx.x & 31) == 0)
+        atomicOr(a.err, kErrBadCu);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    return bad ? -1 : n * columns;
+}
 
 // Are the groups' offsets in order and within the rows?  Called by all threads
 // of a block; a bad list is reported once, and the kernel then writes nothing.
@@ -159,8 +200,9 @@ __device__ __forceinline__ uint64_t bc2(float x) { return f2(x, x); }
 // 5.3e-6 on 0 .. 8 (least squares on Chebyshev points, reweighted until the errors
 // were even); beyond, its value at 8 is taken, where q < 7e-16.  Together 1e-5 of the
 // result (a half step of fp16 is 4.9e-4 of it), negative z included, where
-// 1 + erf would cancel; one exponential and 10 instructions a number against 25
-// for erff.
+// 1 + erf would cancel; one exponential and about 10 instructions a number against 25
+// for erff.  (On single numbers instead of pairs 358 us against 331, 32768 x 1024 ->
+// 8192.)
 __device__ __forceinline__ uint64_t gelu2(uint64_t z)
 {
     float a, b;

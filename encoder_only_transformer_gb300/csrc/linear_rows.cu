@@ -4,19 +4,30 @@
 // Bound by the weights, which are read once: 2 N K bytes against 2 T N K operations.
 // So the operands change places: D^T = W x^T with 128 weight rows as M and 16 to 128
 // rows of x as N, which wastes little of an MMA on rows that are not there, and the
-// bytes of W are spread over all SMs:
-//  * one CTA per 128 output columns (and `tile` rows of x), one or two CTAs an SM,
-//    so that 90 KB or more of weights are on their way to each SM;
-//  * where that leaves SMs idle, the inner dimension is cut among 2, 4 or 8 CTAs of
-//    a cluster.  Each writes its sums into the others' shared memory, rows of x dealt
-//    out among them, and each adds up its rows' parts in the order of the CTAs: the
-//    result does not depend on timing, and there is no second kernel and no workspace.
+// bytes of W are spread evenly over the SMs:
+//  * output columns go by granules of 32.  All granules, row tile after row tile and
+//    group after group, are dealt out to the CTAs (one or two an SM) in even runs, which
+//    a CTA takes in pieces of up to 4 granules (or, where a CTA has few, whole pieces are
+//    dealt out): a whole piece comes as one box, a shorter one as a box a granule.  An MMA
+//    of fewer than 4 leaves the rest of its 128 rows to whatever shared memory holds
+//    behind them, and nobody reads those.  (24 rows, 768 -> 50368 bf16: 16.2 us, 4.9 TB/s;
+//    units of 128 columns in turn 18.4.)
+//  * where there are too few columns to fill the SMs, the inner dimension is cut among 2,
+//    4 or 8 CTAs of a cluster.  Each writes its sums into the others' shared memory, rows
+//    of x dealt out among them, and each adds up its rows' parts in the order of the
+//    CTAs: the result does not depend on timing, and there is no second kernel and no
+//    workspace.
+//  * stages of the ring are as large as the call's pieces, so that short pieces do not
+//    leave the SM waiting for a few bytes at a time.
 // Roles: warp 0 producer (TMA, a ring of stages of 64 numbers of K), warp 1 MMA
-// issuer, warps 2 - 5 epilogue, one output column per thread, the rows one after
-// another: a warp writes 64 bytes of a row at a time.
-// Without a cut the CTAs are persistent, with two accumulators in turn.  Within a
-// group the units go column by column with the row tiles inside, so a weight tile that
-// several row tiles need is read from L2.
+// issuer, warps 2 - 9 epilogue, one output column per thread and 16 rows at a time, which
+// a warp writes as whole vectors through a tile of its own in shared memory (four warps
+// that wrote number by number took 10 us for 128 rows).  Two accumulators in turn.
+// 4001 rows of 64 experts, 768 -> 2 x 1152 fp16 with SiLU and biases: 44 us (242 MB, 5.5
+// TB/s) against 63 with those four warps and 68 by linear.cu.
+// What bounds short calls: a warp needs 330 clocks from one step to the next, whatever
+// it loads or multiplies (half of the MMAs, or one load for two, change nothing, nor do
+// more warps that load), and a call 5 us beside its steps.
 #include "linear.cuh"
 #include "internal.h"
 #include "pair.cuh"
@@ -24,40 +35,56 @@
 namespace mbert {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kEpiThreads = 128;
-constexpr int kM = kLinearRowsColumns;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kM = kLinearGranule * kLinearGranules;
 constexpr int kBK = 64;
-constexpr uint32_t kWBytes = kM * kBK * 2;
+constexpr uint32_t kGranuleBytes = kLinearGranule * kBK * 2;
+constexpr int kMostStages = kLinearRowsStages;
+constexpr int kBlock = 16;              // rows of x that an epilogue warp takes at a time
+static_assert(kLinearGranule == 32, "a warp's columns");
 
 template <int kNB, bool kGated>
 struct Layout {
     static constexpr int kSides = kGated ? 2 : 1;
-    static constexpr uint32_t kStageBytes = kSides * kWBytes + kNB * kBK * 2;
+    static constexpr uint32_t kXBytes = kNB * kBK * 2;
     static constexpr int kCtas = linear_rows_ctas(kNB, kGated);
-    // two CTAs: up to 108 KB each; one: up to 192 KB
-    static constexpr int kStages = kCtas == 2 ? 108 * 1024 / kStageBytes : kNB == 64 ? 4 : 192 * 1024 / kStageBytes;
-    static constexpr uint32_t kOffBar = kStages * kStageBytes;
-    static constexpr uint32_t kOffParts = kOffBar + 256;
-    // with a cut: every CTA's sums of this CTA's share of the rows
-    static constexpr uint32_t kPartsBytes = kSides * kNB * kM * 4;
-    static constexpr uint32_t smem(int split) { return kOffParts + (split > 1 ? kPartsBytes : 0) + 1024; }
     static constexpr uint32_t kTmemCols = 2 * kSides * kNB;
-    static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2,
+    // shared memory: barriers, the epilogue warps' tiles of 16 rows x 32 results, the sums
+    // that a cluster's CTAs exchange, the ring (x, then the granules of each side), and as
+    // much behind it as an MMA reads beyond its piece
+    static constexpr uint32_t kOffTiles = 1024, kTileBytes = kBlock * kLinearGranule * 2;
+    static constexpr uint32_t kOffParts = kOffTiles + kEpiWarps * kTileBytes;
+    static_assert(kOffParts + 1024 == kLinearRowsFixed, "shared memory");
+    static constexpr uint32_t parts_bytes(int granules, int split)
+    {
+        return linear_rows_parts(kNB, kGated, granules, split);
+    }
+    static constexpr uint32_t stage_bytes(int granules) { return linear_rows_stage(kNB, kGated, granules); }
+    static constexpr uint32_t behind(int granules) { return (kLinearGranules - granules) * kGranuleBytes; }
+    static constexpr int stages(int granules, int split) { return linear_rows_stages(kNB, kGated, granules, split); }
+    static constexpr uint32_t smem(int granules, int split)
+    {
+        return kLinearRowsFixed + parts_bytes(granules, split) + stages(granules, split) * stage_bytes(granules) +
+               behind(granules);
+    }
+    static constexpr int kFull = 0, kEmpty = kMostStages, kAccFull = 2 * kMostStages, kAccEmpty = kAccFull + 2,
                          kBars = kAccEmpty + 2;
-    static_assert(8 * kBars <= 256 && smem(linear_rows_most_split(kNB, kGated)) + 16 <= 227 * 1024, "shared memory");
-    static_assert(kCtas * (smem(1) + 1040) <= 228 * 1024 && kCtas * kTmemCols <= 512, "CTAs on one SM");
+    static_assert(8 * kBars <= kOffTiles, "barriers");
+    static_assert(stages(kLinearGranules, 1) >= 2 && kCtas * (linear_rows_budget(kNB, kGated) + 1040) <= 228 * 1024 &&
+                  kCtas * kTmemCols <= 512,
+                  "CTAs on one SM");
 };
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+__device__ __forceinline__ void st_cluster_pair(uint32_t addr, uint32_t a, uint32_t b)
 {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" :: "r"(addr), "r"(a), "r"(b) : "memory");
 }
 
-__device__ __forceinline__ float lds_f32(uint32_t addr)
+__device__ __forceinline__ uint64_t lds_pair(uint32_t addr)
 {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    uint64_t v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
     return v;
 }
 
@@ -68,47 +95,108 @@ __device__ __forceinline__ uint32_t cluster_nctarank()
     return r;
 }
 
-// What an epilogue thread writes: its output column of some rows.
+// A place in a ring of stages, and the stages gone through.
+struct Ring {
+    int done, slot;
+    uint32_t parity;
+
+    __device__ void step(int stages)
+    {
+        ++done;
+        if (++slot == stages) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+// A CTA's pieces: granules `at` .. `at` + n of the unit's row tile, one after another.
+// Called by all lanes of a warp.
+class PieceWalk {
+public:
+    __device__ PieceWalk(const LinearArgs &a, int block, int split)
+        : all_((a.outer + kLinearGranule - 1) / kLinearGranule), most_(a.granules), whole_(a.whole_pieces),
+          walk_(a, block, whole_ ? (all_ + most_ - 1) / most_ : all_, 1)
+    {
+        const long long units = count_units(a, block, whole_ ? (all_ + most_ - 1) / most_ : all_);
+        const unsigned b = blockIdx.x / split, n = gridDim.x / split;
+        valid_ = units >= 0;
+        at_ = valid_ ? static_cast<int>(units * b / n) : 0;
+        end_ = valid_ ? static_cast<int>(units * (b + 1ll) / n) : 0;
+    }
+
+    __device__ bool next(Unit &u, int &at, int &n)
+    {
+        if (at_ >= end_ || !walk_.find(at_, u))
+            return false;
+        if (whole_) {
+            at = u.column * most_;
+            n = min(most_, all_ - at);
+            ++at_;
+        } else {
+            at = u.column;
+            n = min(min(most_, all_ - at), end_ - at_);
+            at_ += n;
+        }
+        return true;
+    }
+
+    __device__ bool valid() const { return valid_; }
+
+private:
+    int all_, most_;
+    bool whole_;
+    UnitWalk walk_;
+    bool valid_;
+    int at_, end_;
+};
+
+// An epilogue thread's output column, in a warp's 32 of them.
 template <bool kGated, bool kHalf>
 struct Column {
     const LinearArgs &a;
-    long long f;            // output column
+    int f0, f;              // the warp's first column, this thread's
+    bool on;                // within the row
     float bg = 0.f, bu = 0.f;
 
-    __device__ Column(const LinearArgs &args, const Unit &u) : a(args)
+    __device__ Column(const LinearArgs &args, const Unit &u, int at, int quadrant) : a(args)
     {
-        f = static_cast<long long>(u.column) * kM + 32 * (threadIdx.x / 32 % 4) + threadIdx.x % 32;
-        const long long width = kGated ? 2 * a.outer : a.outer;
-        if (a.bias && f < a.outer) {
+        f0 = (at + quadrant) * kLinearGranule;
+        f = f0 + threadIdx.x % 32;
+        on = f < a.outer;
+        const long long width = kGated ? 2ll * a.outer : a.outer;
+        if (a.bias && on) {
             bg = load16<kHalf>(a.bias, u.group * width + f);
             if constexpr (kGated)
                 bu = load16<kHalf>(a.bias, u.group * width + a.outer + f);
         }
     }
 
-    // rows `row` and the next one, where they lie before `end`
-    __device__ void put(long long row, long long end, uint64_t z, uint64_t w) const
+    // z (and w) of rows `row` and the next one, their weights -> the results as 16-bit
+    // numbers; rows from `end` on are of no matter
+    template <int kAct>
+    __device__ uint32_t finish(long long row, long long end, uint64_t z, uint64_t w, uint64_t scale) const
     {
-        z = fadd2p(z, bc2(bg));
+        z = activate2<kAct>(fadd2p(z, bc2(bg)));
         if constexpr (kGated)
-            w = fadd2p(w, bc2(bu));
-        with_activation(a.activation, [&](auto act) { z = activate2<decltype(act)::value>(z); });
-        if constexpr (kGated)
-            z = fmul2(z, w);
-        float y[2];
-        f2_split(z, y[0], y[1]);
-        if (f >= a.outer)
-            return;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (row + e >= end)
-                return;
-            if (a.row_scale)
-                y[e] *= a.row_scale[row + e];
-            if (a.residual)
-                y[e] += load16<kHalf>(a.residual, (row + e) * a.residual_row + f);
-            static_cast<uint16_t *>(a.out)[(row + e) * a.out_row + f] = static_cast<uint16_t>(pack2<kHalf>(y[e], 0.f));
-        }
+            z = fmul2(z, fadd2p(w, bc2(bu)));
+        if (a.row_scale)
+            z = fmul2(z, scale);
+        if (a.residual && on)
+            z = fadd2p(z, f2(row < end ? load16<kHalf>(a.residual, row * a.residual_row + f) : 0.f,
+                             row + 1 < end ? load16<kHalf>(a.residual, (row + 1) * a.residual_row + f) : 0.f));
+        float lo, hi;
+        f2_split(z, lo, hi);
+        return pack2<kHalf>(lo, hi);
+    }
+
+    __device__ void put(long long row, long long end, uint32_t y) const
+    {
+        uint16_t *o = static_cast<uint16_t *>(a.out) + row * a.out_row + f;
+        if (on && row < end)
+            o[0] = static_cast<uint16_t>(y);
+        if (on && row + 1 < end)
+            o[a.out_row] = static_cast<uint16_t>(y >> 16);
     }
 };
 
@@ -118,139 +206,189 @@ linear_rows_kernel(const __grid_constant__ LinearArgs a)
 {
     using L = Layout<kNB, kGated>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t s_tmem;
-    pdl_wait();
+    __shared__ uint32_t s_tmem, s_gave_up;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;    // the same offset in every CTA of a cluster
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
-    const int first = blockIdx.x / split, stride = gridDim.x / split;
-    auto bar = [&](int i) { return base + L::kOffBar + 8u * i; };
+    const int stages = a.stages;
+    const uint32_t ring = base + L::kOffParts + L::parts_bytes(a.granules, split);
+    auto bar = [&](int i) { return base + 8u * i; };
 
     if (warp == 1) {
         tmem_alloc(smem_u32(&s_tmem), L::kTmemCols);
         tmem_relinquish();
-    } else if (tid == 0) {
-        tma_prefetch_desc(&a.tm_x);
-        tma_prefetch_desc(&a.tm_w);
-        for (int i = 0; i < L::kBars; ++i)
-            mbar_init(bar(i), i >= L::kAccEmpty ? kEpiThreads / 32 : 1);
+    } else if (warp == 0) {
+        if (lane == 0) {
+            s_gave_up = 0;
+            tma_prefetch_desc(&a.tm_x);
+            tma_prefetch_desc(&a.tm_w);
+        }
+        for (int i = lane; i < L::kBars; i += 32)
+            mbar_init(bar(i), i >= L::kAccEmpty ? kEpiWarps : 1);
         fence_mbar_init();
     }
-    const bool valid = offsets_ok(a);
     tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = s_tmem;
-    const int columns = (a.outer + kM - 1) / kM;
-    const int steps = (a.inner + kBK - 1) / kBK;
-    const int k0 = steps * rank / split, k1 = steps * (rank + 1) / split;
-    int *const err = a.err;
-    bool ok = valid;
-    UnitWalk walk(a, kNB, columns, INT32_MAX);
-    Unit u;
     // with a cut every CTA of the cluster is there before another writes to it
     if (split > 1)
         cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int steps = (a.inner + kBK - 1) / kBK;
+    const int k0 = steps * rank / split, k1 = steps * (rank + 1) / split;
+    int *const err = a.err;
+    const uint32_t gave_up = smem_u32(&s_gave_up);
+    pdl_wait();
+    PieceWalk walk(a, kNB, split);
+    Unit u;
+    int at, n;
 
-    if (valid && warp == 0) {
+    if (warp == 0) {
         // ------------------------------------------------------ producer
-        int g = 0;
-        for (int i = first; ok && walk.find(i, u); i += stride) {
-            for (int k = k0; k < k1; ++k, ++g) {
-                const int st = g % L::kStages;
-                if (!(ok = mbar_wait_warp(bar(L::kEmpty + st), ((g / L::kStages) & 1) ^ 1u, err)))
-                    break;
+        Ring r{0, 0, 1};
+        while (!any_gave_up(gave_up) && walk.next(u, at, n)) {
+            for (int k = k0; k < k1; ++k, r.step(stages)) {
+                mbar_wait_mark(bar(L::kEmpty + r.slot), r.parity, err, gave_up);
+                const uint32_t dst = ring + r.slot * a.stage_bytes, full = bar(L::kFull + r.slot);
                 if (elect_one_sync()) {
-                    const uint32_t dst = base + st * L::kStageBytes, full = bar(L::kFull + st);
-                    mbar_arrive_expect_tx(full, L::kStageBytes);
+                    mbar_arrive_expect_tx(full, L::kXBytes + L::kSides * n * kGranuleBytes);
 #pragma unroll
-                    for (int s = 0; s < L::kSides; ++s)
-                        tma_load_3d(dst + s * kWBytes, &a.tm_w, k * kBK, s * a.outer + u.column * kM, u.group, full);
-                    tma_load_2d(dst + L::kSides * kWBytes, &a.tm_x, k * kBK, static_cast<int>(u.row), full);
+                    for (int s = 0; s < L::kSides; ++s) {
+                        const uint32_t to = dst + L::kXBytes + s * a.granules * kGranuleBytes;
+                        const int row = s * a.outer + at * kLinearGranule;
+                        if (n == a.granules)
+                            tma_load_3d(to, &a.tm_w, k * kBK, row, u.group, full);
+                        else
+                            for (int i = 0; i < n; ++i)
+                                tma_load_3d(to + i * kGranuleBytes, &a.tm_granule, k * kBK, row + i * kLinearGranule,
+                                            u.group, full);
+                    }
+                    tma_load_2d(dst, &a.tm_x, k * kBK, static_cast<int>(u.row), full);
                 }
                 __syncwarp();
             }
         }
-        // the loads have landed and the MMAs have read them
-        for (int t = max(0, g - L::kStages); t < g; ++t)
-            drain_wait(bar(L::kFull + t % L::kStages), (t / L::kStages) & 1);
-    } else if (valid && warp == 1) {
+        // the loads have landed
+        ring_drain(bar(L::kFull), r.done, stages);
+    } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t kIdesc = make_idesc_f16(kM, kNB, kHalf);
-        int g = 0, n = 0;
-        for (int i = first; ok && walk.find(i, u); i += stride, ++n) {
-            const int acc = n & 1;
+        // the descriptors of stage 0; a stage, a side and 16 numbers of K further on
+        const uint64_t dx0 = make_sdesc_sw128(ring, 16, 1024), dw0 = make_sdesc_sw128(ring + L::kXBytes, 16, 1024);
+        const uint32_t d_stage = a.stage_bytes >> 4, d_side = a.granules * kGranuleBytes >> 4;
+        Ring r{0, 0, 0};
+        for (int units = 0; !any_gave_up(gave_up) && walk.next(u, at, n); ++units) {
+            const int acc = units & 1;
             const uint32_t d = tmem + acc * L::kSides * kNB;
-            if (!(ok = mbar_wait_warp(bar(L::kAccEmpty + acc), ((n >> 1) & 1) ^ 1u, err)))
-                break;
+            mbar_wait_mark(bar(L::kAccEmpty + acc), ((units >> 1) & 1) ^ 1u, err, gave_up);
             tc_fence_after();
-            for (int k = k0; k < k1; ++k, ++g) {
-                const int st = g % L::kStages;
-                if (!(ok = mbar_wait_warp(bar(L::kFull + st), (g / L::kStages) & 1, err)))
-                    break;
+            for (int k = k0; k < k1; ++k, r.step(stages)) {
+                const uint64_t dx = dx0 + r.slot * d_stage, dw = dw0 + r.slot * d_stage;
+                mbar_wait_mark(bar(L::kFull + r.slot), r.parity, err, gave_up);
                 tc_fence_after();
-                const uint32_t sw = base + st * L::kStageBytes, sx = sw + L::kSides * kWBytes;
+                if (elect_one_sync()) {
 #pragma unroll
-                for (int s = 0; s < L::kSides; ++s)
+                    for (int s = 0; s < L::kSides; ++s)
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        mma_bf16_ss_warp(d + s * kNB, make_sdesc_sw128(sw + s * kWBytes + 32 * kk, 16, 1024),
-                                         make_sdesc_sw128(sx + 32 * kk, 16, 1024), kIdesc, k > k0 || kk > 0);
-                mma_commit_warp(bar(L::kEmpty + st));
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            mma_bf16_ss(d + s * kNB, dw + s * d_side + 2 * kk, dx + 2 * kk, kIdesc, k > k0 || kk > 0);
+                    mma_commit(bar(L::kEmpty + r.slot));
+                }
+                __syncwarp();
             }
-            if (ok)
-                mma_commit_warp(bar(L::kAccFull + acc));
+            mma_commit_warp(bar(L::kAccFull + acc));
         }
         // every MMA issued has completed before TMEM is released
-        for (int t = max(0, g - L::kStages); t < g; ++t)
-            drain_wait(bar(L::kEmpty + t % L::kStages), (t / L::kStages) & 1);
-    } else if (valid) {
+        ring_drain(bar(L::kEmpty), r.done, stages);
+        __syncwarp();
+    } else {
         // ------------------------------------------------------ epilogue
-        const int q = warp & 3;
-        const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-        int n = 0;
-        for (int i = first; ok && walk.find(i, u); i += stride, ++n) {
-            const int acc = n & 1;
-            const Column<kGated, kHalf> col(a, u);
-            if (!(ok = mbar_wait_warp(bar(L::kAccFull + acc), static_cast<uint32_t>(n >> 1) & 1u, err)))
+        // TMEM quadrant q, that is a granule, and every other block of rows
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int share = kNB / split, columns = a.granules * kLinearGranule;
+        const uint32_t tile = base + L::kOffTiles + (warp - 2) * L::kTileBytes;
+        for (int units = 0; walk.next(u, at, n); ++units) {
+            const int acc = units & 1;
+            const Column<kGated, kHalf> col(a, u, at, q);
+            mbar_wait_mark(bar(L::kAccFull + acc), static_cast<uint32_t>(units >> 1) & 1u, err, gave_up);
+            if (any_gave_up(gave_up))
                 break;
             tc_fence_after();
-            const uint32_t d = tmem + acc * L::kSides * kNB + lanes;
+            const uint32_t d = tmem + acc * L::kSides * kNB + (static_cast<uint32_t>(32 * q) << 16);
             const int rows = static_cast<int>(min(u.end - u.row, static_cast<long long>(kNB)));
-            const int share = kNB / split;
+            if (q < n) {
+                with_activation(split > 1 ? MBERT_ACT_NONE : a.activation, [&](auto act) {
 #pragma unroll 1
-            for (int j = 0; j < kNB; j += 16) {
-                if (j >= rows)
-                    break;
-                uint32_t zg[16], zu[16];
-                tmem_ld16(d + j, zg);
-                if constexpr (kGated)
-                    tmem_ld16(d + kNB + j, zu);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    asm volatile("" : "+r"(zg[e]));
-                    if constexpr (kGated)
-                        asm volatile("" : "+r"(zu[e]));
-                }
-                if (split > 1) {
-                    // to the CTA whose share of the rows it is: [CTA][side][row][column]
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int to = (j + e) / share, c = (j + e) % share;
-                        const uint32_t at = base + L::kOffParts +
-                            (((rank * L::kSides * share) + c) * kM + 32 * q + lane) * 4;
-                        const uint32_t p = map_to_rank(at, to);
-                        st_cluster_f32(p, __uint_as_float(zg[e]));
+                    for (int j = kBlock * half; j < rows; j += 2 * kBlock) {
+                        uint32_t zg[16], zu[16];
+                        const float weight = a.row_scale && split == 1 && lane < kBlock && j + lane < rows
+                                                 ? a.row_scale[u.row + j + lane] : 0.f;
+                        tmem_ld16(d + j, zg);
                         if constexpr (kGated)
-                            st_cluster_f32(p + share * kM * 4, __uint_as_float(zu[e]));
-                    }
-                } else {
+                            tmem_ld16(d + kNB + j, zu);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2)
-                        col.put(u.row + j + e, u.row + rows, f2(__uint_as_float(zg[e]), __uint_as_float(zg[e + 1])),
-                                kGated ? f2(__uint_as_float(zu[e]), __uint_as_float(zu[e + 1])) : 0ull);
-                }
+                        for (int e = 0; e < 16; ++e) {
+                            asm volatile("" : "+r"(zg[e]));
+                            if constexpr (kGated)
+                                asm volatile("" : "+r"(zu[e]));
+                        }
+                        if (split > 1) {
+                            // to the CTA whose share of the rows it is, two rows at a time:
+                            // [CTA][side][pair of rows][column][2]
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const int to = (j + e) / share, c = (j + e) % share;
+                                const uint32_t p = map_to_rank(base + L::kOffParts +
+                                    ((rank * L::kSides * share + c) * columns + 2 * (32 * q + lane)) * 4, to);
+                                st_cluster_pair(p, zg[e], zg[e + 1]);
+                                if constexpr (kGated)
+                                    st_cluster_pair(p + share * columns * 4, zu[e], zu[e + 1]);
+                            }
+                            continue;
+                        }
+                        const long long row = u.row + j, end = u.row + rows;
+                        uint32_t y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            y[e] = col.template finish<decltype(act)::value>(
+                                row + 2 * e, end, f2(__uint_as_float(zg[2 * e]), __uint_as_float(zg[2 * e + 1])),
+                                kGated ? f2(__uint_as_float(zu[2 * e]), __uint_as_float(zu[2 * e + 1])) : 0ull,
+                                f2(__shfl_sync(0xffffffffu, weight, 2 * e), __shfl_sync(0xffffffffu, weight, 2 * e + 1)));
+                        if (!a.out_vectors) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                col.put(row + 2 * e, end, y[e]);
+                            continue;
+                        }
+                        // through the warp's tile, to 8 columns of a row a thread
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            asm volatile("st.shared.b16 [%0], %1;"
+                                         :: "r"(tile + e * 64 + 2 * lane), "h"(static_cast<uint16_t>(y[e / 2] >> 16 * (e & 1)))
+                                         : "memory");
+                        __syncwarp();
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int r = 8 * t + lane / 4, c = 8 * (lane & 3), left = a.outer - col.f0 - c;
+                            uint4 v;
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(tile + r * 64 + 2 * c) : "memory");
+                            uint16_t *o = static_cast<uint16_t *>(a.out) + (row + r) * a.out_row + col.f0 + c;
+                            if (row + r < end && left >= 8) {
+                                *reinterpret_cast<uint4 *>(o) = v;
+                            } else if (row + r < end) {
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    if (e < left)
+                                        o[e] = static_cast<uint16_t>(w[e / 2] >> 16 * (e & 1));
+                            }
+                        }
+                        __syncwarp();
+                    }
+                });
             }
             tc_fence_before();
             __syncwarp();
@@ -260,25 +398,28 @@ linear_rows_kernel(const __grid_constant__ LinearArgs a)
     }
     __syncwarp();
     if (split > 1) {
-        // all parts are written (the launch gives a cluster one unit at most)
+        // all parts are written (a cluster has one piece at most)
         cluster_sync();
-        const int all_ok = __syncthreads_and(ok);
-        UnitWalk again(a, kNB, columns, INT32_MAX);
-        if (valid && warp >= 2 && all_ok && again.find(first, u)) {
-            const Column<kGated, kHalf> col(a, u);
-            const int share = kNB / split, rows = static_cast<int>(min(u.end - u.row, static_cast<long long>(kNB)));
-            const uint32_t mine = base + L::kOffParts + (32 * (warp & 3) + lane) * 4;
-            for (int c = 0; c < share && rank * share + c < rows; c += 2) {
-                float z[2][2] = {};
-                for (int s = 0; s < split; ++s)
+        __syncthreads();
+        PieceWalk again(a, kNB, split);
+        if (warp >= 2 && !any_gave_up(gave_up) && again.next(u, at, n) && (warp & 3) < n) {
+            const int q = warp & 3, half = (warp - 2) >> 2;
+            const Column<kGated, kHalf> col(a, u, at, q);
+            const int share = kNB / split, columns = a.granules * kLinearGranule;
+            const int rows = static_cast<int>(min(u.end - u.row, static_cast<long long>(kNB)));
+            const uint32_t mine = base + L::kOffParts + 2 * (32 * q + lane) * 4;
+            with_activation(a.activation, [&](auto act) {
+                for (int c = 2 * half; c < share && rank * share + c < rows; c += 4) {
+                    uint64_t z[2] = {};
+                    for (int s = 0; s < split; ++s)
 #pragma unroll
-                    for (int side = 0; side < L::kSides; ++side)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            z[side][e] += lds_f32(mine + ((s * L::kSides + side) * share + c + e) * kM * 4);
-                const long long row = u.row + rank * share + c;
-                col.put(row, u.row + rows, f2(z[0][0], z[0][1]), f2(z[1][0], z[1][1]));
-            }
+                        for (int side = 0; side < L::kSides; ++side)
+                            z[side] = fadd2p(z[side], lds_pair(mine + ((s * L::kSides + side) * share + c) * columns * 4));
+                    const long long row = u.row + rank * share + c, end = u.row + rows;
+                    const uint64_t scale = a.row_scale ? f2(a.row_scale[row], row + 1 < end ? a.row_scale[row + 1] : 0.f) : 0ull;
+                    col.put(row, end, col.template finish<decltype(act)::value>(row, end, z[0], z[1], scale));
+                }
+            });
         }
     }
     tc_fence_before();
@@ -291,25 +432,28 @@ linear_rows_kernel(const __grid_constant__ LinearArgs a)
 }
 
 template <int kNB, bool kGated, bool kHalf>
-cudaError_t launch(const LinearArgs &a, int split, long long units, int num_sms, cudaStream_t stream)
+cudaError_t launch(LinearArgs a, const LinearRowsPlan &p, cudaStream_t stream)
 {
     using L = Layout<kNB, kGated>;
     static PerDeviceOnce once;
     auto *kernel = linear_rows_kernel<kNB, kGated, kHalf>;
-    const cudaError_t e = smem_opt_in(once, kernel, L::smem(linear_rows_most_split(kNB, kGated)));
+    const cudaError_t e = smem_opt_in(once, kernel, linear_rows_budget(kNB, kGated));
     if (e != cudaSuccess)
         return e;
-    const long long most = static_cast<long long>(num_sms) * L::kCtas;
+    a.granules = p.granules;
+    a.whole_pieces = p.whole;
+    a.stages = L::stages(p.granules, p.split);
+    a.stage_bytes = static_cast<int>(L::stage_bytes(p.granules));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.x = p.split;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(split > 1 ? units * split : units < most ? units : most));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas * p.split));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = L::smem(split);
+    cfg.dynamicSmemBytes = L::smem(p.granules, p.split);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -317,25 +461,21 @@ cudaError_t launch(const LinearArgs &a, int split, long long units, int num_sms,
 }
 
 template <int kNB>
-cudaError_t launch(const LinearArgs &a, int split, bool gated, bool half, long long units, int num_sms,
-                   cudaStream_t stream)
+cudaError_t launch(const LinearArgs &a, const LinearRowsPlan &p, bool gated, bool half, cudaStream_t stream)
 {
-    return gated ? half ? launch<kNB, true, true>(a, split, units, num_sms, stream)
-                        : launch<kNB, true, false>(a, split, units, num_sms, stream)
-                 : half ? launch<kNB, false, true>(a, split, units, num_sms, stream)
-                        : launch<kNB, false, false>(a, split, units, num_sms, stream);
+    return gated ? half ? launch<kNB, true, true>(a, p, stream) : launch<kNB, true, false>(a, p, stream)
+                 : half ? launch<kNB, false, true>(a, p, stream) : launch<kNB, false, false>(a, p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_rows(const LinearArgs &a, int tile, int split, bool gated, bool half, long long units,
-                               int num_sms, cudaStream_t stream)
+cudaError_t launch_linear_rows(const LinearArgs &a, const LinearRowsPlan &p, bool gated, bool half, cudaStream_t stream)
 {
-    switch (tile) {
-    case 16: return launch<16>(a, split, gated, half, units, num_sms, stream);
-    case 32: return launch<32>(a, split, gated, half, units, num_sms, stream);
-    case 64: return launch<64>(a, split, gated, half, units, num_sms, stream);
-    default: return launch<128>(a, split, gated, half, units, num_sms, stream);
+    switch (p.tile) {
+    case 16: return launch<16>(a, p, gated, half, stream);
+    case 32: return launch<32>(a, p, gated, half, stream);
+    case 64: return launch<64>(a, p, gated, half, stream);
+    default: return launch<128>(a, p, gated, half, stream);
     }
 }
 
