@@ -22,6 +22,7 @@ constexpr int kMaxWidth = 1 << 24;
 // Elements from a tensor's first to its last, at most: beyond any device's memory,
 // and far from where extents in bytes would overflow.
 constexpr int64_t kMaxSpan = 1ll << 48;
+constexpr int64_t kMaxPitch = 1ll << 38;    // what a tensor map can hold
 
 // Rows of `width` elements, `pitch` elements apart.
 struct Rows {
@@ -32,7 +33,7 @@ struct Rows {
     bool ok() const
     {
         return p && reinterpret_cast<uintptr_t>(p) % es == 0 &&
-               (rows <= 1 || (pitch >= width && pitch <= kMaxSpan / rows)) && width <= kMaxSpan;
+               (rows <= 1 || (pitch >= width && pitch <= kMaxPitch && pitch <= kMaxSpan / rows)) && width <= kMaxSpan;
     }
     uintptr_t lo() const { return reinterpret_cast<uintptr_t>(p); }
     uintptr_t hi() const { return lo() + static_cast<uintptr_t>(((rows - 1) * pitch + width) * es); }
@@ -108,7 +109,7 @@ int64_t block_bound(const mbert_attn_linear_args &c, int rows)
 // tiles and no more: over 102 sizes the chosen one took 4 % longer than the best of
 // all.  (Kernel for few rows against that for many, us: 128 x 4096 -> 512 9.2 / 19.0, 300 x
 // 768 -> 2304 8.9 / 9.7, 1024 x 1024 -> 8192 26.8 / 20.5; 500 rows of 16 experts, 768 -> 2304,
-// 15.8 / 26.3, 2000 rows of 2, 1024 -> 8192, 70 / 70; tiles of 64 against 128 rows, 500 rows of
+// 15.8 / 26.3, 2000 rows of 16, 1024 -> 8192, 65 / 70; tiles of 64 against 128 rows, 500 rows of
 // 16 experts, 4096 -> 2 x 512, 48 / 32.)
 struct Cost {
     double clocks;
@@ -262,7 +263,8 @@ MBERT_API int mbert_attn_linear(mbert_attn *h, const mbert_attn_linear_args *arg
     // what TMA can fetch: 16-byte aligned rows
     const int64_t matrix = (width - 1) * c.weight_row + c.inner;
     if (!x.aligned(16) || !weight.aligned(16) ||
-        (groups > 1 && (c.weight_expert < matrix || c.weight_expert % 8 || c.weight_expert > kMaxSpan / groups)))
+        (groups > 1 && (c.weight_expert < matrix || c.weight_expert % 8 || c.weight_expert > kMaxPitch ||
+                        c.weight_expert > kMaxSpan / groups)))
         return MBERT_ERR_BAD_ARG;
     const Rows bias = flat(c.bias, groups * width, 2), scale = flat(c.row_scale, c.rows, 4);
     const Rows weights = flat(c.weight, (groups - 1) * c.weight_expert + matrix, 2);

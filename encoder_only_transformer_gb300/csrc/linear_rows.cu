@@ -249,9 +249,10 @@ linear_rows_kernel(const __grid_constant__ LinearArgs a)
         Ring r{0, 0, 1};
         while (!any_gave_up(gave_up) && walk.next(u, at, n)) {
             for (int k = k0; k < k1; ++k, r.step(stages)) {
-                mbar_wait_mark(bar(L::kEmpty + r.slot), r.parity, err, gave_up);
+                // (after a wait that gives up nothing more is loaded)
+                const bool go = mbar_wait_mark(bar(L::kEmpty + r.slot), r.parity, err, gave_up);
                 const uint32_t dst = ring + r.slot * a.stage_bytes, full = bar(L::kFull + r.slot);
-                if (elect_one_sync()) {
+                if (elect_one_sync() && go) {
                     mbar_arrive_expect_tx(full, L::kXBytes + L::kSides * n * kGranuleBytes);
 #pragma unroll
                     for (int s = 0; s < L::kSides; ++s) {

@@ -454,8 +454,8 @@ enum {
  *                sets MBERT_ERR_BAD_CU_SEQLENS, and nothing is written.
  *   eps          0 <= eps <= 1.
  * All in fp32, h and y rounded once; y is of the h that has not been rounded.  Rows whose squares
- * fp32 does not hold are scaled by a power of two first, so any finite rows do; a row without
- * spread (all zeros, for LayerNorm all equal) is 0/0 with eps = 0.  Any alignment of the element
+ * fp32 does not hold are scaled by a power of two first, so any rows of normal numbers do; a row
+ * without spread (all zeros, for LayerNorm all equal) is 0/0 with eps = 0.  Any alignment of the element
  * size; rows of whole, 16-byte aligned vectors are read in these.  One kernel. */
 typedef struct {
     const void *x, *branch, *gate;
