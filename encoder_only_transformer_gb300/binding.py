@@ -1067,4 +1067,4 @@ def residual_norm(x: torch.Tensor, branch: torch.Tensor = None, weight: torch.Te
     """(h, y): the residual stream behind a block and its norm for the next one:
     Attention.residual_norm on the device's handle."""
     return _of(x).residual_norm(x, branch, weight, bias, branch_weight, branch_bias, gate, cu_seqlens,
-                                            norm, residual_scale, eps, h_out, y_out)
+                                norm, residual_scale, eps, h_out, y_out)

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
+#include <mutex>
 #include <vector>
 
 #include "mbert_attn.h"
@@ -68,6 +69,7 @@ struct mbert_attn {
     MapEntry maps[32];
     uint64_t map_clock = 0;
     mbert::PlanEntry plans[64];             // of products of any width, by their sizes
+    std::mutex plan_lock;
 };
 
 namespace mbert {

@@ -217,7 +217,8 @@ LinearPlan make_plan(const mbert_attn *h, const mbert_attn_linear_args &c)
 }
 
 // The plan of a call; that of one like an earlier one is found again (weighing takes
-// microseconds, as long as a short kernel).
+// microseconds, as long as a short kernel).  Under a lock: a plan that two threads had
+// written together would be none.
 LinearPlan linear_plan(mbert_attn *h, const mbert_attn_linear_args &c)
 {
     const int64_t key[4] = {c.rows, static_cast<int64_t>(c.inner) << 32 | c.outer, c.experts,
@@ -225,6 +226,7 @@ LinearPlan linear_plan(mbert_attn *h, const mbert_attn_linear_args &c)
     uint64_t x = 0;
     for (const int64_t k : key)
         x = (x ^ static_cast<uint64_t>(k)) * 0x9E3779B97F4A7C15ull;
+    const std::lock_guard<std::mutex> lock(h->plan_lock);
     mbert::PlanEntry &e = h->plans[x >> 58];
     if (!e.known || std::memcmp(e.key, key, sizeof key) != 0) {
         e.plan = make_plan(h, c);

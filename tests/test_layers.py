@@ -184,3 +184,29 @@ def test_calls_at_once(built):  # noqa: F811
                 got.append((k, calls[k]()))
     err0()
     assert all(torch.equal(t, want[k]) for k, t in got)
+
+
+def test_threads(built):  # noqa: F811
+    """Products of many sizes from four threads, each on a stream of its own."""
+    import threading
+    x, w = rnd(400, 512, seed=1).cuda(), rnd(900, 512, seed=2, sc=0.05).cuda()
+    sizes = [(t, n) for t in (1, 9, 40, 130, 400) for n in range(20, 900, 67)]
+    want = {s: binding.linear(x[:s[0]], w[:s[1]]) for s in sizes}
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(seed):
+        order = sizes * 3
+        random.Random(seed).shuffle(order)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [(s, binding.linear(x[:s[0]], w[:s[1]])) for s in order]
+            torch.cuda.current_stream().synchronize()
+            wrong.extend(s for s, t in got if not torch.equal(t, want[s]))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    err0()
+    assert not wrong

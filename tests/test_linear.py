@@ -399,10 +399,12 @@ def test_refusals(built):
     for kw in (dict(rows=-1), dict(rows=2 ** 31 - 1), dict(inner=0), dict(outer=0), dict(outer=2 ** 24 + 1),
                dict(activation=5), dict(activation=-1), dict(gated=2), dict(experts=-1), dict(x=None), dict(out=None),
                dict(weight=None), dict(x_row=56), dict(x_row=65), dict(weight_row=2 ** 61), dict(out_row=11),
+               dict(x_row=2 ** 39), dict(out_row=2 ** 39),
                dict(out_row=2 ** 62), dict(out=out.data_ptr() + 1), dict(x=x.data_ptr() + 2),
                dict(cu_experts=cu.data_ptr()), dict(row_scale=out.data_ptr()), dict(experts=1),
                dict(experts=1, cu_experts=cu.data_ptr() + 1), dict(experts=1, cu_experts=cu.data_ptr(), residual=x.data_ptr()),
-               dict(experts=2, cu_experts=cu.data_ptr(), weight_expert=64), dict(residual=out.data_ptr(), residual_row=13)):
+               dict(experts=2, cu_experts=cu.data_ptr(), weight_expert=64),
+               dict(experts=2, cu_experts=cu.data_ptr(), weight_expert=2 ** 39), dict(residual=out.data_ptr(), residual_row=13)):
         assert call(**kw) == -1, kw
     assert call(rows=0, x=None) == 0
     err0()
