@@ -557,9 +557,15 @@ residual_norm_kernel(const ResidualNormArgs a)
     pdl_trigger();
 }
 
-// Shared memory of one SM for the rings: one slot of the widest rows at least.
-constexpr int kRingBytes = 200 * 1024;
-static_assert(3 * (kResidualNormMaxWidth * 4 + 30) <= kRingBytes, "a slot");
+// Shared memory of one SM for the rings of its blocks, each of which takes a little
+// beside: one slot of the widest rows at least.
+constexpr int kMostRing = 220 * 1024;
+constexpr int kBlockBytes = 1024 + 256;
+constexpr int ring_bytes(int blocks)
+{
+    return 228 * 1024 - blocks * kBlockBytes < kMostRing ? 228 * 1024 - blocks * kBlockBytes : kMostRing;
+}
+static_assert(3 * (kResidualNormMaxWidth * 4 + 30) <= ring_bytes(1), "a slot");
 
 template <int kType, bool kVectors, int kVecs, bool kLayer>
 cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
@@ -572,7 +578,7 @@ cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
         cudaFuncAttributes f;
         cudaError_t r = cudaFuncGetAttributes(&f, kernel);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+            r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(1));
         *out = 65536 / (32 * ((f.numRegs > 0 ? f.numRegs + 7 : 64) / 8 * 8));
         return r;
     });
@@ -587,9 +593,10 @@ cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
     // not do, and one slot where it does not do for a single block (rows of 48 KB or
     // more from three tensors in fp32)
     const int slot = crews * beside * a.row_bytes * a.tensors;
-    const int per_sm =
-        std::max(1, std::min(std::min(fit / (threads / 32), 2048 / threads), kRingBytes / (2 * slot)));
-    a.slots = std::min(kMostSlots, kRingBytes / (per_sm * slot));
+    int per_sm = std::max(1, std::min(fit / (threads / 32), 2048 / threads));
+    while (per_sm > 1 && ring_bytes(per_sm) < per_sm * 2 * slot)
+        --per_sm;
+    a.slots = std::min(kMostSlots, ring_bytes(per_sm) / (per_sm * slot));
     const long long need = (a.rows + crews * beside - 1) / (crews * beside);
     const long long most = static_cast<long long>(num_sms) * per_sm;
     return launch_chained(kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(threads), a.slots * slot,
