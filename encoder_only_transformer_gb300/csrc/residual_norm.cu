@@ -8,8 +8,8 @@
 // h that has not been rounded.
 //
 // Bound by HBM: x and branch in, h and y out.  A crew takes a row (or, of short rows,
-// as many as a warp has lanes for): a warp up to 2048 numbers (1024 in fp32), 32 to 64
-// a lane in registers, and up to 16 warps beyond, which add their sums up in shared
+// as many as a warp has lanes for): a warp up to 1536 numbers (1024 in fp32), 32 or
+// 48 a lane in registers, and up to 16 warps beyond, which add their sums up in shared
 // memory.  Rows come by cp.async into a ring of shared-memory slots of the crew's own,
 // and a slot is filled again as soon as h is in registers: the loads of the next rows run
 // while a row goes through its sums, which are chains of shuffles.  Every thread copies
@@ -573,13 +573,14 @@ cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
     static PerDeviceOnce once;
     constexpr int kBytes = Row<kType, kVectors, kVecs>::kBytes;
     auto *kernel = residual_norm_kernel<kType, kVectors, kVecs, kLayer>;
-    int fit = 0;                                            // warps on one SM, by registers
+    // warps on one SM, by registers: each of its four parts has 16384 of them
+    int fit = 0;
     const cudaError_t e = per_device_once(once, &fit, [&](int *out) {
         cudaFuncAttributes f;
         cudaError_t r = cudaFuncGetAttributes(&f, kernel);
         if (r == cudaSuccess)
             r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(1));
-        *out = 65536 / (32 * ((f.numRegs > 0 ? f.numRegs + 7 : 64) / 8 * 8));
+        *out = 4 * (16384 / (32 * ((f.numRegs > 0 ? f.numRegs + 7 : 64) / 8 * 8)));
         return r;
     });
     if (e != cudaSuccess)
@@ -609,16 +610,25 @@ cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
     constexpr int kN = Row<kType, kVectors, 1>::kN;
     const int vecs = (a.width + kN - 1) / kN;           // of a row
     // up to 32 lanes take a row (all 32 where they take single numbers), then more
-    // vectors each, then more warps
+    // vectors each, then more warps: those that share out 16 numbers a lane, or, with
+    // many rows of 16-bit vectors, 32, so that two crews or more share an SM and one
+    // sums while another loads (f16, LayerNorm with the residual, 7812 x 4096 45 us
+    // against 49, 3906 x 8192 42 / 52, RMS on both sides with gates of sequences 50 / 65 and 53 / 71;
+    // 304 x 4096 with all parts 5.7 / 4.5.  In fp32 slots of twice the bytes leave
+    // no room for more crews: 3906 x 4096 with all parts 75 / 52)
     a.lanes = kVectors ? 1 : 32;
     while (a.lanes < 32 && a.lanes < vecs)
         a.lanes *= 2;
-    const int most = kVectors ? 8 : 32 / kN;            // vectors a lane in a crew of one warp
-    a.warps = vecs <= 32 * most ? 1 : std::min(kMostWarps, (a.width + 32 * kCrewNumbers - 1) / (32 * kCrewNumbers));
+    const int most = kVectors ? kType == MBERT_F32 ? 8 : 6 : 32 / kN;
+    const int few = (a.width + 64 * kCrewNumbers - 1) / (64 * kCrewNumbers);
+    a.warps = vecs <= 32 * most ? 1
+              : kVectors && kType != MBERT_F32 && few <= kMostWarps / 2 && a.rows > 2 * num_sms ? few
+              : std::min(kMostWarps, (a.width + 32 * kCrewNumbers - 1) / (32 * kCrewNumbers));
     const int each = (vecs + a.lanes * a.warps - 1) / (a.lanes * a.warps);
     if constexpr (kVectors || kN == 4) {
-        if (each > 6)
-            return launch<kType, kVectors, 8, kLayer>(a, num_sms, stream);
+        if constexpr (kN == 4)
+            if (each > 6)
+                return launch<kType, kVectors, 8, kLayer>(a, num_sms, stream);
         if (each == 6)
             return launch<kType, kVectors, 6, kLayer>(a, num_sms, stream);
         if (each == 5)

@@ -210,3 +210,9 @@ def test_threads(built):  # noqa: F811
         t.join()
     err0()
     assert not wrong
+
+
+@pytest.mark.parametrize("sizes", [[300, 0] * 80, [0] * 127 + [513] + [0] * 130 + [1, 700]], ids=["160", "260"])
+def test_many_experts_of_many_rows(built, sizes):  # noqa: F811
+    """More groups than a warp holds the offsets of at a time, whole tiles in each."""
+    L.run_experts(sizes, 64, 136, "bf16", "gelu", True, False, True, 3, 5)

@@ -140,6 +140,20 @@ def test_widths(built, D, kind, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("D", [1280, 1535, 1536, 1544, 2048, 2056, 2560, 4088, 4096, 6152, 8192, 8200])
+def test_wide_rows_by_fewer_warps(built, D, dtype):
+    """Rows enough for every SM several times over, in crews of every size."""
+    T = 650
+    m = make(T, D, dtype, seed=D + 2)
+    # scaled a second time (f16 holds 65504, twice 2^12 times 7 deviations are less)
+    m["x"][::50] *= 2.0 ** 12 if dtype == "f16" else 2.0 ** 66
+    m["branch"][7::50] = 0
+    run(m["x"], m["branch"], m["w"], m["b"], m["aw"], m["ab"], rnd(T, D, seed=9, dtype=dtype), "layer", 0.7)
+    run(m["x"], m["branch"], m["w"], aw=m["aw"], gate=rnd(D, seed=9, dtype=dtype), kind="rms")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("D", [64, 768, 1001, 2304])
 def test_parts(built, D, dtype):
     T = 300
