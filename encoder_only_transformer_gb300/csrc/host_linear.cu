@@ -313,7 +313,6 @@ MBERT_API int mbert_attn_linear(mbert_attn *h, const mbert_attn_linear_args *arg
     a.inner = c.inner;
     a.outer = c.outer;
     a.activation = c.activation;
-    a.bias_vectors = c.bias && bias.aligned(16) && c.outer % 8 == 0;
     a.err = h->err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool half = c.dtype == MBERT_F16;

@@ -30,7 +30,6 @@ struct LinearArgs {
     // linear_rows.cu: granules of a piece, stages of its ring, bytes of one
     int granules = 0, stages = 0, stage_bytes = 0;
     int whole_pieces = 0;               // dealt out to the CTAs, not granules
-    int bias_vectors = 0;               // bias at n (and outer + n) is 16-byte aligned for n % 8 == 0
     int out_vectors = 0, residual_vectors = 0;
     int out_bytes = 2, residual_bytes = 2;      // else: bytes of a word, 2, 4 or 8
     int32_t *err = nullptr;
