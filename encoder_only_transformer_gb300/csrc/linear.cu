@@ -36,14 +36,15 @@
 // about 8 x 10 blocks, whose rows and weights stay in L2.
 // Units of 256 x 128 accumulators serve calls with too few units for every pair.
 //
-// 32768 x 1024 -> 2 x 4096 bf16, GELU and gate: 287 us, 1.92 PFLOP/s (1.64 under
+// 32768 x 1024 -> 2 x 4096 bf16, GELU and gate: 277 us, 1.98 PFLOP/s (1.66 under
 // the power cap, where the same calls follow each other for seconds); without a gate the
-// epilogue, 5000 clocks of a unit and 3700 more for GELU, shows: 331 us with it, 290
-// without.  65536 rows of 8 experts, 768 -> 2 x 1152: 140 us; 1152 -> 768: 76 us, 780 units
+// epilogue, 5000 clocks of a unit and 3700 more for GELU, shows: 325 us with it, 290
+// without.  65536 rows of 8 experts, 768 -> 2 x 1152: 133 us; 1152 -> 768: 74 us, 780 units
 // on 76 pairs in 11 rounds.
-// Not kept: the accumulators through fp32 tiles, 8 columns of a row a thread, plain
-// stores: 150 and 351 us for 140 and 331; 8 warps without a gate 339; an arrival at the
-// leader's barrier with a release at the cluster's scope, which waits for stores: 144.
+// Not kept (before the bias came ahead, when these calls took 140 and 331 us): the
+// accumulators through fp32 tiles, 8 columns of a row a thread, plain stores: 150 and 351;
+// 8 warps without a gate 339; an arrival at the leader's barrier with a release at the
+// cluster's scope, which waits for stores: 144.
 #include "linear.cuh"
 #include "internal.h"
 #include "pair.cuh"
