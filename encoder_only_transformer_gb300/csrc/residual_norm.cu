@@ -18,13 +18,14 @@
 // TB/s), rows loaded into registers 84.  A norm's statistics are sums over the registers
 // in pairs, the LayerNorm's in two passes (mean, then squares about it).  Weights come
 // from L1 or L2 for each row.  Rows off 16 bytes come as the 16-byte pieces they lie in
-// and are taken number by number.
+// (see pieces.h for those at a tensor's ends) and are taken number by number.
 //
 // Where the squares add up to what fp32 does not hold (or, beside a small eps, to
 // what it holds badly), the row is scaled by a power of two first: see norm_row.
 #include <algorithm>
 
 #include "internal.h"
+#include "pieces.h"
 #include "residual_norm.h"
 #include "linear.cuh"
 
@@ -356,6 +357,16 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
 }
 
+// a number of 2 or 4 bytes to shared memory
+template <int kBytes>
+__device__ __forceinline__ void copy_number(uint32_t dst, const char *src)
+{
+    if constexpr (kBytes == 4)
+        asm volatile("st.shared.b32 [%0], %1;" :: "r"(dst), "r"(*reinterpret_cast<const uint32_t *>(src)) : "memory");
+    else
+        asm volatile("st.shared.b16 [%0], %1;" :: "r"(dst), "h"(*reinterpret_cast<const uint16_t *>(src)) : "memory");
+}
+
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // all but the `n` newest groups have landed
@@ -417,6 +428,7 @@ residual_norm_kernel(const ResidualNormArgs a)
         if (bad && blockIdx.x == 0 && threadIdx.x == 0)
             atomicOr(a.err, kErrBadCu);
     }
+    const unsigned all_rows = static_cast<unsigned>(a.rows);
     const unsigned rows = static_cast<unsigned>(bad ? 0 : a.cu ? a.cu[a.n_seqs] : a.rows);
     // this thread's first row and the rows from round to round (a row and a stride stay
     // below 2^32: there are at most 2^31 - 1024 rows, and a row for every lane)
@@ -432,18 +444,18 @@ residual_norm_kernel(const ResidualNormArgs a)
     auto row_of = [&](const void *p, long long pitch, unsigned row) {
         return static_cast<const char *>(p) + row * pitch * kBytes;
     };
-    auto gate_of = [&](unsigned row, int &s) {
-        if (a.cu) {
-            s = sequence_of(a.cu, a.n_seqs, static_cast<int>(row), s);
-            row = s;
-        }
-        return row_of(a.gate, a.gate_row, row);
+    // the row of `gate` that row `row` takes; s is the sequence of an earlier row
+    auto gate_row = [&](unsigned row, int &s) {
+        return a.cu ? static_cast<unsigned>(s = sequence_of(a.cu, a.n_seqs, static_cast<int>(row), s)) : row;
     };
     // Whole vectors: every thread copies the ones that it will read, so nothing but its
     // own copies has to be waited for.  Single numbers: the crew copies the 16-byte pieces
     // of memory that the row lies in (its neighbours' numbers at either end are not looked
-    // at), and waits for each other.
-    auto copy = [&](uint32_t dst, const char *p) {
+    // at), and waits for each other.  `row` of `count`: nothing is read before a tensor's
+    // first number or behind its last (9456 x 92 bf16, gates of 12 sequences, 10.7 us
+    // against 9.6 with whole pieces everywhere; 707 x 9647 fp16 32.3 / 31.3).
+    auto copy = [&](uint32_t dst, const void *tensor, long long pitch, unsigned row, unsigned count) {
+        const char *p = row_of(tensor, pitch, row);
         if constexpr (kVectors) {
 #pragma unroll
             for (int j = 0; j < kVecs; ++j)
@@ -451,20 +463,24 @@ residual_norm_kernel(const ResidualNormArgs a)
                     copy_async(dst + (at.first + At::at(j, 0)) * kBytes, p + (at.first + At::at(j, 0)) * kBytes);
         } else {
             const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
-            const int pieces = (off + a.width * kBytes + 15) / 16;
-            for (int i = one_warp ? lane : threadIdx.x; i < pieces; i += 32 * a.warps)
+            const Pieces s = pieces_of(off, a.width, kBytes, row * pitch * kBytes, (count - 1 - row) * pitch * kBytes);
+            const int t = one_warp ? lane : threadIdx.x;
+            for (int i = s.first + t; i < s.end; i += 32 * a.warps)
                 copy_async(dst + 16 * i, p - off + 16 * i);
+            const int e = t < s.head ? t : s.tail + t - s.head;
+            if (e < a.width)
+                copy_number<kBytes>(dst + off + e * kBytes, p + e * kBytes);
         }
     };
     unsigned fill_row = row0 + mine;
     uint32_t fill = slot0;
     auto refill = [&] {
         if (fill_row < rows) {
-            copy(fill, row_of(a.x, a.x_row, fill_row));
+            copy(fill, a.x, a.x_row, fill_row, all_rows);
             if (a.branch)
-                copy(fill + tensor_bytes, row_of(a.branch, a.branch_row, fill_row));
+                copy(fill + tensor_bytes, a.branch, a.branch_row, fill_row, all_rows);
             if (gate_rows)
-                copy(fill + 2 * tensor_bytes, gate_of(fill_row, seq));
+                copy(fill + 2 * tensor_bytes, a.gate, a.gate_row, gate_row(fill_row, seq), a.cu ? a.n_seqs : all_rows);
         }
         copy_commit();      // one group a slot, if an empty one
         fill_row += stride;
@@ -521,7 +537,7 @@ residual_norm_kernel(const ResidualNormArgs a)
                     v[j][e] = fmul2(v[j][e], w[e]);
             };
             if (gate_rows) {
-                take(2, kVectors ? nullptr : gate_of(on ? row : 0, read_seq), times);
+                take(2, kVectors ? nullptr : row_of(a.gate, a.gate_row, gate_row(on ? row : 0, read_seq)), times);
             } else if (a.gate) {
                 uint64_t w[kPairs];
 #pragma unroll

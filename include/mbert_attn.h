@@ -456,7 +456,9 @@ enum {
  * All in fp32, h and y rounded once; y is of the h that has not been rounded.  Rows whose squares
  * fp32 does not hold are scaled by a power of two first, so any rows of normal numbers do; a row
  * without spread (all zeros, for LayerNorm all equal) is 0/0 with eps = 0.  Any alignment of the element
- * size; rows of whole, 16-byte aligned vectors are read in these.  One kernel. */
+ * size; rows of whole, 16-byte aligned vectors are read in these.  Of other rows the bytes beside them,
+ * within 16-byte boundaries, may be read too, but never those before a tensor's first number or behind
+ * its last one; what they hold does not count.  One kernel. */
 typedef struct {
     const void *x, *branch, *gate;
     const void *weight, *bias, *branch_weight, *branch_bias;
