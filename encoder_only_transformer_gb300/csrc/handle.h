@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <mutex>
 #include <vector>
 
@@ -56,7 +57,7 @@ struct mbert_attn {
     // start, end, start, end, ... per profile slot (global, local, projection)
     std::vector<cudaEvent_t> ev[MBERT_PROFILE_SLOTS];
     size_t ev_used[MBERT_PROFILE_SLOTS] = {};
-    int64_t launches = 0;                   // every kernel this handle enqueued
+    std::atomic<int64_t> launches{0};       // every kernel this handle enqueued (calls of several threads count)
     // recently encoded tensor maps, by (address, width, rows): encoding one
     // costs microseconds of host time, as much as a short kernel
     struct MapEntry {

@@ -865,8 +865,8 @@ MBERT_API int mbert_attn_profile_read(mbert_attn *h, double *kernel_ms, int64_t 
             kernel_launches[k] = static_cast<int64_t>(h->ev_used[k] / 2);
         h->ev_used[k] = 0;
     }
+    const int64_t launches = h->launches.exchange(0);
     if (total_launches)
-        *total_launches = h->launches;
-    h->launches = 0;
+        *total_launches = launches;
     return MBERT_OK;
 }

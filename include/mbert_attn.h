@@ -34,7 +34,9 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  All device work is enqueued asynchronously on it; the caller
  *    keeps ownership of the stream and of every buffer it passes.
- *  - A handle may be used from one host thread at a time.
+ *  - A handle may be used from one host thread at a time.  Only
+ *    mbert_attn_linear and mbert_attn_residual_norm may be called on it by any
+ *    number of threads at once, and beside one thread's other calls.
  */
 #ifndef MBERT_ATTN_H
 #define MBERT_ATTN_H
@@ -380,9 +382,10 @@ int mbert_attn_cross(mbert_attn *h, const mbert_attn_cross_args *args, void *wor
 /* ------------------------------------------------------------------------
  * Layers of any width: matrix products with their epilogue, plain and grouped by
  * expert, and the norms around a block.  For encoders of other sizes, a model's
- * heads, decoders beside the cross attention, and mixtures of experts.  These too
- * keep nothing in the handle but the error word, so calls on different streams may
- * overlap on the GPU.
+ * heads, decoders beside the cross attention, and mixtures of experts.  Nothing of a
+ * call's data stays in the handle but the error word, so calls on different streams may
+ * overlap on the GPU; on the host it keeps how calls of the same sizes run (the plans of
+ * 64 of them, under a lock) and the count of launches.
  * ------------------------------------------------------------------------ */
 
 /* Activations, of z in fp32. */
