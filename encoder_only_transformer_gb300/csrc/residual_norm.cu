@@ -211,7 +211,7 @@ struct Team {
     int turn;
 
     template <typename Op>
-    __device__ float all(float v, float none, Op op)
+    __device__ float all(float v, Op op)
     {
         if (lanes == 32) {
 #pragma unroll
@@ -221,27 +221,50 @@ struct Team {
             for (int o = lanes >> 1; o > 0; o >>= 1)
                 v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
         }
-        if (warps > 1) {
-            // two places in turn, so that one barrier a sum will do
-            float *s = scratch + (turn ^= 1) * 32;
-            const int lane = threadIdx.x & 31;
-            if (lane == 0)
-                s[threadIdx.x >> 5] = v;
-            __syncthreads();
-            v = lane < warps ? s[lane] : none;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-        }
-        return v;
+        return warps > 1 ? join(v, 32, op) : v;
     }
-    __device__ float sum(uint64_t v)
+    static __device__ float add(uint64_t v)
     {
         float lo, hi;
         f2_split(v, lo, hi);
-        return all(lo + hi, 0.f, [](float x, float y) { return x + y; });
+        return lo + hi;
     }
-    __device__ float most(float v) { return all(v, 0.f, [](float x, float y) { return fmaxf(x, y); }); }
+    __device__ float sum(uint64_t v)
+    {
+        return all(add(v), [](float x, float y) { return x + y; });
+    }
+    // sums u of each warp's first half of numbers, v of the second, added up like those of
+    // twice as many warps
+    __device__ float sum(uint64_t u, uint64_t v)
+    {
+        const bool upper = threadIdx.x & 16;
+        const float a = add(u), b = add(v);
+        // lanes 0 - 15 go on with u, the others with v
+        float x = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+        return join(x, 16, [](float y, float z) { return y + z; });
+    }
+    __device__ float most(float v) { return all(v, [](float x, float y) { return fmaxf(x, y); }); }
+
+private:
+    // v of every group of `width` lanes of the crew
+    template <typename Op>
+    __device__ float join(float v, int width, Op op)
+    {
+        // two places in turn, so that one barrier a sum will do
+        float *s = scratch + (turn ^= 1) * 32;
+        const int lane = threadIdx.x & 31;
+        if (lane % width == 0)
+            s[threadIdx.x / width] = v;
+        __syncthreads();
+        v = lane < 32 / width * warps ? s[lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    }
 };
 
 // v[] of a row -> its norm times w plus b.  Called by all lanes of a warp.
@@ -252,7 +275,7 @@ struct Team {
 // 2^-40, to less than 2^-90 (those that round to nothing are then off by 2^-45 of the
 // sum at most), are taken again of the row times a power of two that brings its
 // largest number to 1 .. 2, or as near as keeps eps times its square at 2^100.
-template <int kType, bool kVectors, int kVecs, bool kLayer>
+template <int kType, bool kVectors, int kVecs, bool kLayer, bool kHalves>
 __device__ __forceinline__ void norm_row(const ResidualNormArgs &a, const Row<kType, kVectors, kVecs> &at,
                                          uint64_t (&v)[kVecs][Row<kType, kVectors, kVecs>::kPairs], const void *w,
                                          const void *b, Team &team)
@@ -265,15 +288,21 @@ __device__ __forceinline__ void norm_row(const ResidualNormArgs &a, const Row<kT
             for (int e = 0; e < kPairs; ++e)
                 f(v[j][e]);
     };
-    // two chains of sums
+    // two chains of sums, or two for each half of a lane's vectors (see launch)
     auto total = [&](auto &&f) {
-        uint64_t s[2] = {};
+        uint64_t s[2][2] = {};
 #pragma unroll
         for (int j = 0; j < kVecs; ++j)
 #pragma unroll
-            for (int e = 0; e < kPairs; ++e)
-                s[e & 1] = f(v[j][e], s[e & 1]);
-        return team.sum(fadd2p(s[0], s[1]));
+            for (int e = 0; e < kPairs; ++e) {
+                uint64_t &x = s[kHalves && j >= kVecs / 2][e & 1];
+                x = f(v[j][e], x);
+            }
+        const uint64_t u = fadd2p(s[0][0], s[0][1]);
+        if constexpr (kHalves)
+            return team.sum(u, fadd2p(s[1][0], s[1][1]));
+        else
+            return team.sum(u);
     };
     auto half_mean = [&] {
         const uint64_t scale = bc2(a.sum_scale);
@@ -399,7 +428,7 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int n, long long t
 }
 
 // kVecs 16-byte vectors a lane.
-template <int kType, bool kVectors, int kVecs, bool kLayer>
+template <int kType, bool kVectors, int kVecs, bool kLayer, bool kHalves>
 __global__ void __maxnreg__(most_registers(kVectors, kVecs * (kType == MBERT_F32 ? 4 : 8), kType == MBERT_F32 ? 4 : 2))
 residual_norm_kernel(const ResidualNormArgs a)
 {
@@ -530,7 +559,7 @@ residual_norm_kernel(const ResidualNormArgs a)
         if (a.branch) {
             take(1, row_of(a.branch, a.branch_row, row), keep);
             if (a.after_weight)
-                norm_row<kType, kVectors, kVecs, kLayer>(a, at, v, a.after_weight, a.after_bias, team);
+                norm_row<kType, kVectors, kVecs, kLayer, kHalves>(a, at, v, a.after_weight, a.after_bias, team);
             auto times = [&](int j, const uint64_t (&w)[kPairs]) {
 #pragma unroll
                 for (int e = 0; e < kPairs; ++e)
@@ -565,7 +594,7 @@ residual_norm_kernel(const ResidualNormArgs a)
         if (a.branch)
             store(a.h, a.h_row);
         if (a.weight) {
-            norm_row<kType, kVectors, kVecs, kLayer>(a, at, v, a.weight, a.bias, team);
+            norm_row<kType, kVectors, kVecs, kLayer, kHalves>(a, at, v, a.weight, a.bias, team);
             store(a.y, a.y_row);
         }
     }
@@ -583,12 +612,12 @@ constexpr int ring_bytes(int blocks)
 }
 static_assert(3 * (kResidualNormMaxWidth * 4 + 30) <= ring_bytes(1), "a slot");
 
-template <int kType, bool kVectors, int kVecs, bool kLayer>
+template <int kType, bool kVectors, int kVecs, bool kLayer, bool kHalves = false>
 cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
 {
     static PerDeviceOnce once;
     constexpr int kBytes = Row<kType, kVectors, kVecs>::kBytes;
-    auto *kernel = residual_norm_kernel<kType, kVectors, kVecs, kLayer>;
+    auto *kernel = residual_norm_kernel<kType, kVectors, kVecs, kLayer, kHalves>;
     // warps on one SM, by registers: each of its four parts has 16384 of them
     int fit = 0;
     const cudaError_t e = per_device_once(once, &fit, [&](int *out) {
@@ -637,9 +666,18 @@ cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
         a.lanes *= 2;
     const int most = kVectors ? kType == MBERT_F32 ? 8 : 6 : 32 / kN;
     const int few = (a.width + 64 * kCrewNumbers - 1) / (64 * kCrewNumbers);
+    const int small = (vecs + 32 * few - 1) / (32 * few);       // vectors of a lane of such a crew
+    const bool fewer = kVectors && kType != MBERT_F32 && vecs > 32 * most && few <= kMostWarps / 2 &&
+                       (a.rows > 2 * num_sms || small != 4);
     a.warps = vecs <= 32 * most ? 1
-              : kVectors && kType != MBERT_F32 && few <= kMostWarps / 2 && a.rows > 2 * num_sms ? few
+              : fewer ? few
               : std::min(kMostWarps, (a.width + 32 * kCrewNumbers - 1) / (32 * kCrewNumbers));
+    // A row's bits do not go by the number of rows: the halves of a lane's 4 vectors in the
+    // smaller crew are the warps of the other, with 2 a lane, and are summed like these.
+    // (Rows of 2056 to 2304 numbers, 3 vectors a lane, have the smaller crew always.)
+    if constexpr (kVectors && kType != MBERT_F32)
+        if (fewer && small == 4)
+            return launch<kType, kVectors, 4, kLayer, true>(a, num_sms, stream);
     const int each = (vecs + a.lanes * a.warps - 1) / (a.lanes * a.warps);
     if constexpr (kVectors || kN == 4) {
         if constexpr (kN == 4)

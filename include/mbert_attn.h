@@ -409,7 +409,8 @@ enum {
  *                overlaps nothing.  x 16-byte aligned with x_row a multiple of 8; out, residual
  *                and bias of any alignment (16-byte aligned rows are faster).
  *   weight       device [max(experts, 1)][outer or 2 outer][inner], rows weight_row and experts
- *                weight_expert elements apart, multiples of 8, 16-byte aligned.  ([out][in].)
+ *                weight_expert elements apart (at least a row's and an expert's extent), multiples
+ *                of 8, 16-byte aligned.  ([out][in].)
  *   bias         device [max(experts, 1)][outer or 2 outer], contiguous, or NULL.
  *   rows         0 <= rows < 2^31 - 1024 (0 enqueues nothing); inner, outer 1 .. 2^24.
  *   dtype        MBERT_BF16 or MBERT_F16, of all of these, else MBERT_ERR_UNSUPPORTED.
@@ -419,7 +420,8 @@ enum {
  *                mbert_attn_get_error(), and nothing is written.
  *   row_scale    device fp32 [rows], with experts only, or NULL for 1.
  * Products, sums and the epilogue in fp32, out rounded once.  One kernel, no workspace; results
- * do not depend on timing. */
+ * do not depend on timing, but the order of sums may go by all sizes of the call, rows and experts
+ * among them. */
 typedef struct {
     const void *x, *weight, *bias, *residual;
     void *out;
@@ -461,7 +463,8 @@ enum {
  * without spread (all zeros, for LayerNorm all equal) is 0/0 with eps = 0.  Any alignment of the element
  * size; rows of whole, 16-byte aligned vectors are read in these.  Of other rows the bytes beside them,
  * within 16-byte boundaries, may be read too, but never those before a tensor's first number or behind
- * its last one; what they hold does not count.  One kernel. */
+ * its last one; what they hold does not count.  One kernel; the order of a row's sums goes by its width,
+ * type and alignment alone, so its results do not depend on the other rows or on how many there are. */
 typedef struct {
     const void *x, *branch, *gate;
     const void *weight, *bias, *branch_weight, *branch_bias;
