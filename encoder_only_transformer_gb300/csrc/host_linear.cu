@@ -146,13 +146,12 @@ Cost rows_cost(const mbert_attn *h, const mbert_attn_linear_args &c, int tile)
     const double epilogue = (plain(c) ? 1300.0 : 2300.0) * (gated ? 1.3 : 1.0) * ceil_div(tile, 32);
     // every row tile reads its group's weights, from memory or from L2, at 2850 a clock
     const double traffic = static_cast<double>(tiles) * c.outer * sides * c.inner * 2 / 2850;
-    auto consider = [&](int m, int split, bool whole) {
-        const int64_t pieces = ceil_div(granules, m), ctas = split > 1 ? bound * pieces : std::min(places, bound * (whole ? pieces : granules));
+    auto consider = [&](int m, int split) {
+        const int64_t pieces = ceil_div(granules, m), ctas = split > 1 ? bound * pieces : std::min(places, bound * pieces);
         // clusters fit where their SMs lie together, which leaves some idle
         if (split > 1 && (10 * ctas * split > 8 * places || linear_rows_stages(tile, gated, m, split) < 3))
             return;
-        // pieces of a CTA (a run of granules may begin and end within a row tile)
-        const int64_t runs = split > 1 ? 1 : whole ? ceil_div(tiles * pieces, ctas) : ceil_div(ceil_div(tiles * granules, ctas), m) + 1;
+        const int64_t runs = split > 1 ? 1 : ceil_div(tiles * pieces, ctas);     // pieces of a CTA
         const int64_t share = std::max<int64_t>(1, ceil_div(std::min(ctas, tiles * pieces) * split, h->num_sms));
         const double step = std::max(330.0, share * std::max(mma, (tile * 128 + sides * m * 4096) / 60.0));
         const double work = runs * std::max(ceil_div(steps, split) * step, epilogue) + epilogue;
@@ -161,15 +160,13 @@ Cost rows_cost(const mbert_attn *h, const mbert_attn_linear_args &c, int tile)
         if (clocks < best.clocks) {
             best.clocks = clocks;
             best.plan.few = true;
-            best.plan.rows = {tile, m, split, whole, ctas};
+            best.plan.rows = {tile, m, split, ctas};
             best.plan.units = bound * granules;
         }
     };
     for (int m = 1; m <= kLinearGranules; ++m)
         for (int split = 1; split <= 8 && split <= steps; split *= 2)
-            consider(m, split, true);
-    if (bound * granules >= 2 * kLinearGranules * places)
-        consider(kLinearGranules, 1, false);
+            consider(m, split);
     return best;
 }
 
@@ -286,10 +283,7 @@ MBERT_API int mbert_attn_linear(mbert_attn *h, const mbert_attn_linear_args *arg
     const int xbox = p.few ? p.rows.tile : kLinearRows / 2, wbox = p.few ? kLinearGranule * p.rows.granules : p.columns / 2;
     if (encode_rows(h, &a.tm_x, c.x, c.inner, c.rows, pitch(c.rows, c.x_row, c.inner), xbox, 256) != MBERT_OK ||
         encode_groups(h, &a.tm_w, c.weight, c.inner, width, groups, wrow, groups > 1 ? c.weight_expert : width * wrow,
-                      wbox) != MBERT_OK ||
-        (p.few && p.rows.granules > 1 &&
-         encode_groups(h, &a.tm_granule, c.weight, c.inner, width, groups, wrow,
-                       groups > 1 ? c.weight_expert : width * wrow, kLinearGranule) != MBERT_OK))
+                      wbox) != MBERT_OK)
         return MBERT_ERR_CUDA;
     a.out_vectors = out.aligned(16);
     a.out_bytes = out.aligned(8) ? 8 : out.aligned(4) ? 4 : 2;

@@ -14,7 +14,6 @@ namespace mbert {
 struct LinearArgs {
     CUtensorMap tm_x;                   // [rows][inner], box 64 columns
     CUtensorMap tm_w;                   // [groups][width][inner], box 64 columns, one group
-    CUtensorMap tm_granule;             // the same, box of a granule's rows (linear_rows.cu, pieces of several)
     CUtensorMap tm_out, tm_residual;    // [rows][outer], box linear_chunk columns x 32 rows (linear.cu, where
                                         // out_vectors / residual_vectors say that the rows allow it)
     const void *bias = nullptr;         // [groups][width]
@@ -29,7 +28,6 @@ struct LinearArgs {
     int activation = 0;                 // MBERT_ACT_*
     // linear_rows.cu: granules of a piece, stages of its ring, bytes of one
     int granules = 0, stages = 0, stage_bytes = 0;
-    int whole_pieces = 0;               // dealt out to the CTAs, not granules
     int out_vectors = 0, residual_vectors = 0;
     int out_bytes = 2, residual_bytes = 2;      // else: bytes of a word, 2, 4 or 8
     int32_t *err = nullptr;
@@ -44,13 +42,12 @@ cudaError_t launch_linear(const LinearArgs &a, int columns, bool gated, bool hal
 
 // The kernel for few rows: `tile` rows (16, 32, 64 or 128) x up to `granules` times 32
 // output columns a piece, the inner dimension shared by `split` CTAs of a cluster.
-// The granules of all row tiles, or whole pieces, are dealt out evenly to `ctas` CTAs;
-// with a split every piece has a cluster of its own, `ctas` of them.
+// The pieces of all row tiles are dealt out evenly to `ctas` CTAs; with a split every
+// piece has a cluster of its own, `ctas` of them.
 constexpr int kLinearGranule = 32;
 constexpr int kLinearGranules = 4;      // at most
 struct LinearRowsPlan {
     int tile, granules, split;
-    bool whole;
     long long ctas;
 };
 // CTAs on one SM, the shared memory of one

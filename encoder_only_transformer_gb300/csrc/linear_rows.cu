@@ -5,13 +5,13 @@
 // So the operands change places: D^T = W x^T with 128 weight rows as M and 16 to 128
 // rows of x as N, which wastes little of an MMA on rows that are not there, and the
 // bytes of W are spread evenly over the SMs:
-//  * output columns go by granules of 32.  All granules, row tile after row tile and
-//    group after group, are dealt out to the CTAs (one or two an SM) in even runs, which
-//    a CTA takes in pieces of up to 4 granules (or, where a CTA has few, whole pieces are
-//    dealt out): a whole piece comes as one box, a shorter one as a box a granule.  An MMA
-//    of fewer than 4 leaves the rest of its 128 rows to whatever shared memory holds
-//    behind them, and nobody reads those.  (24 rows, 768 -> 50368 bf16: 16.2 us, 4.9 TB/s;
-//    units of 128 columns in turn 18.4.)
+//  * output columns go by granules of 32, in pieces of 1 to 4 granules, as many as
+//    leave the CTAs (one or two an SM) the least to do.  All pieces, row tile after row tile
+//    and group after group, are dealt out in even runs.  An MMA of fewer than 4 granules
+//    leaves the rest of its 128 rows to whatever shared memory holds behind them, and
+//    nobody reads those.  (24 rows, 768 -> 50368 bf16, 525 pieces of 3 granules on 304 CTAs:
+//    16.0 us, 4.9 TB/s; pieces of 4 in turn 18.4; even runs of granules, cut into pieces by
+//    each CTA, 17.1, and 25.8 against 23.1 for -> 80000.)
 //  * where there are too few columns to fill the SMs, the inner dimension is cut among 2,
 //    4 or 8 CTAs of a cluster.  Each writes its sums into the others' shared memory, rows
 //    of x dealt out among them, and each adds up its rows' parts in the order of the
@@ -115,10 +115,10 @@ struct Ring {
 class PieceWalk {
 public:
     __device__ PieceWalk(const LinearArgs &a, int block, int split)
-        : all_((a.outer + kLinearGranule - 1) / kLinearGranule), most_(a.granules), whole_(a.whole_pieces),
-          walk_(a, block, whole_ ? (all_ + most_ - 1) / most_ : all_, 1)
+        : all_((a.outer + kLinearGranule - 1) / kLinearGranule), most_(a.granules),
+          walk_(a, block, (all_ + most_ - 1) / most_, 1)
     {
-        const long long units = count_units(a, block, whole_ ? (all_ + most_ - 1) / most_ : all_);
+        const long long units = count_units(a, block, (all_ + most_ - 1) / most_);
         const unsigned b = blockIdx.x / split, n = gridDim.x / split;
         valid_ = units >= 0;
         at_ = valid_ ? static_cast<int>(units * b / n) : 0;
@@ -129,15 +129,9 @@ public:
     {
         if (at_ >= end_ || !walk_.find(at_, u))
             return false;
-        if (whole_) {
-            at = u.column * most_;
-            n = min(most_, all_ - at);
-            ++at_;
-        } else {
-            at = u.column;
-            n = min(min(most_, all_ - at), end_ - at_);
-            at_ += n;
-        }
+        at = u.column * most_;
+        n = min(most_, all_ - at);
+        ++at_;
         return true;
     }
 
@@ -145,7 +139,6 @@ public:
 
 private:
     int all_, most_;
-    bool whole_;
     UnitWalk walk_;
     bool valid_;
     int at_, end_;
@@ -253,18 +246,12 @@ linear_rows_kernel(const __grid_constant__ LinearArgs a)
                 const bool go = mbar_wait_mark(bar(L::kEmpty + r.slot), r.parity, err, gave_up);
                 const uint32_t dst = ring + r.slot * a.stage_bytes, full = bar(L::kFull + r.slot);
                 if (elect_one_sync() && go) {
-                    mbar_arrive_expect_tx(full, L::kXBytes + L::kSides * n * kGranuleBytes);
+                    // (a row tile's last piece may have fewer granules: nobody reads the rest)
+                    mbar_arrive_expect_tx(full, a.stage_bytes);
 #pragma unroll
-                    for (int s = 0; s < L::kSides; ++s) {
-                        const uint32_t to = dst + L::kXBytes + s * a.granules * kGranuleBytes;
-                        const int row = s * a.outer + at * kLinearGranule;
-                        if (n == a.granules)
-                            tma_load_3d(to, &a.tm_w, k * kBK, row, u.group, full);
-                        else
-                            for (int i = 0; i < n; ++i)
-                                tma_load_3d(to + i * kGranuleBytes, &a.tm_granule, k * kBK, row + i * kLinearGranule,
-                                            u.group, full);
-                    }
+                    for (int s = 0; s < L::kSides; ++s)
+                        tma_load_3d(dst + L::kXBytes + s * a.granules * kGranuleBytes, &a.tm_w, k * kBK,
+                                    s * a.outer + at * kLinearGranule, u.group, full);
                     tma_load_2d(dst, &a.tm_x, k * kBK, static_cast<int>(u.row), full);
                 }
                 __syncwarp();
@@ -442,7 +429,6 @@ cudaError_t launch(LinearArgs a, const LinearRowsPlan &p, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     a.granules = p.granules;
-    a.whole_pieces = p.whole;
     a.stages = L::stages(p.granules, p.split);
     a.stage_bytes = static_cast<int>(L::stage_bytes(p.granules));
     cudaLaunchAttribute attr[2];
