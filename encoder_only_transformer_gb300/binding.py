@@ -99,6 +99,7 @@ SIGNATURES = {
     "mbert_attn_cross_workspace": (_c_int, [_vp, ctypes.POINTER(CrossArgs), ctypes.POINTER(_c_i64)]),
     "mbert_attn_cross": (_c_int, [_vp, ctypes.POINTER(CrossArgs), _vp, _c_i64, _vp]),
     "mbert_attn_linear": (_c_int, [_vp, ctypes.POINTER(LinearArgs), _vp]),
+    "mbert_attn_linear_plan": (_c_int, [_vp, ctypes.POINTER(LinearArgs), ctypes.POINTER(ctypes.c_int32)]),
     "mbert_attn_residual_norm": (_c_int, [_vp, ctypes.POINTER(ResidualNormArgs), _vp]),
     "mbert_attn_get_error": (_c_int, [_vp]),
     "mbert_attn_selftest_timeout": (_c_int, [_vp, _c_i64, _vp]),
@@ -779,6 +780,18 @@ class Attention:
         if known is None:
             known = self._linear_known(key, x, weight, None, bias, activation, bool(gated), residual, None, out)
         return self._linear(known, "linear", x, weight, bias, residual, out)
+
+    def linear_plan(self, rows: int, inner: int, outer: int, activation: str = "none", gated: bool = False,
+                    experts: int = 0):
+        """How a product of these sizes runs (experts: of that many groups), for profiles
+        and tests: ("many", columns) for the kernel for many rows, in units of 256 rows
+        and that many accumulator columns, or ("few", rows of a tile, pieces of that many
+        times 32 output columns, CTAs that share the inner dimension)."""
+        args = LinearArgs(rows=rows, inner=inner, outer=outer, activation=_ACTIVATIONS[activation],
+                          gated=1 if gated else 0, experts=experts)
+        plan = (ctypes.c_int32 * 4)()
+        _check(load_library().mbert_attn_linear_plan(self._h, ctypes.byref(args), plan), "linear_plan")
+        return ("few", *plan[1:]) if plan[0] else ("many", plan[1])
 
     def expert_linear(self, x: torch.Tensor, weight: torch.Tensor, cu_experts: torch.Tensor,
                       bias: torch.Tensor = None, activation: str = "none", gated: bool = False,

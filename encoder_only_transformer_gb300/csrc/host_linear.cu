@@ -233,7 +233,26 @@ LinearPlan linear_plan(mbert_attn *h, const mbert_attn_linear_args &c)
     return e.plan;
 }
 
+bool sizes_ok(const mbert_attn_linear_args &c)
+{
+    return c.rows >= 0 && c.rows <= kMaxRows && c.inner >= 1 && c.inner <= kMaxWidth && c.outer >= 1 && c.outer <= kMaxWidth &&
+           c.activation >= MBERT_ACT_NONE && c.activation <= MBERT_ACT_RELU && (c.gated == 0 || c.gated == 1) &&
+           c.experts >= 0 && c.experts <= 65536;
+}
+
 }  // namespace
+
+MBERT_API int mbert_attn_linear_plan(mbert_attn *h, const mbert_attn_linear_args *args, int32_t plan[4])
+{
+    if (!h || !args || !plan || !sizes_ok(*args) || args->rows == 0)
+        return MBERT_ERR_BAD_ARG;
+    const LinearPlan p = linear_plan(h, *args);
+    plan[0] = p.few;
+    plan[1] = p.few ? p.rows.tile : p.columns;
+    plan[2] = p.few ? p.rows.granules : 0;
+    plan[3] = p.few ? p.rows.split : 0;
+    return MBERT_OK;
+}
 
 MBERT_API int mbert_attn_linear(mbert_attn *h, const mbert_attn_linear_args *args, void *stream)
 {
@@ -242,9 +261,7 @@ MBERT_API int mbert_attn_linear(mbert_attn *h, const mbert_attn_linear_args *arg
     const mbert_attn_linear_args &c = *args;
     if (c.dtype != MBERT_BF16 && c.dtype != MBERT_F16)
         return MBERT_ERR_UNSUPPORTED;
-    if (c.rows < 0 || c.rows > kMaxRows || c.inner < 1 || c.inner > kMaxWidth || c.outer < 1 || c.outer > kMaxWidth ||
-        c.activation < MBERT_ACT_NONE || c.activation > MBERT_ACT_RELU || (c.gated != 0 && c.gated != 1) ||
-        c.experts < 0 || c.experts > 65536)
+    if (!sizes_ok(c))
         return MBERT_ERR_BAD_ARG;
     // the router's weights go with experts, a residual with the plain product
     if (c.experts > 0 ? c.residual != nullptr : c.cu_experts || c.row_scale)

@@ -435,6 +435,15 @@ typedef struct {
 
 int mbert_attn_linear(mbert_attn *h, const mbert_attn_linear_args *args, void *stream);
 
+/* How mbert_attn_linear runs a call of these sizes, type aside (pointers and strides are not
+ * looked at; host only), for profiles and tests:
+ *   plan[0]   0: the kernel for many rows, units of 256 rows x plan[1] columns (of both halves
+ *             together where gated);
+ *             1: that for few rows, tiles of plan[1] rows x pieces of plan[2] times 32 output
+ *             columns, the inner dimension shared by plan[3] CTAs.
+ * Its choice goes by rows, experts, inner, outer, activation, gated and the device's SMs. */
+int mbert_attn_linear_plan(mbert_attn *h, const mbert_attn_linear_args *args, int32_t plan[4]);
+
 /* Whose gate a row takes. */
 enum {
     MBERT_GATE_NONE = 0,
