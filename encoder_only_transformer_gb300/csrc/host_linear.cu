@@ -348,7 +348,7 @@ MBERT_API int mbert_attn_residual_norm(mbert_attn *h, const mbert_attn_residual_
         (!c.branch && (c.branch_weight || c.gate || c.h || c.residual_scale != 1.f || !c.weight)) ||
         c.gate_kind < MBERT_GATE_NONE || c.gate_kind > MBERT_GATE_SEQUENCES ||
         (c.gate != nullptr) != (c.gate_kind != MBERT_GATE_NONE) ||
-        (c.cu_seqlens != nullptr) != (c.gate_kind == MBERT_GATE_SEQUENCES) || (c.cu_seqlens && c.n_seqs < 1) ||
+        (c.cu_seqlens != nullptr) != (c.gate_kind == MBERT_GATE_SEQUENCES) || (c.cu_seqlens && (c.n_seqs < 1 || c.n_seqs > kMaxRows)) ||
         reinterpret_cast<uintptr_t>(c.cu_seqlens) % 4)
         return MBERT_ERR_BAD_ARG;
     if (c.rows == 0)

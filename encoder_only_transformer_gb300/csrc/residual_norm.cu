@@ -421,7 +421,7 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int n, long long t
         return seq;
     int hi = n;
     while (hi - seq > 1) {
-        const int mid = (seq + hi) >> 1;
+        const int mid = seq + ((hi - seq) >> 1);
         (cu[mid] <= t ? seq : hi) = mid;
     }
     return seq;

@@ -463,8 +463,8 @@ enum {
  *                nothing.
  *   width        1 .. 16384; rows as in mbert_attn_linear; dtype MBERT_BF16, _F16 or _F32, of all.
  *   gate         rows of width, gate_row elements apart, as gate_kind says.
- *   cu_seqlens   with MBERT_GATE_SEQUENCES: device int32 [n_seqs + 1], cu[0] = 0, non-decreasing,
- *                cu[n] <= rows; rows of h and y from cu[n] on are left as they were.  A bad list
+ *   cu_seqlens   with MBERT_GATE_SEQUENCES: device int32 [n_seqs + 1] (n_seqs as rows), cu[0] = 0,
+ *                non-decreasing, cu[n] <= rows; rows of h and y from cu[n] on are left as they were.  A bad list
  *                sets MBERT_ERR_BAD_CU_SEQLENS, and nothing is written.
  *   eps          0 <= eps <= 1.
  * All in fp32, h and y rounded once; y is of the h that has not been rounded.  Rows whose squares

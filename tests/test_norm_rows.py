@@ -1,5 +1,7 @@
 """A row of the norms around a block has the same bits whatever rows are beside it and
 however many: crews of every size sum in one order."""
+import ctypes
+
 import pytest
 import torch
 
@@ -26,4 +28,21 @@ def test_bits_of_a_row_do_not_go_by_the_rows_beside_it(built, D, kind, dtype):  
     one = slice(777, 778)
     hp, yp = call(one)
     assert torch.equal(h[one], hp) and torch.equal(y[one], yp)
+    err0()
+
+
+def test_number_of_sequences_is_bounded(built):  # noqa: F811
+    """As many sequences as rows may be there at most; more (indexes beyond 32 bits on the
+    device) are refused on the host."""
+    x, gate = rnd(4, 64, seed=1).cuda(), rnd(4, 64, seed=2).cuda()
+    cu, out = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32).cuda(), torch.zeros_like(x)
+    lib, h = binding.load_library(), binding._default(x.device).handle
+    a = binding.ResidualNormArgs(x=x.data_ptr(), branch=x.data_ptr(), gate=gate.data_ptr(), h=out.data_ptr(), x_row=64,
+                                 branch_row=64, gate_row=64, h_row=64, rows=4, width=64, norm=1, gate_kind=3,
+                                 cu_seqlens=cu.data_ptr(), n_seqs=4, residual_scale=1.0, eps=1e-5)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.mbert_attn_residual_norm(h, ctypes.byref(a), stream) == 0
+    for n in (2 ** 31 - 1, 2 ** 31 - 1024, 0, -1):
+        a.n_seqs = n
+        assert lib.mbert_attn_residual_norm(h, ctypes.byref(a), stream) == -1, n
     err0()
