@@ -801,7 +801,8 @@ class Attention:
         [E, N, K] and bias [E, N] ([E, 2N, K] and [E, 2N] gated), and row t's
         result is multiplied by row_scale[t] (fp32, a router's weight).  Empty
         groups are allowed; rows of out behind the last group are left as they
-        were."""
+        were.  Experts' weights lie one behind another (padding between them is
+        fine, rows of several interleaved are refused)."""
         key = ("expert_linear", activation, bool(gated), _key(x), _key(weight), _key(cu_experts), _key(bias),
                _key(row_scale), _key(out))
         known = self._known.get(key)
@@ -826,7 +827,8 @@ class Attention:
         [D], [T, D], or with cu_seqlens (int32 [n+1]) [n, D], of the row's
         sequence; rows behind the last sequence are left as they were.  branch
         None: (x, N(x)).  h_out and y_out may each be x or branch.  y is of the
-        h that has not been rounded.  Rows may be strided."""
+        h that has not been rounded.  Rows may be strided.  A row's bits do not go
+        by the rows beside it or by how many there are."""
         if norm not in _NORMS:
             raise ValueError(f"norm must be 'rms' or 'layer', not {norm!r}")
         residual_scale, eps = float(residual_scale), float(eps)

@@ -106,8 +106,10 @@ int64_t block_bound(const mbert_attn_linear_args &c, int rows)
 
 // What a product takes, in clocks of an SM: estimates from measured calls (a few rows to
 // 2048 by 768 to 8192, 8 to 64 experts), good for the choice between kernels and
-// tiles and no more: over 102 sizes the chosen one took 4 % longer than the best of
-// all.  (Kernel for few rows against that for many, us: 128 x 4096 -> 512 9.2 / 19.0, 300 x
+// tiles and no more: over the first 120 products that perf/more_operators.py draws from
+// random.Random(2026) the chosen form took 6 % longer than the best of both widths of unit
+// and four tiles in the geometric mean, 1.56 times as long at worst (88 x 1128 -> 32, 10.9 us
+// against 7), and as much for even groups as for ragged ones.  (Kernel for few rows against that for many, us: 128 x 4096 -> 512 9.2 / 19.0, 300 x
 // 768 -> 2304 8.9 / 9.7, 1024 x 1024 -> 8192 26.8 / 20.5; 500 rows of 16 experts, 768 -> 2304,
 // 15.8 / 26.3, 2000 rows of 16, 1024 -> 8192, 65 / 70; tiles of 64 against 128 rows, 500 rows of
 // 16 experts, 4096 -> 2 x 512, 48 / 32.)

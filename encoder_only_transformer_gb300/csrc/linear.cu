@@ -22,8 +22,9 @@
 //               leave no registers for 16
 // Each epilogue warp has two staging buffers of 32 rows x a chunk of its own and its own TMA
 // stores from them (clipped at the last row and column by the tensor map), so no warp
-// waits for another's rows; a residual comes into the buffer by TMA two chunks ahead and
-// is overwritten by the result, so `out` may be the residual.
+// waits for another's rows; a residual comes into the buffer by TMA, the first two chunks'
+// at the start and then each as the chunk before it is begun, and is overwritten by the
+// result, so `out` may be the residual.
 // A warp's bias numbers, 64 at most, come in a register or two while the unit's products run
 // and go round by shuffles; read where they are added, as vectors, their latency shows: 62
 // experts of about 127 rows, 80 -> 2 x 6720 with GELU, 187 us against 247.
@@ -36,11 +37,12 @@
 // about 8 x 10 blocks, whose rows and weights stay in L2.
 // Units of 256 x 128 accumulators serve calls with too few units for every pair.
 //
-// 32768 x 1024 -> 2 x 4096 bf16, GELU and gate: 277 us, 1.98 PFLOP/s (1.66 under
-// the power cap, where the same calls follow each other for seconds); without a gate the
+// 32768 x 1024 -> 2 x 4096 bf16, GELU and gate: 277 to 289 us by board, 1.9 to 1.98
+// PFLOP/s (1.62 to 1.66 under the power cap, where the same calls follow each other for
+// seconds); without a gate the
 // epilogue, 5000 clocks of a unit and 3700 more for GELU, shows: 325 us with it, 290
-// without.  65536 rows of 8 experts, 768 -> 2 x 1152: 133 us; 1152 -> 768: 74 us, 780 units
-// on 76 pairs in 11 rounds.
+// without.  65536 rows of 8 experts, 768 -> 2 x 1152: 133 to 139 us by board; 1152 -> 768: 74 us,
+// 780 units on 76 pairs in 11 rounds.
 // Not kept (before the bias came ahead, when these calls took 140 and 331 us): the
 // accumulators through fp32 tiles, 8 columns of a row a thread, plain stores: 150 and 351;
 // 8 warps without a gate 339; an arrival at the leader's barrier with a release at the

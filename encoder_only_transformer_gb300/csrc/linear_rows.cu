@@ -1,5 +1,6 @@
 // Products of any width for few rows (sm_103a): the same as linear.cu, whose head
-// has the formulas, for calls and groups of up to about a hundred rows.
+// has the formulas, for calls and groups of few rows: up to 2048 in the mean, where it is
+// estimated to be the faster (host_linear.cu).
 //
 // Bound by the weights, which are read once: 2 N K bytes against 2 T N K operations.
 // So the operands change places: D^T = W x^T with 128 weight rows as M and 16 to 128
@@ -23,8 +24,8 @@
 // issuer, warps 2 - 9 epilogue, one output column per thread and 16 rows at a time, which
 // a warp writes as whole vectors through a tile of its own in shared memory (four warps
 // that wrote number by number took 10 us for 128 rows).  Two accumulators in turn.
-// 4001 rows of 64 experts, 768 -> 2 x 1152 fp16 with SiLU and biases: 44 us (242 MB, 5.5
-// TB/s) against 63 with those four warps and 68 by linear.cu.
+// 4001 rows of 64 experts, 768 -> 2 x 1152 fp16 with SiLU and biases: 44 to 45 us (242 MB,
+// 5.4 TB/s) against 63 with those four warps and 68 by linear.cu.
 // What bounds short calls: a warp needs 330 clocks from one step to the next, whatever
 // it loads or multiplies (half of the MMAs, or one load for two, change nothing, nor do
 // more warps that load), and a call 5 us beside its steps.

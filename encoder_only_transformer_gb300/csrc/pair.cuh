@@ -1,6 +1,6 @@
-// The pair forms of common.cuh's tcgen05 and TMA wrappers, for linear.cu (projections.cu,
-// of fixed widths, holds its own): two CTAs of a cluster
-// on two SMs issue one MMA (cta_group::2).
+// The pair forms of common.cuh's tcgen05 and TMA wrappers, for linear.cu: two CTAs of a
+// cluster on two SMs issue one MMA (cta_group::2).  (projections.cu, of fixed widths, holds
+// its own, whose arrival on another CTA's barrier releases at the cluster's scope.)
 #pragma once
 
 #include "common.cuh"

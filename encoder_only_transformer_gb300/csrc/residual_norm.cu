@@ -636,8 +636,8 @@ cudaError_t launch(ResidualNormArgs &a, int num_sms, cudaStream_t stream)
     a.row_bytes = kVectors ? a.width * kBytes : (a.width * kBytes + 30) / 16 * 16;
     a.tensors = a.gate && !a.gate_channels ? 3 : a.branch ? 2 : 1;
     // two slots or more: the SM's blocks share the memory, fewer blocks where that does
-    // not do, and one slot where it does not do for a single block (rows of 48 KB or
-    // more from three tensors in fp32)
+    // not do, and one slot where it does not do for a single block (rows of more than
+    // 36 KB from three tensors, 55 KB from two)
     const int slot = crews * beside * a.row_bytes * a.tensors;
     int per_sm = std::max(1, std::min(fit / (threads / 32), 2048 / threads));
     while (per_sm > 1 && ring_bytes(per_sm) < per_sm * 2 * slot)
